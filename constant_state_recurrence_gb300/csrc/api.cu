@@ -47,6 +47,54 @@ int check_params(const float* gamma, const float* omega, const float* phi) {
   return SANATAN_OK;
 }
 
+int check_scan(int dtype, int gate, int B, int T, int D) {
+  if (!ok_dtype(dtype)) return SANATAN_ERR_INVALID;
+  if (gate != SANATAN_GATE_LOG && gate != SANATAN_GATE_SIGMOID) return SANATAN_ERR_INVALID;
+  if (B < 0 || T < 0 || D < 0) return SANATAN_ERR_INVALID;
+  // Elements index with 64-bit arithmetic; thread blocks must fit a grid.
+  if (static_cast<int64_t>(B) * D > (1LL << 31) - 1) return SANATAN_ERR_UNSUPPORTED;
+  return SANATAN_OK;
+}
+
+// Argument checks and launch of the state cache's two directions.
+int state_cache(float* state, float* exact, int layers, int B, int64_t inner, int64_t exact_inner,
+                const int64_t* pages, int64_t num_pages, int fmt, void* codes, float* scales,
+                float* exact_cache, bool write, void* stream) {
+  if (fmt != SANATAN_CACHE_INT8 && fmt != SANATAN_CACHE_E4M3) return SANATAN_ERR_INVALID;
+  if (layers < 0 || B < 0 || inner < 0 || exact_inner < 0 || num_pages < 0)
+    return SANATAN_ERR_INVALID;
+  if (static_cast<int64_t>(layers) * B == 0 || (inner == 0 && exact_inner == 0) || num_pages == 0)
+    return SANATAN_OK;
+  if (!ok_ptr(pages)) return SANATAN_ERR_INVALID;
+  if (inner > 0 && (!ok_ptr(state) || !ok_ptr(codes) || !ok_ptr(scales)))
+    return SANATAN_ERR_INVALID;
+  if (exact_inner > 0 && (!ok_ptr(exact) || !ok_ptr(exact_cache))) return SANATAN_ERR_INVALID;
+  // Thread blocks must fit a grid, and the largest offset 63 bits.
+  const int64_t most = (1LL << 31) - 1;
+  if (inner > (1LL << 40) || exact_inner > (1LL << 40) || num_pages > most)
+    return SANATAN_ERR_UNSUPPORTED;
+  const int64_t blocks = state_cache_blocks(inner);
+  if (blocks > most / (static_cast<int64_t>(layers) * B)) return SANATAN_ERR_UNSUPPORTED;
+  if (static_cast<double>(num_pages) * layers * (inner + exact_inner + 64.0) > 1e18)
+    return SANATAN_ERR_UNSUPPORTED;
+  if (int s = check_arch()) return s;
+  CacheArgs a;
+  a.state = state;
+  a.exact = exact;
+  a.layers = layers;
+  a.B = B;
+  a.inner = inner;
+  a.exact_inner = exact_inner;
+  a.pages = pages;
+  a.num_pages = num_pages;
+  a.fmt = fmt;
+  a.codes = codes;
+  a.scales = scales;
+  a.exact_cache = exact_cache;
+  a.blocks = static_cast<unsigned>(blocks);
+  return from_cuda(state_cache_launch(a, write, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 namespace sanatan {
@@ -549,6 +597,95 @@ int sanatan_decode_step(float* S, float* z, const float* q, const float* k, cons
   if (int s = check_arch()) return s;
   return from_cuda(decode_step_launch(S, z, q, k, v, gamma, omega, phi, pos, N, G, eps, o,
                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t sanatan_gated_scan_marks_size(int B, int T, int D) {
+  if (B < 0 || T < 0 || D < 0) return 0;
+  return static_cast<size_t>(B) * ((static_cast<size_t>(T) + kScanMark - 1) / kScanMark) * D *
+         sizeof(float);
+}
+
+int sanatan_gated_scan_fwd(const void* x, const void* g, int dtype, int gate, const int64_t* lens,
+                           int B, int T, int D, const float* h0, void* y, float* h_out,
+                           float* marks, void* stream) {
+  if (int s = check_scan(dtype, gate, B, T, D)) return s;
+  if (!ok_nullable(lens) || !ok_nullable(h0) || !ok_nullable(h_out) || !ok_nullable(marks))
+    return SANATAN_ERR_INVALID;
+  if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
+  if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || !ok_ptr(y))) return SANATAN_ERR_INVALID;
+  if (T == 0 && h_out == nullptr) return SANATAN_OK;
+  if (int s = check_arch()) return s;
+  ScanArgs a;
+  a.x = x;
+  a.g = g;
+  a.dtype = dtype;
+  a.gate = gate;
+  a.lens = lens;
+  a.B = B;
+  a.T = T;
+  a.D = D;
+  a.h0 = h0;
+  a.y = y;
+  a.h_out = h_out;
+  a.marks = marks;
+  return from_cuda(gated_scan_fwd_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+int sanatan_gated_scan_bwd(const void* x, const void* g, const void* dy, int dtype, int gate,
+                           const int64_t* lens, int B, int T, int D, const float* marks,
+                           const float* dh_out, void* dx, void* dg, float* dh0, void* stream) {
+  if (int s = check_scan(dtype, gate, B, T, D)) return s;
+  if (!ok_nullable(lens) || !ok_nullable(dh_out) || !ok_nullable(dh0)) return SANATAN_ERR_INVALID;
+  if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
+  if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || !ok_ptr(dy) || !ok_ptr(marks) || !ok_ptr(dx) ||
+                !ok_ptr(dg)))
+    return SANATAN_ERR_INVALID;
+  if (T == 0 && dh0 == nullptr) return SANATAN_OK;
+  if (int s = check_arch()) return s;
+  ScanBwdArgs a;
+  a.x = x;
+  a.g = g;
+  a.dy = dy;
+  a.dtype = dtype;
+  a.gate = gate;
+  a.lens = lens;
+  a.B = B;
+  a.T = T;
+  a.D = D;
+  a.marks = marks;
+  a.dh_out = dh_out;
+  a.dx = dx;
+  a.dg = dg;
+  a.dh0 = dh0;
+  return from_cuda(gated_scan_bwd_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+int sanatan_gated_scan_step(float* h, const void* x, const void* g, int dtype, int gate, int N,
+                            int D, void* y, void* stream) {
+  if (int s = check_scan(dtype, gate, N, 1, D)) return s;
+  const int64_t n = static_cast<int64_t>(N) * D;
+  if (n == 0) return SANATAN_OK;
+  if (!ok_ptr(h) || !ok_ptr(x) || !ok_ptr(g) || !ok_ptr(y)) return SANATAN_ERR_INVALID;
+  if (int s = check_arch()) return s;
+  return from_cuda(gated_scan_step_launch(h, x, g, dtype, gate, n, y,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+int sanatan_state_cache_write(const float* state, const float* exact, int layers, int B,
+                              int64_t inner, int64_t exact_inner, const int64_t* pages,
+                              int64_t num_pages, int fmt, void* codes, float* scales,
+                              float* exact_cache, void* stream) {
+  return state_cache(const_cast<float*>(state), const_cast<float*>(exact), layers, B, inner,
+                     exact_inner, pages, num_pages, fmt, codes, scales, exact_cache, true, stream);
+}
+
+int sanatan_state_cache_read(const void* codes, const float* scales, const float* exact_cache,
+                             int64_t num_pages, int fmt, const int64_t* pages, int layers, int B,
+                             int64_t inner, int64_t exact_inner, float* state, float* exact,
+                             void* stream) {
+  return state_cache(state, exact, layers, B, inner, exact_inner, pages, num_pages, fmt,
+                     const_cast<void*>(codes), const_cast<float*>(scales),
+                     const_cast<float*>(exact_cache), false, stream);
 }
 
 }  // extern "C"

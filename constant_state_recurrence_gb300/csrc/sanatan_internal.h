@@ -216,4 +216,52 @@ size_t pow_bwd_tc_workspace_bytes(int B, int H, int T);
 cudaError_t pow_bwd_tc_launch(const PowBwdArgs& a, cudaStream_t st);
 int pow_bwd_tc_read_and_clear_error(cudaStream_t st);
 int pow_tc_read_and_clear_error(cudaStream_t st);
+
+// Gated linear recurrence over [B, T, D] (gated_scan.cu).
+constexpr int kScanMark = 64;  // tokens between two marks (saved states)
+struct ScanArgs {
+  const void* x = nullptr;
+  const void* g = nullptr;
+  int dtype = 0, gate = 0;
+  const int64_t* lens = nullptr;  // [B] or null
+  int B = 0, T = 0, D = 0;
+  const float* h0 = nullptr;      // [B, D] or null
+  void* y = nullptr;
+  float* h_out = nullptr;         // [B, D] or null
+  float* marks = nullptr;         // [B, ceil(T / 64), D] or null
+};
+struct ScanBwdArgs {
+  const void* x = nullptr;
+  const void* g = nullptr;
+  const void* dy = nullptr;
+  int dtype = 0, gate = 0;
+  const int64_t* lens = nullptr;
+  int B = 0, T = 0, D = 0;
+  const float* marks = nullptr;
+  const float* dh_out = nullptr;  // [B, D] or null
+  void* dx = nullptr;
+  void* dg = nullptr;
+  float* dh0 = nullptr;           // [B, D] or null
+};
+cudaError_t gated_scan_fwd_launch(const ScanArgs& a, cudaStream_t st);
+cudaError_t gated_scan_bwd_launch(const ScanBwdArgs& a, cudaStream_t st);
+cudaError_t gated_scan_step_launch(float* h, const void* x, const void* g, int dtype, int gate,
+                                   int64_t n, void* y, cudaStream_t st);
+
+// Quantised state cache (state_cache.cu).
+struct CacheArgs {
+  float* state = nullptr;         // [layers, B, inner]
+  float* exact = nullptr;         // [layers, B, exact_inner] or null
+  int layers = 0, B = 0;
+  int64_t inner = 0, exact_inner = 0;
+  const int64_t* pages = nullptr;  // [B]
+  int64_t num_pages = 0;
+  int fmt = 0;
+  void* codes = nullptr;           // [num_pages, layers, ceil(inner / 64), 64]
+  float* scales = nullptr;         // [num_pages, layers, ceil(inner / 64)]
+  float* exact_cache = nullptr;    // [num_pages, layers, exact_inner] or null
+  unsigned blocks = 0;             // thread blocks of one stretch
+};
+int64_t state_cache_blocks(int64_t inner);
+cudaError_t state_cache_launch(const CacheArgs& a, bool write, cudaStream_t st);
 }  // namespace sanatan

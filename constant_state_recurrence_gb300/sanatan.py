@@ -12,6 +12,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libsanatan.so")
@@ -80,6 +81,17 @@ _SIGS = {
                                               _c_p, _c_p]),
     "sanatan_decode_step": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_int,
                                      _c_int, _c_int, _c_int, _c_f, _c_p, _c_p]),
+    "sanatan_gated_scan_marks_size": (_c_sz, [_c_int] * 3),
+    "sanatan_gated_scan_fwd": (_c_int, [_c_p, _c_p, _c_int, _c_int, _c_p, _c_int, _c_int, _c_int,
+                                        _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "sanatan_gated_scan_bwd": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_int, _c_p, _c_int, _c_int,
+                                        _c_int, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "sanatan_gated_scan_step": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_int, _c_int, _c_int, _c_p,
+                                         _c_p]),
+    "sanatan_state_cache_write": (_c_int, [_c_p, _c_p, _c_int, _c_int, _c_i64, _c_i64, _c_p,
+                                           _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p]),
+    "sanatan_state_cache_read": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_int, _c_p, _c_int, _c_int,
+                                          _c_i64, _c_i64, _c_p, _c_p, _c_p]),
 }
 
 _lib = None
@@ -727,6 +739,200 @@ def sanatan_decode_step_harmonic(S, z, q, k, v, gamma, omega, phi, pos, harmonic
                                               G, d, dv, int(harmonics), float(eps), _ptr(o),
                                               _stream(q.device)))
     return o
+
+
+SCAN_GATES = {"log": 0, "sigmoid": 1}
+SCAN_MARK = 64    # tokens between two saved states of the gated recurrence
+CACHE_GROUP = 64  # values that share a scale in the state cache
+_CACHE_FMT = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+def _gate(gate):
+    if gate not in SCAN_GATES:
+        raise ValueError(f"gate must be one of {tuple(SCAN_GATES)}, not {gate!r}")
+    return SCAN_GATES[gate]
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _call(name, dev, *args):
+    """Call a library function with the tensors' device current, on its stream."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev))
+    _check(name, st)
+
+
+def _scan_args(x, g, gate, lens):
+    _need(x, "x", (torch.float32, torch.bfloat16))
+    if x.dim() != 3:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, T, D]")
+    _need(g, "g", (x.dtype,), x.shape)
+    if lens is not None:
+        _need(lens, "lens", (torch.int64,), (x.shape[0],))
+    return _gate(gate)
+
+
+def sanatan_gated_scan_fwd(x, g, gate="log", h0=None, lens=None, want_state=False,
+                           want_marks=False, out=None, h_out=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + u_t over x, g [B, T, D] (f32
+    or bf16): gate "log" has a = exp(g), u = x, gate "sigmoid" a = 1 / (1 +
+    exp(-g)), u = (1 - a) x.  h0 [B, D] f32 is the state before the first
+    token; tokens from lens[b] (int64 [B]) on are left out and give zeros.
+
+    Returns (y [B,T,D] in x's dtype, the last state [B,D] f32 or None, marks
+    [B, ceil(T/64), D] f32 (states for the backward) or None)."""
+    gt = _scan_args(x, g, gate, lens)
+    B, T, D = x.shape
+    dev = x.device
+    y = torch.empty_like(x) if out is None else _need(out, "out", (x.dtype,), x.shape)
+    if h0 is not None:
+        _need(h0, "h0", (torch.float32,), (B, D))
+    if h_out is not None:
+        _need(h_out, "h_out", (torch.float32,), (B, D))
+    elif want_state:
+        h_out = torch.empty(B, D, dtype=torch.float32, device=dev)
+    marks = torch.empty(B, -(-T // SCAN_MARK), D, dtype=torch.float32, device=dev) \
+        if want_marks else None
+    _same_device(dev, g=g, h0=h0, lens=lens, out=y, h_out=h_out)
+    _call("sanatan_gated_scan_fwd", dev, _ptr(x), _ptr(g), _DT[x.dtype], gt, _ptr(lens), B, T, D,
+          _ptr(h0), _ptr(y), _ptr(h_out), _ptr(marks))
+    return y, h_out, marks
+
+
+def sanatan_gated_scan_bwd(x, g, dy, marks, gate="log", lens=None, dh_last=None, want_dh0=False):
+    """Gradients of sum(y * dy) + sum(h_last * dh_last) for
+    sanatan_gated_scan_fwd: dict(dx, dg, dh0); marks are the forward's."""
+    gt = _scan_args(x, g, gate, lens)
+    B, T, D = x.shape
+    dev = x.device
+    _need(dy, "dy", (x.dtype,), x.shape)
+    _need(marks, "marks", (torch.float32,), (B, -(-T // SCAN_MARK), D))
+    if dh_last is not None:
+        _need(dh_last, "dh_last", (torch.float32,), (B, D))
+    _same_device(dev, g=g, dy=dy, marks=marks, lens=lens, dh_last=dh_last)
+    dx, dg = torch.empty_like(x), torch.empty_like(g)
+    dh0 = torch.empty(B, D, dtype=torch.float32, device=dev) if want_dh0 else None
+    _call("sanatan_gated_scan_bwd", dev, _ptr(x), _ptr(g), _ptr(dy), _DT[x.dtype], gt, _ptr(lens),
+          B, T, D, _ptr(marks), _ptr(dh_last), _ptr(dx), _ptr(dg), _ptr(dh0))
+    return dict(dx=dx, dg=dg, dh0=dh0)
+
+
+def sanatan_gated_scan_step(h, x, g, gate="log", out=None):
+    """One token of the gated recurrence for N sequences: h [N, D] f32 is
+    updated in place, x and g [N, D] f32 or bf16.  Returns y [N, D]."""
+    _need(x, "x", (torch.float32, torch.bfloat16))
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [N, D]")
+    _need(g, "g", (x.dtype,), x.shape)
+    _need(h, "h", (torch.float32,), x.shape)
+    y = torch.empty_like(x) if out is None else _need(out, "out", (x.dtype,), x.shape)
+    _same_device(x.device, h=h, g=g, out=y)
+    _call("sanatan_gated_scan_step", x.device, _ptr(h), _ptr(x), _ptr(g), _DT[x.dtype],
+          _gate(gate), x.shape[0], x.shape[1], _ptr(y))
+    return y
+
+
+class GatedScan(torch.autograd.Function):
+    """autograd wrapper: (y, h_last) = GatedScan.apply(x, g, gate, h0, lens);
+    forward = sanatan_gated_scan_fwd, backward = sanatan_gated_scan_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, g, gate="log", h0=None, lens=None):
+        y, h, marks = sanatan_gated_scan_fwd(x, g, gate, h0=h0, lens=lens, want_state=True,
+                                             want_marks=any(ctx.needs_input_grad))
+        ctx.save_for_backward(x, g, marks, lens)
+        ctx.gate = gate
+        ctx.want_dh0 = h0 is not None and ctx.needs_input_grad[3]
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh_last):
+        x, g, marks, lens = ctx.saved_tensors
+        if dy is None and dh_last is None:
+            return None, None, None, None, None
+        dy = torch.zeros_like(x) if dy is None else dy.contiguous()
+        dh_last = None if dh_last is None else dh_last.contiguous()
+        d = sanatan_gated_scan_bwd(x, g, dy, marks, ctx.gate, lens=lens, dh_last=dh_last,
+                                   want_dh0=ctx.want_dh0)
+        return d["dx"], d["dg"], None, d["dh0"], None
+
+
+def _cache_args(state, pages, codes, scales, z, z_cache, layers, name):
+    """Checks shared by the two directions; returns (B, inner, z's inner, P, format)."""
+    _need(state, name, (torch.float32,))
+    _need(pages, "pages", (torch.int64,))
+    _need(codes, "codes", tuple(_CACHE_FMT))
+    if pages.dim() != 1 or codes.dim() != 4:
+        raise ValueError("pages must be [B] and codes [P, layers, groups, 64]")
+    B, P = pages.shape[0], codes.shape[0]
+    n = int(layers) * B
+    if layers < 1 or (n and state.numel() % n) or (not n and state.numel()):
+        raise ValueError(f"{name} has shape {tuple(state.shape)}: not {layers} layers of {B} "
+                         "sequences")
+    inner = state.numel() // n if n else 0
+    groups = -(-inner // CACHE_GROUP)
+    if n:
+        _need(codes, "codes", None, (P, layers, groups, CACHE_GROUP))
+        _need(scales, "scales", (torch.float32,), (P, layers, groups))
+    if (z is None) != (z_cache is None):
+        raise ValueError("z and z_cache go together")
+    zi = 0
+    if z is not None:
+        _need(z, "z", (torch.float32,))
+        if (n and z.numel() % n) or (not n and z.numel()):
+            raise ValueError(f"z has shape {tuple(z.shape)}: not {layers} layers of {B} sequences")
+        zi = z.numel() // n if n else 0
+        if n:
+            _need(z_cache, "z_cache", (torch.float32,), (P, layers, zi))
+    _same_device(state.device, pages=pages, codes=codes, scales=scales, z=z, z_cache=z_cache)
+    return B, inner, zi, P, _CACHE_FMT[codes.dtype]
+
+
+def state_cache_empty(pages, inner, z_inner=0, layers=1, dtype=torch.int8, device=None):
+    """A pool of zeroed pages: (codes [pages, layers, ceil(inner/64), 64] int8 or
+    float8_e4m3fn, scales f32, z_cache [pages, layers, z_inner] f32 or None)."""
+    if dtype not in _CACHE_FMT:
+        raise ValueError(f"dtype must be one of {tuple(_CACHE_FMT)}, not {dtype}")
+    groups = -(-int(inner) // CACHE_GROUP)
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    codes = torch.zeros(pages, layers, groups, CACHE_GROUP, dtype=torch.int8, device=dev)
+    scales = torch.zeros(pages, layers, groups, dtype=torch.float32, device=dev)
+    zc = torch.zeros(pages, layers, z_inner, dtype=torch.float32, device=dev) if z_inner else None
+    return codes.view(dtype), scales, zc
+
+
+def sanatan_state_cache_write(state, pages, codes, scales, z=None, z_cache=None, layers=1):
+    """Keep the float32 states of B sequences in the pages[b] of a pool (int8 or
+    e4m3 codes with a scale per 64 values; z in float32).  state is read as
+    [layers, B, inner] and z as [layers, B, z_inner] (any shape of that many
+    values, e.g. the S and z of sanatan_chunk_fwd, of decode slots in
+    sequence-major order, or, with layers = L, of the stack decode); pages [B]
+    int64, where a value outside the pool leaves the sequence out.  See
+    include/sanatan.h for the formats."""
+    B, inner, zi, P, fmt = _cache_args(state, pages, codes, scales, z, z_cache, layers, "state")
+    _call("sanatan_state_cache_write", state.device, _ptr(state), _ptr(z), layers, B, inner, zi,
+          _ptr(pages), P, fmt, _ptr(codes), _ptr(scales), _ptr(z_cache))
+
+
+def sanatan_state_cache_read(codes, scales, pages, state, z_cache=None, z=None, layers=1):
+    """Take the states of B sequences up from the pages[b] of a pool into state
+    (and z), laid out as for sanatan_state_cache_write.  A page may serve
+    several sequences; sequences whose page is outside the pool keep what state
+    holds.  Returns state."""
+    B, inner, zi, P, fmt = _cache_args(state, pages, codes, scales, z, z_cache, layers, "state")
+    _call("sanatan_state_cache_read", state.device, _ptr(codes), _ptr(scales), _ptr(z_cache), P,
+          fmt, _ptr(pages), layers, B, inner, zi, _ptr(state), _ptr(z))
+    return state
 
 
 class SanatanAttention(torch.autograd.Function):

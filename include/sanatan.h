@@ -64,6 +64,12 @@ enum sanatan_status {
 /* Element types of q, k, v (and of dq, dk, dv, dO where stated). */
 enum sanatan_dtype { SANATAN_F32 = 0, SANATAN_BF16 = 1 };
 
+/* Gates of the gated linear recurrence (sanatan_gated_scan_fwd). */
+enum sanatan_gate { SANATAN_GATE_LOG = 0, SANATAN_GATE_SIGMOID = 1 };
+
+/* Code formats of the state cache (sanatan_state_cache_write). */
+enum sanatan_cache_format { SANATAN_CACHE_INT8 = 0, SANATAN_CACHE_E4M3 = 1 };
+
 /* Human-readable text of a status code (static storage, never NULL). */
 SANATAN_API const char* sanatan_status_string(int status);
 
@@ -422,6 +428,109 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
                         const float* gamma, const float* omega, const float* phi,
                         const int64_t* pos, int N, int G, int d, int dv, float eps, float* o,
                         void* stream);
+
+/*
+ * Gated linear recurrence: a second constant-state mixer beside the attention
+ * above, for layers that forget.  Per channel of [B, T, D], with a float32
+ * state h [B, D]:
+ *     h_t = a_t h_{t-1} + u_t,   y_t = h_t,
+ *     SANATAN_GATE_LOG:      a = exp(g),           u = x        (g: log of the decay)
+ *     SANATAN_GATE_SIGMOID:  a = 1 / (1 + exp(-g)), u = (1 - a) x
+ * The sequence mixers are the notes' own comparison (§4.1 names gated linear
+ * attention); the pages give no formula for a gate, these are the plain ones.
+ *   x, g    [B, T, D]  dtype;   y [B, T, D] dtype (the float32 state rounded once)
+ *   lens    [B] int64 or NULL: tokens of each sequence (values outside [0, T]
+ *           are taken as the nearest of the two).  Tokens from lens[b] on are
+ *           not read; their y, dx and dg are written as zeros, and the state
+ *           passes them unchanged.  NULL: all T tokens.
+ *   h0      [B, D] f32 or NULL (zero): the state before the first token
+ *   h_out   [B, D] f32 or NULL: the state after the last token
+ *   marks   sanatan_gated_scan_marks_size(B, T, D) bytes or NULL: float32
+ *           [B, ceil(T / 64), D], the states before tokens 0, 64, 128, ...,
+ *           from which the backward recomputes h.
+ * With the log gate g <= 0 is meant; g = -inf (a = 0) starts a new text.  Gates
+ * above 0 grow, and give what the formula gives while the products of the
+ * decays stay finite.  Values that are not finite reach only later tokens (and,
+ * backward, earlier ones) of their own sequence and channel.
+ * All sums are taken in a fixed order: the same call gives the same bits.
+ * B = 0 or D = 0 does nothing; T = 0 copies h0 (or zeros) to h_out.
+ *
+ * sanatan_gated_scan_bwd -- gradients of sum(y * dy) + sum(h_out * dh_out):
+ *   marks as the forward wrote them for the same x, g, h0 and lens (h0 is their
+ *   first row); dy [B, T, D] dtype; dh_out [B, D] f32 or NULL (zero);
+ *   dx, dg [B, T, D] dtype outputs; dh0 [B, D] f32 output or NULL.
+ *     dh_t = dy_t + a_{t+1} dh_{t+1};  dh0 = a_0 dh_0;
+ *     log: dx = dh, dg = dh a h_{t-1};
+ *     sigmoid: dx = dh (1 - a), dg = dh (h_{t-1} - x) a (1 - a).
+ * sanatan_gated_scan_step -- one token of N sequences: h [N, D] f32 is updated
+ *   in place, x, g, y [N, D] dtype.
+ * Errors: SANATAN_ERR_INVALID for an unknown dtype or gate, a negative size, a
+ * null (where not allowed) or misaligned pointer; SANATAN_ERR_UNSUPPORTED for
+ * B * D (N * D) of 2^31 or more.  Outputs must not overlap inputs (the step's h
+ * excepted).
+ */
+SANATAN_API size_t sanatan_gated_scan_marks_size(int B, int T, int D);
+SANATAN_API int sanatan_gated_scan_fwd(const void* x, const void* g, int dtype, int gate,
+                                       const int64_t* lens, int B, int T, int D, const float* h0,
+                                       void* y, float* h_out, float* marks, void* stream);
+SANATAN_API int sanatan_gated_scan_bwd(const void* x, const void* g, const void* dy, int dtype,
+                                       int gate, const int64_t* lens, int B, int T, int D,
+                                       const float* marks, const float* dh_out, void* dx,
+                                       void* dg, float* dh0, void* stream);
+SANATAN_API int sanatan_gated_scan_step(float* h, const void* x, const void* g, int dtype,
+                                        int gate, int N, int D, void* y, void* stream);
+
+/*
+ * State cache: the constant states of sequences that are not being decoded
+ * (paused sessions, shared prefixes) kept in 8 bits in a pool of pages, one page
+ * a sequence, and taken up again into float32 states.  The paper has no
+ * counterpart; the state is what its method has in place of a key-value cache
+ * (Notes §4.5).
+ *   state   [layers, B, inner] f32: sequence b's state is `layers` stretches of
+ *           `inner` values.  layers = 1 is the sequence-major order of
+ *           sanatan_chunk_fwd's S_out and sanatan_decode_step's slots (inner =
+ *           heads * 6d * dv, or layers * heads * 6d * dv when slots are ordered
+ *           sequence-major); the stack decode's S [L, B * heads, 6d, dv] has
+ *           layers = L, inner = heads * 6d * dv; the gated recurrence's h
+ *           [B, D] has layers = 1, inner = D.
+ *   exact   [layers, B, exact_inner] f32 or NULL (exact_inner = 0): values that
+ *           are kept in float32: z, which every output is divided by through
+ *           Phi(q) . z.
+ *   pages   [B] int64: the page of each sequence, in [0, num_pages); any other
+ *           value (-1) leaves that sequence out: nothing of it is read or
+ *           written.  Where a write names a page twice the last of the call's
+ *           sequences is kept; a read may name a page any number of times.
+ *   codes   [num_pages, layers, ceil(inner / 64), 64] 8-bit codes,
+ *   scales  [num_pages, layers, ceil(inner / 64)] f32, one a group of 64
+ *           consecutive values x (with dv = 64, one a feature row):
+ *     SANATAN_CACHE_INT8: s = max|x| / 127 rounded to float32; the code is the
+ *       integer nearest to the exact x / s, ties to even.
+ *     SANATAN_CACHE_E4M3: s = the smallest power of two with max|x| / s <= 448;
+ *       the code is x / s rounded to e4m3, ties to even.
+ *     The value read back is code * s in float32: off by at most s / 2 = max|x| /
+ *     254 (and the product's rounding) with int8, by 2^-4 of the value (2^-10 s
+ *     where |x| < 2^-6 s) with e4m3.
+ *     A group whose largest magnitude is below 2^-100 is stored as zeros, one
+ *     with a value that is not finite, or is 2^127 or more, reads back as NaN.
+ *   exact_cache  [num_pages, layers, exact_inner] f32 or NULL.
+ * Pages that the call does not name, and state of sequences left out, stay as
+ * they were.  The fill of a last group (inner not a multiple of 64) is stored as
+ * code 0.  Two calls that write the same page must be ordered by the caller.
+ * Errors: SANATAN_ERR_INVALID for an unknown format, a negative size, a null
+ * (where not allowed) or misaligned pointer; SANATAN_ERR_UNSUPPORTED for sizes
+ * whose thread blocks or offsets leave the grid.  layers = 0, B = 0, num_pages
+ * = 0 or no values at all does nothing.
+ */
+SANATAN_API int sanatan_state_cache_write(const float* state, const float* exact, int layers,
+                                          int B, int64_t inner, int64_t exact_inner,
+                                          const int64_t* pages, int64_t num_pages, int fmt,
+                                          void* codes, float* scales, float* exact_cache,
+                                          void* stream);
+SANATAN_API int sanatan_state_cache_read(const void* codes, const float* scales,
+                                         const float* exact_cache, int64_t num_pages, int fmt,
+                                         const int64_t* pages, int layers, int B, int64_t inner,
+                                         int64_t exact_inner, float* state, float* exact,
+                                         void* stream);
 
 #ifdef __cplusplus
 }

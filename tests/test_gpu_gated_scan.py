@@ -1,0 +1,421 @@
+"""The gated linear recurrence on the GPU (scan forward, backward, single-token
+step, autograd) against the float64 definitions.
+
+Tolerances, element by element, from the rounding steps e = 2^-24 of float32: a
+decay and its 1 - a are within k = (10 + 2 |g|) e of their values (exponential
+2 ulp, its argument's product half an ulp of |g|, sum and reciprocal 1 ulp each);
+every token adds a multiplication and an addition, and a scan in pieces at most
+40 more additions on the way to a token.  With Hm the recurrence of |u| and |h0|,
+    E_t = a_t (E_{t-1} + (k + 3 e) Hm_{t-1}) + (k + 3 e) |u_t|
+bounds the state's error up to 40 e Hm_t, and the same in reverse time bounds
+dh's.  Products of both add up.  An output in bf16 is off by half a step more,
+2^-8 of its value (float32: 2^-24); 1e-36 stands for underflow."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.state_oracle as R
+from constant_state_recurrence_gb300 import sanatan as S
+from gpu_util import dev, f64
+
+pytestmark = pytest.mark.gpu
+
+E = 2.0 ** -24
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def make(B, T, D, dtype, gate, seed, h0=True, bias=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(B, T, D, generator=gen)
+    g = torch.randn(B, T, D, generator=gen) + bias
+    if gate == "log":
+        g = -torch.nn.functional.softplus(-g)
+    dy = torch.randn(B, T, D, generator=gen)
+    h = torch.randn(B, D, generator=gen) if h0 else None
+    dh = torch.randn(B, D, generator=gen) if h0 else None
+    return x.to(dtype), g.to(dtype), dy.to(dtype), h, dh
+
+
+def bounds(x, g, gate, h0, dy=None, dh_last=None, lens=None):
+    """Error bounds before the outputs' own rounding: dict of arrays."""
+    B, T, D = x.shape
+    a, keep, u = R.gates(x, g, gate)
+    k = (10 + 2 * np.where(np.isfinite(g), np.abs(g), 0.0)) * E
+    if lens is not None:
+        gone = (np.arange(T)[None] >= np.asarray(lens)[:, None])[..., None]
+        a, u, k = np.where(gone, 1.0, a), np.where(gone, 0.0, u), np.where(gone, 0.0, k)
+    Hm = np.zeros((B, T + 1, D))
+    Er = np.zeros((B, T + 1, D))
+    if h0 is not None:
+        Hm[:, 0] = np.abs(h0)
+    for t in range(T):
+        Hm[:, t + 1] = a[:, t] * Hm[:, t] + np.abs(u[:, t])
+        Er[:, t + 1] = a[:, t] * (Er[:, t] + (k[:, t] + 3 * E) * Hm[:, t]) \
+            + (k[:, t] + 3 * E) * np.abs(u[:, t])
+    Er = Er + 40 * E * Hm + 1e-36
+    out = dict(y=Er[:, 1:], last=Er[:, -1], before=Er[:, :-1])
+    if dy is None:
+        return out
+    Dm, Ed = np.zeros((B, T, D)), np.zeros((B, T, D))
+    m = np.zeros((B, D)) if dh_last is None else np.abs(dh_last)
+    e = np.zeros((B, D))
+    for t in range(T - 1, -1, -1):
+        Dm[:, t] = m + np.abs(dy[:, t])
+        Ed[:, t] = e + 2 * E * Dm[:, t]
+        e = a[:, t] * (Ed[:, t] + (k[:, t] + 3 * E) * Dm[:, t])
+        m = a[:, t] * Dm[:, t]
+    Ed = Ed + 40 * E * Dm + 1e-36
+    out["dh0"] = e + 40 * E * m + 1e-36
+    Hb, Eb = Hm[:, :-1], Er[:, :-1]
+    if gate == "log":
+        out["dx"] = Ed
+        out["dg"] = a * (Hb * Ed + Dm * Eb) + (k + 4 * E) * a * Dm * Hb
+    else:
+        w = Hb + np.abs(x)
+        out["dx"] = keep * (Ed + (k + 2 * E) * Dm)
+        out["dg"] = a * keep * (w * Ed + Dm * (Eb + 2 * E * w)) + (2 * k + 6 * E) * a * keep * Dm * w
+    return out
+
+
+def close(got, ref, bound, dtype, what):
+    got = f64(got)
+    assert got.shape == ref.shape, what
+    room = bound * (1 + 1e-3) + HALF[dtype] * (np.abs(ref) + bound) + 1e-36
+    off = np.abs(got - ref) - room
+    assert np.isfinite(got).all(), what
+    assert off.max(initial=-1.0) <= 0, (what, np.unravel_index(off.argmax(), off.shape), off.max())
+
+
+def check(B, T, D, dtype, gate, seed=0, h0=True, lens=None, bias=1.0):
+    x, g, dy, h, dh = make(B, T, D, dtype, gate, seed, h0, bias)
+    d = lambda t: None if t is None else t.to(dev())  # noqa: E731
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int64)
+    y, last, marks = S.sanatan_gated_scan_fwd(d(x), d(g), gate, h0=d(h), lens=d(ln),
+                                              want_state=True, want_marks=True)
+    gr = S.sanatan_gated_scan_bwd(d(x), d(g), d(dy), marks, gate, lens=d(ln), dh_last=d(dh),
+                                  want_dh0=True)
+    S.device_status()
+    n = lambda t: None if t is None else f64(t)  # noqa: E731
+    cut = None if lens is None else [min(max(v, 0), T) for v in lens]
+    y_ref, last_ref, before = R.gated_scan(n(x), n(g), gate, n(h), cut)
+    dx, dg, dh0 = R.gated_scan_backward(n(x), n(g), gate, n(dy), n(h), cut, n(dh))
+    b = bounds(n(x), n(g), gate, n(h), n(dy), n(dh), cut)
+    there = np.ones((B, T, 1)) if cut is None else \
+        (np.arange(T)[None] < np.asarray(cut)[:, None])[..., None]
+    close(y, y_ref, b["y"] * there, dtype, "y")
+    close(last, last_ref, b["last"], F32, "h_last")
+    close(marks, before[:, ::64], b["before"][:, ::64], F32, "marks")
+    close(gr["dx"], dx, b["dx"] * there, dtype, "dx")
+    close(gr["dg"], dg, b["dg"] * there, dtype, "dg")
+    close(gr["dh0"], dh0, b["dh0"], F32, "dh0")
+
+
+SHAPES = [(1, 1, 1), (1, 1, 64), (2, 2, 3), (1, 7, 4), (3, 63, 65), (2, 64, 64), (2, 65, 130),
+          (1, 127, 768), (2, 128, 12), (3, 129, 100), (1, 1000, 33), (5, 300, 257), (70, 5, 64),
+          (2, 2049, 72)]
+
+
+@pytest.mark.parametrize("gate", ["log", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,D", SHAPES)
+def test_forward_and_backward(B, T, D, dtype, gate):
+    check(B, T, D, dtype, gate, seed=B + T + D)
+
+
+@pytest.mark.parametrize("gate", ["log", "sigmoid"])
+@pytest.mark.parametrize("B,T,D,lens", [
+    (4, 150, 64, [150, 149, 1, 0]), (3, 700, 70, [650, 64, 128]), (2, 40, 5, [-7, 1 << 40]),
+    (1, 2000, 8, [1030])])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_lengths(B, T, D, lens, gate, dtype):
+    check(B, T, D, dtype, gate, seed=T, lens=lens)
+
+
+def test_lengths_leave_what_lies_behind_unread():
+    """NaN in the padding reaches neither outputs, state nor gradients."""
+    x, g, dy, h, _ = make(2, 200, 66, F32, "sigmoid", 3)
+    lens = torch.tensor([130, 3], dtype=torch.int64)
+    for b in range(2):
+        for t in (x, g, dy):
+            t[b, lens[b]:] = float("nan")
+    d = lambda t: t.to(dev())  # noqa: E731
+    y, last, marks = S.sanatan_gated_scan_fwd(d(x), d(g), "sigmoid", h0=d(h), lens=d(lens),
+                                              want_state=True, want_marks=True)
+    gr = S.sanatan_gated_scan_bwd(d(x), d(g), d(dy), marks, "sigmoid", lens=d(lens), want_dh0=True)
+    for b in range(2):
+        n = int(lens[b])
+        for t in (y, gr["dx"], gr["dg"]):
+            assert not t[b, n:].any() and torch.isfinite(t[b]).all()
+    assert torch.isfinite(last).all() and torch.isfinite(gr["dh0"]).all()
+
+
+def test_without_initial_state_and_without_gradients_of_it():
+    check(2, 130, 48, BF16, "log", seed=4, h0=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_long_memory(dtype):
+    """Decays next to 1 over a long sequence (a channel's memory: hundreds of tokens)."""
+    check(1, 6000, 16, dtype, "log", seed=9, bias=6.0)
+    check(1, 6000, 16, dtype, "sigmoid", seed=10, bias=6.0)
+
+
+@pytest.mark.parametrize("gate", ["log", "sigmoid"])
+def test_closed_and_open_gates(gate):
+    """Gates of -inf start a new text; the sigmoid's of +inf keep the state."""
+    x, g, dy, h, dh = make(1, 300, 64, F32, gate, 11)
+    g[0, 100] = g[0, 228, :32] = -float("inf")
+    if gate == "sigmoid":
+        g[0, 50] = float("inf")
+    d = lambda t: t.to(dev())  # noqa: E731
+    y, last, marks = S.sanatan_gated_scan_fwd(d(x), d(g), gate, h0=d(h), want_state=True,
+                                              want_marks=True)
+    gr = S.sanatan_gated_scan_bwd(d(x), d(g), d(dy), marks, gate, dh_last=d(dh), want_dh0=True)
+    y_ref, _, _ = R.gated_scan(f64(x), f64(g), gate, f64(h))
+    dx, dg, dh0 = R.gated_scan_backward(f64(x), f64(g), gate, f64(dy), f64(h), None, f64(dh))
+    b = bounds(f64(x), f64(g), gate, f64(h), f64(dy), f64(dh))
+    close(y, y_ref, b["y"], F32, "y")
+    close(gr["dx"], dx, b["dx"], F32, "dx")
+    close(gr["dg"], dg, b["dg"], F32, "dg")
+    close(gr["dh0"], dh0, b["dh0"], F32, "dh0")
+    if gate == "log":       # a = 0: nothing of what lies before, to the bit
+        assert torch.equal(y[:, 100], d(x)[:, 100]) and not gr["dg"][:, 100].any()
+
+
+def test_values_that_are_not_finite_stay_in_their_channel():
+    x, g, _, _, _ = make(2, 500, 70, F32, "log", 12)
+    x[0, 200, 7] = float("nan")
+    x[1, 300, 69] = float("inf")
+    y, last, _ = S.sanatan_gated_scan_fwd(x.to(dev()), g.to(dev()), want_state=True)
+    bad = ~torch.isfinite(y).cpu()
+    want = torch.zeros_like(bad)
+    want[0, 200:, 7] = True
+    want[1, 300:, 69] = True
+    assert torch.equal(bad, want)
+    assert torch.isnan(last[0, 7]) and torch.isinf(last[1, 69])
+
+
+def test_one_call_is_two_halves():
+    """The state carries a sequence over two calls, and its gradient back."""
+    x, g, dy, h, dh = make(2, 333, 96, F32, "log", 13)
+    d = lambda t: t.contiguous().to(dev())  # noqa: E731
+    whole, last, _ = S.sanatan_gated_scan_fwd(d(x), d(g), h0=d(h), want_state=True)
+    y1, s1, m1 = S.sanatan_gated_scan_fwd(d(x[:, :200]), d(g[:, :200]), h0=d(h), want_state=True,
+                                          want_marks=True)
+    y2, s2, m2 = S.sanatan_gated_scan_fwd(d(x[:, 200:]), d(g[:, 200:]), h0=s1, want_state=True,
+                                          want_marks=True)
+    b = bounds(f64(x), f64(g), "log", f64(h), f64(dy), f64(dh))
+    assert (np.abs(f64(torch.cat([y1, y2], 1)) - f64(whole)) <= 2 * b["y"]).all()
+    assert (np.abs(f64(s2) - f64(last)) <= 2 * b["last"]).all()
+    g2 = S.sanatan_gated_scan_bwd(d(x[:, 200:]), d(g[:, 200:]), d(dy[:, 200:]), m2, dh_last=d(dh),
+                                  want_dh0=True)
+    g1 = S.sanatan_gated_scan_bwd(d(x[:, :200]), d(g[:, :200]), d(dy[:, :200]), m1,
+                                  dh_last=g2["dh0"], want_dh0=True)
+    dx, dg, dh0 = R.gated_scan_backward(f64(x), f64(g), "log", f64(dy), f64(h), None, f64(dh))
+    close(torch.cat([g1["dx"], g2["dx"]], 1), dx, 2 * b["dx"], F32, "dx")
+    close(torch.cat([g1["dg"], g2["dg"]], 1), dg, 2 * b["dg"], F32, "dg")
+    close(g1["dh0"], dh0, 2 * b["dh0"], F32, "dh0")
+
+
+def test_same_call_same_bits():
+    x, g, dy, h, dh = (t.to(dev()) for t in make(2, 1500, 200, BF16, "sigmoid", 14))
+    runs = []
+    for _ in range(3):
+        y, last, marks = S.sanatan_gated_scan_fwd(x, g, "sigmoid", h0=h, want_state=True,
+                                                  want_marks=True)
+        gr = S.sanatan_gated_scan_bwd(x, g, dy, marks, "sigmoid", dh_last=dh, want_dh0=True)
+        runs.append((y, last, marks, gr["dx"], gr["dg"], gr["dh0"]))
+    for r in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(runs[0], r))
+
+
+@pytest.mark.parametrize("gate", ["log", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,D", [(1, 1), (1, 768), (3, 5), (9, 129), (400, 768)])
+def test_step(N, D, dtype, gate):
+    x, g, _, h, _ = make(N, 1, D, dtype, gate, N + D)
+    hd = h.to(dev())
+    y = S.sanatan_gated_scan_step(hd, x[:, 0].contiguous().to(dev()),
+                                  g[:, 0].contiguous().to(dev()), gate)
+    ref = R.gated_scan_step(f64(h), f64(x[:, 0]), f64(g[:, 0]), gate)
+    b = bounds(f64(x), f64(g), gate, f64(h))["last"]
+    close(hd, ref, b, F32, "h")
+    close(y, ref, b, dtype, "y")
+    assert torch.equal(y, hd.to(dtype))
+
+
+def test_steps_continue_a_scan():
+    x, g, _, h, _ = make(3, 40, 100, F32, "sigmoid", 15)
+    d = lambda t: t.contiguous().to(dev())  # noqa: E731
+    _, state, _ = S.sanatan_gated_scan_fwd(d(x[:, :30]), d(g[:, :30]), "sigmoid", h0=d(h),
+                                           want_state=True)
+    ref, last, _ = R.gated_scan(f64(x), f64(g), "sigmoid", f64(h))
+    b = bounds(f64(x), f64(g), "sigmoid", f64(h))
+    for t in range(30, 40):
+        y = S.sanatan_gated_scan_step(state, d(x[:, t]), d(g[:, t]), "sigmoid")
+        close(y, ref[:, t], b["y"][:, t], F32, t)
+    close(state, last, b["last"], F32, "state")
+
+
+def test_empty_problems():
+    h = torch.randn(2, 8, device=dev())
+    x = torch.empty(2, 0, 8, device=dev())
+    y, last, marks = S.sanatan_gated_scan_fwd(x, x, h0=h, want_state=True, want_marks=True)
+    assert y.shape == x.shape and torch.equal(last, h) and marks.shape == (2, 0, 8)
+    gr = S.sanatan_gated_scan_bwd(x, x, x, marks, dh_last=h, want_dh0=True)
+    assert torch.equal(gr["dh0"], h)
+    _, last, _ = S.sanatan_gated_scan_fwd(x, x, want_state=True)
+    assert not last.any()
+    for shape in ((0, 5, 8), (3, 5, 0)):
+        x = torch.empty(shape, device=dev())
+        y, last, _ = S.sanatan_gated_scan_fwd(x, x, want_state=True)
+        assert y.shape == x.shape and last.shape == (shape[0], shape[2])
+    e = torch.empty(0, 8, device=dev())
+    assert S.sanatan_gated_scan_step(e, e, e).shape == (0, 8)
+
+
+def test_large_sequence_sampled_channels():
+    """B=1, T=32768, D=768 bf16 (a long prefill of a layer): every token of some
+    channels, in every block of channels."""
+    gen = torch.Generator(device=dev()).manual_seed(16)
+    x = torch.randn(1, 32768, 768, generator=gen, device=dev()).to(BF16)
+    g = (torch.randn(1, 32768, 768, generator=gen, device=dev()) + 2).to(BF16)
+    y, last, _ = S.sanatan_gated_scan_fwd(x, g, "sigmoid", want_state=True)
+    pick = torch.arange(0, 768, 31, device=dev())
+    xs, gs = f64(x[..., pick]), f64(g[..., pick])
+    ref, last_ref, _ = R.gated_scan(xs, gs, "sigmoid")
+    b = bounds(xs, gs, "sigmoid", None)
+    close(y[..., pick], ref, b["y"], BF16, "y")
+    close(last[..., pick], last_ref, b["last"], F32, "last")
+
+
+def test_offsets_beyond_32_bits():
+    """B T D of more than 2^31 elements: the last sequence is where it should be."""
+    B, T, D = 3, 32768, 22000
+    x = torch.zeros(B, T, D, dtype=BF16, device=dev())
+    g = torch.zeros(B, T, D, dtype=BF16, device=dev())
+    x[2, -1] = torch.arange(D, device=dev()).remainder(251).to(BF16)
+    x[2, -2] = 1.0
+    y, last, _ = S.sanatan_gated_scan_fwd(x, g, want_state=True)     # a = 1: running sums
+    want = torch.arange(D, device=dev()).remainder(251).float() + 1
+    assert torch.equal(last[2], want) and not last[:2].any()
+    assert torch.equal(y[2, -1], want.to(BF16)) and not y[:2].any() and not y[2, :-2].any()
+
+
+def test_autograd_trains_gates_inputs_and_states():
+    """Gradients through GatedScan of a projection shared by two scans, against
+    float64 autograd-free formulas and differences of the float64 definition."""
+    x, g, dy, h, dh = make(2, 70, 24, F32, "sigmoid", 17)
+    xs = x.to(dev()).requires_grad_()
+    gs = g.to(dev()).requires_grad_()
+    h0 = h[:1].to(dev()).requires_grad_()          # one learned state for the whole batch
+    y, last = S.GatedScan.apply(xs, gs, "sigmoid", h0.expand(2, -1).contiguous())
+    (y * dy.to(dev())).sum().add((last * dh.to(dev())).sum()).backward()
+    h2 = np.repeat(f64(h[:1]), 2, 0)
+    dx, dg, dh0 = R.gated_scan_backward(f64(x), f64(g), "sigmoid", f64(dy), h2, None, f64(dh))
+    b = bounds(f64(x), f64(g), "sigmoid", h2, f64(dy), f64(dh))
+    close(xs.grad, dx, b["dx"], F32, "dx")
+    close(gs.grad, dg, b["dg"], F32, "dg")
+    close(h0.grad, dh0.sum(0, keepdims=True), b["dh0"].sum(0, keepdims=True), F32, "dh0")
+
+    def loss(a):
+        y, last, _ = R.gated_scan(*a[:2], "sigmoid", a[2])
+        return (y * f64(dy)).sum() + (last * f64(dh)).sum()
+
+    rng = np.random.default_rng(18)
+    way = [rng.standard_normal(t.shape) for t in (dx, dg, dh0)]
+    base = [f64(x), f64(g), h2]
+    step = 1e-5
+    diff = (loss([p + step * w for p, w in zip(base, way)]) -
+            loss([p - step * w for p, w in zip(base, way)])) / (2 * step)
+    got = sum((f64(p) * w).sum() for p, w in ((xs.grad, way[0]), (gs.grad, way[1])))
+    got += (dh0 * way[2]).sum()
+    room = sum((np.abs(w) * (b[n] + E * np.abs(v))).sum()
+               for w, n, v in ((way[0], "dx", dx), (way[1], "dg", dg)))
+    assert abs(got - diff) <= room + 1e-6 * abs(diff)
+
+
+def test_autograd_with_one_of_the_outputs_only():
+    x, g, dy, h, dh = (t.to(dev()) for t in make(2, 66, 16, F32, "log", 19))
+    xs = x.clone().requires_grad_()
+    _, last = S.GatedScan.apply(xs, g)
+    last.sum().backward()
+    a = xs.grad.clone()
+    xs.grad = None
+    y, _ = S.GatedScan.apply(xs, g)
+    y[:, -1].sum().backward()
+    assert torch.equal(a, xs.grad)
+    with pytest.raises(RuntimeError):
+        y, _ = S.GatedScan.apply(xs, g)
+        d, = torch.autograd.grad(y.sum(), xs, create_graph=True)
+        d.sum().backward()
+
+
+def test_captured_training_step_replays_with_new_inputs():
+    """Forward and backward in one graph, on its own stream, replayed on other data."""
+    x, g, dy, h, dh = (t.to(dev()) for t in make(2, 400, 130, BF16, "log", 20))
+    xs, gs, ds = x.clone(), g.clone(), dy.clone()
+
+    def step():
+        y, last, marks = S.sanatan_gated_scan_fwd(xs, gs, h0=h, want_state=True, want_marks=True)
+        gr = S.sanatan_gated_scan_bwd(xs, gs, ds, marks, want_dh0=True)
+        return y, last, gr["dx"], gr["dg"], gr["dh0"]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    x2, g2, dy2, _, _ = (t.to(dev()) for t in make(2, 400, 130, BF16, "log", 21))
+    for to, new in ((xs, x2), (gs, g2), (ds, dy2)):
+        to.copy_(new)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = step()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_two_streams_at_once():
+    a = [t.to(dev()) for t in make(2, 3000, 96, F32, "log", 22)]
+    b = [t.to(dev()) for t in make(3, 2500, 64, F32, "sigmoid", 23)]
+    ya, _, _ = S.sanatan_gated_scan_fwd(a[0], a[1], "log", h0=a[3])
+    yb, _, _ = S.sanatan_gated_scan_fwd(b[0], b[1], "sigmoid", h0=b[3])
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(one):
+            y1, _, _ = S.sanatan_gated_scan_fwd(a[0], a[1], "log", h0=a[3])
+        with torch.cuda.stream(two):
+            y2, _, _ = S.sanatan_gated_scan_fwd(b[0], b[1], "sigmoid", h0=b[3])
+    torch.cuda.synchronize()
+    assert torch.equal(ya, y1) and torch.equal(yb, y2)
+
+
+def test_refusals_of_the_binding():
+    x = torch.zeros(2, 8, 4, device=dev())
+    h = torch.zeros(2, 4, device=dev())
+    for bad in (dict(g=x[:, :7]), dict(g=x.to(BF16)), dict(g=x.transpose(0, 1)),
+                dict(g=x, h0=h[:1]), dict(g=x, h0=h.to(BF16)), dict(g=x, gate="relu"),
+                dict(g=x, lens=torch.zeros(3, dtype=torch.int64, device=dev())),
+                dict(g=x, lens=torch.zeros(2, dtype=torch.int32, device=dev())),
+                dict(g=x.cpu()), dict(g=x, out=x.to(BF16)), dict(g=x, h_out=h[:, :2])):
+        with pytest.raises(ValueError):
+            S.sanatan_gated_scan_fwd(x, **bad)
+    with pytest.raises(ValueError):
+        S.sanatan_gated_scan_fwd(x[0], x[0])
+    with pytest.raises(ValueError):
+        S.sanatan_gated_scan_fwd(x.half(), x.half())
+    with pytest.raises(S.SanatanError) as e:        # rows of 5 floats: the second is misaligned
+        odd = torch.zeros(3, 1, 5, device=dev())
+        S.sanatan_gated_scan_fwd(odd[1:], odd[1:])
+    assert e.value.status == 1
+    with pytest.raises(ValueError):
+        S.sanatan_gated_scan_bwd(x, x, x, torch.zeros(2, 2, 4, device=dev()))
+    with pytest.raises(ValueError):
+        S.sanatan_gated_scan_step(h.to(BF16), h, h)
+    with pytest.raises(ValueError):
+        S.sanatan_gated_scan_step(x, x, x)
