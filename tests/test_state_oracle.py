@@ -139,7 +139,7 @@ def test_scan_refusals(lib):
     assert fwd(B=-1) == 1 and fwd(T=-1) == 1 and fwd(D=-1) == 1
     assert fwd(x=None) == 1 and fwd(g=P(24)) == 1 and fwd(y=None) == 1
     assert fwd(lens=P(8)) == 1 and fwd(h0=P(4)) == 1 and fwd(h=P(8)) == 1 and fwd(m=P(8)) == 1
-    assert fwd(B=1 << 20, D=1 << 11) == 2
+    assert fwd(B=1 << 20, D=1 << 11) == 2 and fwd(T=(1 << 30) + 1) == 2
     assert fwd(B=0) == 0 and fwd(D=0) == 0 and fwd(T=0, x=None, g=None, y=None) == 0
 
     def bwd(x=ok, dy=ok, dt=1, gate=1, B=2, T=3, D=4, m=ok, dh=None, dx=ok, dg=ok, dh0=None):
