@@ -11,13 +11,13 @@
 // A stretch of tokens is the affine map h -> A h + H of the state before it
 // (A the product of its decays, H its result from a zero state), and maps
 // compose: (A1, H1) then (A2, H2) is (A1 A2, A2 H1 + H2).  So every tensor is
-// read once: a cluster of CTAs walks the tokens of 64 channels of a sequence, in
-// every step each CTA takes the next tile, each half-warp kRun consecutive tokens
-// of it (a lane four channels), and the maps meet in registers, shared memory and,
+// read once: a cluster of CTAs walks the tokens of 64 or 32 channels of a
+// sequence, in every step each CTA takes the next tile, 16 or 8 lanes four
+// consecutive tokens of it (a lane four channels), and the maps meet in registers, shared memory and,
 // across the cluster, distributed shared memory, always in the same order (the
 // same call gives the same bits).  One cluster barrier a step; tiles of later
 // steps are on their way meanwhile (cp.async into a ring that each thread fills
-// and reads for itself).
+// and reads for itself).  Arithmetic is packed, two channels an instruction.
 //
 // The backward needs h_{t-1}: the forward leaves the state before every 64th
 // token (a mark, 1/64 of the elements in float32), from which a tile's states are
@@ -26,34 +26,89 @@
 // from later tokens is (A, P) with the same A.
 #include <cooperative_groups.h>
 
+#include "f32x2.cuh"
 #include "sanatan_internal.h"
 #include "sanatan_math.cuh"
+#include "tc_ptx.cuh"
 
 namespace sanatan {
 namespace {
 
 namespace cg = cooperative_groups;
+using namespace f2;
 
 constexpr int kMark = kScanMark;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRuns = kThreads / 16;  // half-warps
-constexpr int kChannels = 64;         // of a CTA: 16 lanes x 4
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+constexpr int R = 4;  // consecutive tokens of a thread
 
-// a and 1 - a of a gate value; the sigmoid's two sides come from exp(-|g|), so
-// neither overflows nor loses digits next to 1.
+// Four channels as two packed pairs.
+struct V4 {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ V4 v4(float a, float b, float c, float d) { return {pk2(a, b), pk2(c, d)}; }
+__device__ __forceinline__ V4 v4(float a) { return v4(a, a, a, a); }
+__device__ __forceinline__ V4 mul(const V4& a, const V4& b) {
+  return {fmul2(a.lo, b.lo), fmul2(a.hi, b.hi)};
+}
+__device__ __forceinline__ V4 fma(const V4& a, const V4& b, const V4& c) {
+  return {ffma2(a.lo, b.lo, c.lo), ffma2(a.hi, b.hi, c.hi)};
+}
+__device__ __forceinline__ V4 sub(const V4& a, const V4& b) {
+  return {fsub2(a.lo, b.lo), fsub2(a.hi, b.hi)};
+}
+__device__ __forceinline__ V4 select(bool first, const V4& a, const V4& b) {
+  return {first ? a.lo : b.lo, first ? a.hi : b.hi};
+}
+__device__ __forceinline__ void get(const V4& v, float (&f)[4]) {
+  upk2(v.lo, f[0], f[1]);
+  upk2(v.hi, f[2], f[3]);
+}
+__device__ __forceinline__ V4 shfl_xor(const V4& v, int mask) {
+  float f[4];
+  get(v, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = __shfl_xor_sync(0xffffffffu, f[j], mask);
+  return v4(f[0], f[1], f[2], f[3]);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// a and 1 - a of four gate values.  The hardware's powers of two are as near
+// as expf while |g| < 1 (mean error -0.3 to 0.2, r.m.s. 0.7 steps of 2^-24 either
+// way, so that long memories keep their digits); beyond, the rounded argument
+// costs |g| steps of a decay that is small.  The sigmoid's sides come from
+// exp(-|g|): neither overflows, and the one next to 1 is 1 minus the other.
 template <int G>
-__device__ __forceinline__ void gate(float g, float& a, float& keep) {
+__device__ __forceinline__ void gate(const V4& g, V4& a, V4& keep) {
+  float t[4];
+  get(mul(g, v4(kLog2e)), t);
   if (G == SANATAN_GATE_LOG) {
-    a = expf(g);
-    keep = 1.0f;
+    a = v4(ex2(t[0]), ex2(t[1]), ex2(t[2]), ex2(t[3]));
   } else {
-    const float e = expf(-fabsf(g));
-    const float r = 1.0f / (1.0f + e);
-    const float q = e * r;
-    a = g >= 0.0f ? r : q;
-    keep = g >= 0.0f ? q : r;
+    const V4 e = v4(ex2(-fabsf(t[0])), ex2(-fabsf(t[1])), ex2(-fabsf(t[2])), ex2(-fabsf(t[3])));
+    const V4 one = v4(1.0f);
+    float s[4], p[4], q[4];
+    get(fma(e, one, one), s);
+    const V4 small = mul(e, v4(rcp(s[0]), rcp(s[1]), rcp(s[2]), rcp(s[3])));
+    get(small, q);
+    get(sub(one, small), p);
+    a = v4(t[0] >= 0.0f ? p[0] : q[0], t[1] >= 0.0f ? p[1] : q[1], t[2] >= 0.0f ? p[2] : q[2],
+           t[3] >= 0.0f ? p[3] : q[3]);
+    keep = v4(t[0] >= 0.0f ? q[0] : p[0], t[1] >= 0.0f ? q[1] : p[1], t[2] >= 0.0f ? q[2] : p[2],
+              t[3] >= 0.0f ? q[3] : p[3]);
   }
 }
 
@@ -73,29 +128,25 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void unpack(const float4& v, float (&f)[4]) {
-  f[0] = v.x;
-  f[1] = v.y;
-  f[2] = v.z;
-  f[3] = v.w;
-}
-__device__ __forceinline__ void unpack(const uint2& v, float (&f)[4]) {
-  f[0] = __uint_as_float(v.x << 16);
-  f[1] = __uint_as_float(v.x & 0xffff0000u);
-  f[2] = __uint_as_float(v.y << 16);
-  f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
+// Four values of a row in memory.
 template <typename E>
-struct Quad;  // four values of a row
+struct Quad;
 template <>
 struct Quad<float> {
-  using type = float4;
-  __device__ static float4 pack(const float (&f)[4]) { return make_float4(f[0], f[1], f[2], f[3]); }
+  using type = ulonglong2;
+  __device__ __forceinline__ static V4 get(const ulonglong2& v) { return {v.x, v.y}; }
+  __device__ __forceinline__ static ulonglong2 put(const V4& v) { return make_ulonglong2(v.lo, v.hi); }
 };
 template <>
 struct Quad<__nv_bfloat16> {
   using type = uint2;
-  __device__ static uint2 pack(const float (&f)[4]) {
+  __device__ __forceinline__ static V4 get(const uint2& v) {
+    return v4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+              __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  }
+  __device__ __forceinline__ static uint2 put(const V4& v) {
+    float f[4];
+    sanatan::get(v, f);
     const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(f[2], f[3]);
     return make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
@@ -103,59 +154,85 @@ struct Quad<__nv_bfloat16> {
   }
 };
 
-// Where a thread's four channels are.  VEC (D a multiple of 4): four neighbours,
-// one load or store a row.  Otherwise rows start at any element: channels 16
-// apart, so that the 16 lanes of a load are neighbours.
-template <bool VEC>
-__device__ __forceinline__ int channel(int c0, int lane, int j) {
-  return VEC ? c0 + 4 * lane + j : c0 + lane + 16 * j;
-}
-
-template <typename E, bool VEC>
-__device__ __forceinline__ void store_row(E* row, int c0, int lane, int D, const float (&f)[4]) {
-  if (VEC) {
-    if (channel<VEC>(c0, lane, 0) < D)
-      *reinterpret_cast<typename Quad<E>::type*>(row + channel<VEC>(c0, lane, 0)) =
-          Quad<E>::pack(f);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (channel<VEC>(c0, lane, j) < D)
-        row[channel<VEC>(c0, lane, j)] = store_from_float<E>(f[j]);
+// A thread's four channels of the CTA's 4 * LANES.  VEC (D a multiple of 4): four
+// neighbours, one load or store a row.  Otherwise rows start at any element:
+// channels LANES apart, so that the lanes of a load are neighbours.
+template <int LANES, bool VEC>
+struct Place {
+  int c0, lane, D;
+  __device__ __forceinline__ int channel(int j) const {
+    return VEC ? c0 + 4 * lane + j : c0 + lane + LANES * j;
   }
-}
+  __device__ __forceinline__ bool there(int j) const { return channel(j) < D; }
+  template <typename E>
+  __device__ __forceinline__ void store(E* row, const V4& v) const {
+    if (VEC) {
+      if (there(0)) *reinterpret_cast<typename Quad<E>::type*>(row + channel(0)) = Quad<E>::put(v);
+    } else {
+      float f[4];
+      get(v, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (there(j)) row[channel(j)] = store_from_float<E>(f[j]);
+    }
+  }
+};
 
-__device__ __forceinline__ float4 f4(const float (&f)[4]) {
-  return make_float4(f[0], f[1], f[2], f[3]);
-}
+// The same channels in pairs, pair < 2 * LANES, for the lanes of warp 0 (with 8
+// LANES its upper half does what the lower one does).
+template <int LANES, bool VEC>
+struct PairPlace {
+  int c[2];
+  bool ok[2];
+  __device__ __forceinline__ PairPlace(int c0, int pair, int D) {
+    const Place<LANES, VEC> p{c0, pair / 2, D};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[i] = p.channel(pair % 2 * 2 + i);
+      ok[i] = c[i] < D;
+    }
+  }
+  __device__ __forceinline__ uint64_t load(const float* row) const {  // zeros for null
+    return pk2(row != nullptr && ok[0] ? row[c[0]] : 0.0f,
+               row != nullptr && ok[1] ? row[c[1]] : 0.0f);
+  }
+  __device__ __forceinline__ void store(float* row, uint64_t v) const {
+    float a, b;
+    upk2(v, a, b);
+    if (ok[0]) row[c[0]] = a;
+    if (ok[1]) row[c[1]] = b;
+  }
+};
 
-// The tensors' tiles on their way.  VEC: a ring of kStages tiles in shared memory,
+// The tensors' tiles on their way.  VEC: a ring of STAGES tiles in shared memory,
 // in which every thread has its own places (no barrier).  Otherwise the next tile
 // waits in registers.
-template <typename E, bool VEC, int NT, int R, int STAGES>
+template <typename E, int LANES, bool VEC, int NT, int STAGES>
 struct Tiles {
   using Q = typename Quad<E>::type;
   static constexpr int kBytes = VEC ? STAGES * NT * R * kThreads * static_cast<int>(sizeof(Q)) : 0;
-  const E* src[NT];
-  int64_t base;  // element of token 0, channel of lane and j = 0
-  int c0, lane, D, len, tid;
-  uint32_t ring;
-  Q* ring_ptr;
+  const E* src[NT];  // the thread's first channel of token 0
+  int64_t D;
+  int len;
+  uint32_t at;       // the thread's first place in the ring
+  const Q* places;
+  Place<LANES, VEC> place;
   E next[VEC ? 1 : NT][VEC ? 1 : R][4];
 
-  // Loads of tile `k` of this thread (tokens t0 ...; those from len on are not there).
+  // Loads the thread's tokens t0 ... of a tile; those from len on are not there.
   __device__ __forceinline__ void issue(int t0, int slot) {
     if constexpr (VEC) {
-      if (channel<VEC>(c0, lane, 0) < D) {
+      if (place.there(0)) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT; ++i) {
+          const E* from = src[i] + static_cast<int64_t>(t0) * D;
+          const uint32_t to = at + static_cast<uint32_t>((slot * NT + i) * R * kThreads *
+                                                         static_cast<int>(sizeof(Q)));
 #pragma unroll
           for (int r = 0; r < R; ++r)
             if (t0 + r < len)
-              cp_async<sizeof(Q)>(
-                  ring + static_cast<uint32_t>((((slot * NT + i) * R + r) * kThreads + tid) *
-                                               static_cast<int>(sizeof(Q))),
-                  src[i] + base + static_cast<int64_t>(t0 + r) * D);
+              cp_async<sizeof(Q)>(to + r * kThreads * static_cast<int>(sizeof(Q)), from + r * D);
+        }
       }
       cp_commit();
     } else {
@@ -165,244 +242,330 @@ struct Tiles {
         for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            next[i][r][j] = t0 + r < len && channel<VEC>(c0, lane, j) < D
-                                ? src[i][base + static_cast<int64_t>(t0 + r) * D + 16 * j]
+            next[i][r][j] = t0 + r < len && place.there(j)
+                                ? src[i][(static_cast<int64_t>(t0) + r) * D + LANES * j]
                                 : store_from_float<E>(0.0f);
     }
   }
-  __device__ __forceinline__ void get(int i, int r, int slot, float (&f)[4]) const {
-    if constexpr (VEC) {
-      unpack(ring_ptr[((slot * NT + i) * R + r) * kThreads + tid], f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = load_as_float(&next[i][r][j]);
-    }
+  __device__ __forceinline__ V4 get(int i, int r, int slot) const {
+    if constexpr (VEC)
+      return Quad<E>::get(places[((slot * NT + i) * R + r) * kThreads]);
+    else
+      return v4(load_as_float(&next[i][r][0]), load_as_float(&next[i][r][1]),
+                load_as_float(&next[i][r][2]), load_as_float(&next[i][r][3]));
   }
 };
 
-template <typename E>
-constexpr int kRunFwd = sizeof(E) == 2 ? 8 : 4;  // tokens of a half-warp's run
-constexpr int kStagesFwd = 3;
+__device__ __forceinline__ uint64_t* pairs(V4* v) { return &v->lo; }
 
-// One step's exchange: the maps of a CTA's tile, and of all tiles of the cluster.
-struct Shared {
-  float4 a[kWarps][16];
-  float4 h[kWarps][16];
-  float4 p[kWarps][16];
-  float4 all_a[2][kMaxCluster][16];  // by parity of the step
-  float4 all_h[2][kMaxCluster][16];
+// One step's exchange.  Channel pairs: lane l of a run has the pairs 2 l and 2 l + 1
+// (V4 rows read as pairs).
+template <int LANES>
+struct Exchange {
+  V4 a[kWarps][LANES];   // the maps of the CTA's warps
+  V4 h[kWarps][LANES];
+  V4 p[kWarps][LANES];   // backward: in reverse time
+  V4 in[kWarps][LANES];  // what comes into each warp
+  V4 in_p[kWarps][LANES];
+  ulonglong2 all[2][kMaxCluster][2 * LANES];  // (A, H) of the cluster's CTAs, by the step's parity
+  uint64_t full[2];      // mbarriers: all of a step's maps have come
 };
 
-// then: the map (a, h) after the map (pa, ph).
-__device__ __forceinline__ void then(float (&pa)[4], float (&ph)[4], const float4& a,
-                                     const float4& h) {
-  float fa[4], fh[4];
-  unpack(a, fa);
-  unpack(h, fh);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    ph[j] = fmaf(fa[j], ph[j], fh[j]);
-    pa[j] *= fa[j];
+__device__ int g_scan_error;  // a bounded wait gave up
+
+// Wait for a phase of `bar` that other CTAs of the cluster complete with st.async;
+// false after about two seconds.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = tc::smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(at), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (n == 0) t0 = tc::globaltimer_ns();
+    if (n % 64 == 63 && tc::globaltimer_ns() - t0 > 2000000000ull) return false;
   }
 }
 
-template <typename E, int G, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs p, int blocks,
+// Phase `bar` completes once `bytes` have come.  Relaxed: nothing the thread did
+// before has to be seen by anyone (a release would wait for its global stores).
+__device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(
+          tc::smem_u32(bar)),
+      "r"(bytes)
+      : "memory");
+}
+
+// The cluster's side of the recurrence, by warp 0, lane = channel pair.  A step:
+// share() sends the CTA's map to every CTA of the cluster (st.async, counted by
+// the receiver's mbarrier; a cluster barrier instead would make every thread wait
+// for its own global stores), arrive() waits for all of them and takes carry over
+// them.  Buffers alternate: who sends step s + 2 has received step s + 1 from
+// every CTA, and they sent that after reading step s.
+template <int LANES>
+struct Cluster {
+  Exchange<LANES>& ex;
+  int rank, size, steps, pair;
+  bool dead = false;
+
+  __device__ __forceinline__ uint32_t bytes() const { return size * 2 * LANES * 16; }
+  __device__ __forceinline__ void start() {  // all threads
+    if (size == 1) return;
+    if (threadIdx.x == 0) {
+      tc::mbar_init(&ex.full[0], 1);
+      tc::mbar_init(&ex.full[1], 1);
+      tc::fence_mbar_init();
+      expect(&ex.full[0], bytes());
+      expect(&ex.full[1], bytes());
+    }
+    cg::this_cluster().sync();
+  }
+  __device__ __forceinline__ void share(int s, uint64_t A, uint64_t H) {
+    if (threadIdx.x >= 2 * LANES) return;
+    const uint32_t at = tc::smem_u32(&ex.all[s & 1][rank][pair]), bar = tc::smem_u32(&ex.full[s & 1]);
+    for (int r = 0; r < size; ++r) {
+      uint32_t to, to_bar;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(r));
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to_bar) : "r"(bar), "r"(r));
+      asm volatile(
+          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::
+              "r"(to),
+          "l"(A), "l"(H), "r"(to_bar)
+          : "memory");
+    }
+  }
+  // Returns what comes into this CTA's tile.
+  __device__ __forceinline__ uint64_t arrive(int s, uint64_t& carry) {
+    if (!dead && !wait_cluster(&ex.full[s & 1], (s >> 1) & 1)) {
+      dead = true;
+      g_scan_error = 1;
+    }
+    uint64_t in = carry;
+    for (int r = 0; r < size; ++r) {
+      const ulonglong2 m = ex.all[s & 1][r][pair];
+      if (r == rank) in = carry;
+      carry = ffma2(m.x, carry, m.y);
+    }
+    __syncwarp();
+    if (threadIdx.x == 0 && s + 2 < steps) expect(&ex.full[s & 1], bytes());
+    return in;
+  }
+  // No CTA leaves while another may still send to it.
+  __device__ __forceinline__ void finish() {
+    if (size == 1) return;
+    if (dead) __nanosleep(1000000);
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+  }
+};
+
+// The maps of the 32 / LANES runs of a warp: (wA, wH) all of them in order, (bA,
+// bH) those before the thread's own.  Forward in time, or backward.
+template <int LANES, bool REVERSE>
+__device__ __forceinline__ void warp_scan(int tid, const V4& A, const V4& H, V4& bA, V4& bH, V4& wA,
+                                          V4& wH) {
+  bA = v4(1.0f);
+  bH = v4(0.0f);
+  wA = A;
+  wH = H;
+#pragma unroll
+  for (int off = LANES; off < 32; off *= 2) {
+    const V4 oA = shfl_xor(wA, off), oH = shfl_xor(wH, off);
+    const bool second = ((tid & off) != 0) != REVERSE;  // the other half comes before
+    const V4 nH = second ? fma(wA, oH, wH) : fma(oA, wH, oH);
+    if (second) {
+      bH = fma(bA, oH, bH);
+      bA = mul(bA, oA);
+    }
+    wH = nH;
+    wA = mul(wA, oA);
+  }
+}
+
+template <typename E, int LANES>
+constexpr int kStagesFwd = sizeof(E) == 2 ? 3 : 2;
+
+template <typename E, int G, int LANES, bool VEC>
+__global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs p, int blocks,
                                                                int cluster_size) {
-  constexpr int R = kRunFwd<E>;
-  constexpr int kTile = kRuns * R;
-  using Ring = Tiles<E, VEC, 2, R, kStagesFwd>;
+  constexpr int kTile = kThreads / LANES * R;
+  constexpr int kStages = kStagesFwd<E, LANES>;
+  using Ring = Tiles<E, LANES, VEC, 2, kStages>;
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ Shared sh;
-  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ __align__(16) Exchange<LANES> ex;
 
   const int rank = static_cast<int>(blockIdx.x % cluster_size);
   const int unit = static_cast<int>(blockIdx.x / cluster_size);
   const int b = unit / blocks;
-  const int tid = threadIdx.x, lane = tid & 15, warp = tid >> 5;
-  const bool upper = (tid & 16) != 0;
+  const int tid = threadIdx.x, lane = tid % LANES, warp = tid >> 5;
   const int T = p.T, D = p.D;
-  const int c0 = (unit % blocks) * kChannels;
+  const Place<LANES, VEC> place{(unit % blocks) * 4 * LANES, lane, D};
   const int len = length_of(p.lens, b, T);
-  const int run = (tid >> 4) * R;  // first token of this half-warp's run in a tile
   const int tiles = (T + kTile - 1) / kTile;
   const int steps = (tiles + cluster_size - 1) / cluster_size;
 
   Ring in;
-  in.src[0] = static_cast<const E*>(p.g);
-  in.src[1] = static_cast<const E*>(p.x);
-  in.base = static_cast<int64_t>(b) * T * D + channel<VEC>(c0, lane, 0);
-  in.c0 = c0;
-  in.lane = lane;
+  const int64_t base = static_cast<int64_t>(b) * T * D + place.channel(0);
+  in.src[0] = static_cast<const E*>(p.g) + base;
+  in.src[1] = static_cast<const E*>(p.x) + base;
   in.D = D;
   in.len = len;
-  in.tid = tid;
-  in.ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  in.ring_ptr = reinterpret_cast<typename Ring::Q*>(ring);
+  in.at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+          tid * static_cast<int>(sizeof(typename Ring::Q));
+  in.places = reinterpret_cast<const typename Ring::Q*>(ring) + tid;
+  in.place = place;
   E* y = static_cast<E*>(p.y) + static_cast<int64_t>(b) * T * D;
-  const int marks_of = (T + kMark - 1) / kMark;
 
-  float carry[4];  // the state before the step's first tile
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = channel<VEC>(c0, lane, j);
-    carry[j] = p.h0 != nullptr && c < D ? p.h0[static_cast<int64_t>(b) * D + c] : 0.0f;
-  }
-
-  const int stride = cluster_size * kTile;
-  const int64_t first = static_cast<int64_t>(rank) * kTile + run;
-  // Token of step s; steps past the last one load nothing.
+  const int64_t first = static_cast<int64_t>(rank) * kTile + tid / LANES * R;
+  // The thread's first token in step s; T past the last step.
   auto token = [&](int s) {
-    const int64_t t = first + static_cast<int64_t>(s) * stride;
+    const int64_t t = first + static_cast<int64_t>(s) * cluster_size * kTile;
     return t < T ? static_cast<int>(t) : T;
   };
   if constexpr (VEC) {
 #pragma unroll
-    for (int s = 0; s < kStagesFwd - 1; ++s) in.issue(token(s), s);
+    for (int s = 0; s < kStages - 1; ++s) in.issue(token(s), s);
   } else {
     in.issue(token(0), 0);
   }
+  // Warp 0: the state before the step's first tile.
+  const int at = tid % (2 * LANES);
+  const PairPlace<LANES, VEC> pair(place.c0, at, D);
+  uint64_t carry = pair.load(p.h0 == nullptr ? nullptr : p.h0 + static_cast<int64_t>(b) * D);
+  Cluster<LANES> cluster{ex, rank, cluster_size, steps, at};
+  cluster.start();
 
   int slot = 0;
   for (int s = 0; s < steps; ++s) {
     const int t0 = token(s);
     if constexpr (VEC) {
-      in.issue(token(s + kStagesFwd - 1), slot == 0 ? kStagesFwd - 1 : slot - 1);
-      cp_wait<kStagesFwd - 1>();
+      in.issue(token(s + kStages - 1), slot == 0 ? kStages - 1 : slot - 1);
+      cp_wait<kStages - 1>();
     }
     // The run's decays and inputs, and its map.
-    float a[R][4], u[R][4], A[4] = {1.0f, 1.0f, 1.0f, 1.0f}, H[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    V4 a[R], u[R], A, H;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float g[4], x[4];
-      in.get(0, r, slot, g);
-      in.get(1, r, slot, x);
-      const bool there = t0 + r < len;
+      V4 keep;
+      gate<G>(in.get(0, r, slot), a[r], keep);
+      u[r] = in.get(1, r, slot);
+      if (G == SANATAN_GATE_SIGMOID) u[r] = mul(keep, u[r]);
+    }
+    if (t0 + R > len) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float keep;
-        gate<G>(g[j], a[r][j], keep);
-        u[r][j] = G == SANATAN_GATE_LOG ? x[j] : keep * x[j];
-        if (!there) {
-          a[r][j] = 1.0f;
-          u[r][j] = 0.0f;
-        }
-        H[j] = fmaf(a[r][j], H[j], u[r][j]);
-        A[j] *= a[r][j];
+      for (int r = 0; r < R; ++r) {
+        a[r] = select(t0 + r < len, a[r], v4(1.0f));
+        u[r] = select(t0 + r < len, u[r], v4(0.0f));
       }
+    }
+    A = a[0];
+    H = u[0];
+#pragma unroll
+    for (int r = 1; r < R; ++r) {
+      H = fma(a[r], H, u[r]);
+      A = mul(a[r], A);
     }
     if constexpr (!VEC) in.issue(token(s + 1), 0);
-    // The two runs of the warp, then the warps of the CTA.
-    float oA[4], oH[4], wA[4], wH[4];  // the other run's map; the warp's
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      oA[j] = __shfl_xor_sync(0xffffffffu, A[j], 16);
-      oH[j] = __shfl_xor_sync(0xffffffffu, H[j], 16);
-      wA[j] = A[j] * oA[j];
-      wH[j] = upper ? fmaf(A[j], oH[j], H[j]) : fmaf(oA[j], H[j], oH[j]);
-    }
-    if (!upper) {
-      sh.a[warp][lane] = f4(wA);
-      sh.h[warp][lane] = f4(wH);
+    // The runs of the warp, the warps of the CTA, the CTAs of the cluster.
+    V4 bA, bH, wA, wH;
+    warp_scan<LANES, false>(tid, A, H, bA, bH, wA, wH);
+    if ((tid & 31) < LANES) {
+      ex.a[warp][lane] = wA;
+      ex.h[warp][lane] = wH;
     }
     __syncthreads();
-    float pA[4] = {1.0f, 1.0f, 1.0f, 1.0f}, pH[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int w = 0; w < warp; ++w) then(pA, pH, sh.a[w][lane], sh.h[w][lane]);
-    if (warp == kWarps - 1) {  // the CTA's map, to every CTA of the cluster
-      float tA[4], tH[4];
+    if (warp == 0) {
+      uint64_t h = carry;
+      if (cluster_size > 1) {
+        uint64_t tA = pk2(1.0f, 1.0f), tH = pk2(0.0f, 0.0f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        tA[j] = pA[j] * wA[j];
-        tH[j] = fmaf(wA[j], pH[j], wH[j]);
+        for (int w = 0; w < kWarps; ++w) {
+          const uint64_t fa = pairs(ex.a[w])[at];
+          tH = ffma2(fa, tH, pairs(ex.h[w])[at]);
+          tA = fmul2(fa, tA);
+        }
+        cluster.share(s, tA, tH);
+        h = cluster.arrive(s, carry);
       }
-      for (int r = upper ? 1 : 0; r < cluster_size; r += 2) {
-        *cluster.map_shared_rank(&sh.all_a[s & 1][rank][lane], r) = f4(tA);
-        *cluster.map_shared_rank(&sh.all_h[s & 1][rank][lane], r) = f4(tH);
-      }
-    }
-    cluster.sync();
-    // The state before this CTA's tile, and after the step's last.
-    float h[4] = {carry[0], carry[1], carry[2], carry[3]};
-    for (int r = 0; r < cluster_size; ++r) {
-      float fa[4], fh[4];
-      unpack(sh.all_a[s & 1][r][lane], fa);
-      unpack(sh.all_h[s & 1][r][lane], fh);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (r == rank) h[j] = carry[j];
-        carry[j] = fmaf(fa[j], carry[j], fh[j]);
+      for (int w = 0; w < kWarps; ++w) {
+        pairs(ex.in[w])[at] = h;
+        h = ffma2(pairs(ex.a[w])[at], h, pairs(ex.h[w])[at]);
       }
+      if (cluster_size == 1) carry = h;
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[j] = fmaf(pA[j], h[j], pH[j]);
-      if (upper) h[j] = fmaf(oA[j], h[j], oH[j]);
-    }
+    __syncthreads();
+    V4 h = fma(bA, ex.in[warp][lane], bH);
     if (p.marks != nullptr && t0 % kMark == 0 && t0 < T)
-      store_row<float, VEC>(
-          p.marks + (static_cast<int64_t>(b) * marks_of + t0 / kMark) * D, c0, lane, D, h);
+      place.store(p.marks + (static_cast<int64_t>(b) * ((T + kMark - 1) / kMark) + t0 / kMark) * D,
+                  h);
+    E* row = y + static_cast<int64_t>(t0) * D;
+    if (t0 + R <= len) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float out[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = fmaf(a[r][j], h[j], u[r][j]);
-        out[j] = t0 + r < len ? h[j] : 0.0f;
+      for (int r = 0; r < R; ++r) {
+        h = fma(a[r], h, u[r]);
+        place.store(row + static_cast<int64_t>(r) * D, h);
       }
-      if (t0 + r < T) store_row<E, VEC>(y + static_cast<int64_t>(t0 + r) * D, c0, lane, D, out);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        h = fma(a[r], h, u[r]);
+        if (t0 + r < T)
+          place.store(row + static_cast<int64_t>(r) * D, select(t0 + r < len, h, v4(0.0f)));
+      }
     }
-    slot = slot == kStagesFwd - 1 ? 0 : slot + 1;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
   }
-  if (p.h_out != nullptr && rank == 0 && tid < 16)
-    store_row<float, VEC>(p.h_out + static_cast<int64_t>(b) * D, c0, lane, D, carry);
+  if (p.h_out != nullptr && rank == 0 && warp == 0)
+    pair.store(p.h_out + static_cast<int64_t>(b) * D, carry);
+  cluster.finish();
 }
 
-constexpr int kRunBwd = kMark / kRuns;  // a tile lies between two marks
-constexpr int kStagesBwd = 2;
+template <typename E, int LANES>
+constexpr int kStagesBwd = sizeof(E) == 2 ? 3 : 2;
 
-template <typename E, int G, bool VEC>
+template <typename E, int G, int LANES, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs p, int blocks,
                                                                int cluster_size) {
-  constexpr int R = kRunBwd;
-  constexpr int kTile = kRuns * R;
-  using Ring = Tiles<E, VEC, 3, R, kStagesBwd>;
+  constexpr int kTile = kThreads / LANES * R;  // starts at a mark
+  static_assert(kTile % kMark == 0, "tile");
+  constexpr int kStages = kStagesBwd<E, LANES>;
+  using Ring = Tiles<E, LANES, VEC, 3, kStages>;
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ Shared sh;
-  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ __align__(16) Exchange<LANES> ex;
 
   const int rank = static_cast<int>(blockIdx.x % cluster_size);
   const int unit = static_cast<int>(blockIdx.x / cluster_size);
   const int b = unit / blocks;
-  const int tid = threadIdx.x, lane = tid & 15, warp = tid >> 5;
-  const bool upper = (tid & 16) != 0;
+  const int tid = threadIdx.x, lane = tid % LANES, warp = tid >> 5;
   const int T = p.T, D = p.D;
-  const int c0 = (unit % blocks) * kChannels;
+  const Place<LANES, VEC> place{(unit % blocks) * 4 * LANES, lane, D};
   const int len = length_of(p.lens, b, T);
-  const int run = (tid >> 4) * R;
   const int tiles = (T + kTile - 1) / kTile;
   const int steps = (tiles + cluster_size - 1) / cluster_size;
 
   Ring in;
-  in.src[0] = static_cast<const E*>(p.g);
-  in.src[1] = static_cast<const E*>(p.x);
-  in.src[2] = static_cast<const E*>(p.dy);
-  in.base = static_cast<int64_t>(b) * T * D + channel<VEC>(c0, lane, 0);
-  in.c0 = c0;
-  in.lane = lane;
+  const int64_t base = static_cast<int64_t>(b) * T * D + place.channel(0);
+  in.src[0] = static_cast<const E*>(p.g) + base;
+  in.src[1] = static_cast<const E*>(p.x) + base;
+  in.src[2] = static_cast<const E*>(p.dy) + base;
   in.D = D;
   in.len = len;
-  in.tid = tid;
-  in.ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  in.ring_ptr = reinterpret_cast<typename Ring::Q*>(ring);
+  in.at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+          tid * static_cast<int>(sizeof(typename Ring::Q));
+  in.places = reinterpret_cast<const typename Ring::Q*>(ring) + tid;
+  in.place = place;
   E* dx = static_cast<E*>(p.dx) + static_cast<int64_t>(b) * T * D;
   E* dg = static_cast<E*>(p.dg) + static_cast<int64_t>(b) * T * D;
-
-  float carry[4];  // gradient that comes into the step's last token from later ones
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = channel<VEC>(c0, lane, j);
-    carry[j] = p.dh_out != nullptr && c < D ? p.dh_out[static_cast<int64_t>(b) * D + c] : 0.0f;
-  }
+  const float* marks = p.marks + static_cast<int64_t>(b) * ((T + kMark - 1) / kMark) * D;
 
   // Tile of step s: rank 0 has the last one, rank 1 the one before it, and so on;
   // -1 past the first.
@@ -412,144 +575,129 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
   };
   auto token = [&](int s) {
     const int k = tile(s);
-    return k < 0 ? T : k * kTile + run;
+    return k < 0 ? T : min(k * kTile + tid / LANES * R, T);
   };
   if constexpr (VEC) {
 #pragma unroll
-    for (int s = 0; s < kStagesBwd - 1; ++s) in.issue(token(s), s);
+    for (int s = 0; s < kStages - 1; ++s) in.issue(token(s), s);
   } else {
     in.issue(token(0), 0);
   }
+  // Warp 0: the gradient that comes into the step's last token from later ones.
+  const int at = tid % (2 * LANES);
+  const PairPlace<LANES, VEC> pair(place.c0, at, D);
+  uint64_t carry = pair.load(p.dh_out == nullptr ? nullptr : p.dh_out + static_cast<int64_t>(b) * D);
+  Cluster<LANES> cluster{ex, rank, cluster_size, steps, at};
+  cluster.start();
+  // Warp 0: the state before the tile of step s, loaded a step ahead.
+  auto mark_of = [&](int s) {
+    const int k = tile(s);
+    return pair.load(k < 0 ? nullptr
+                           : marks + static_cast<int64_t>(k) * (kTile / kMark) *
+                                         static_cast<int64_t>(D));
+  };
+  uint64_t next_mark = warp == 0 ? mark_of(0) : 0;
 
   int slot = 0;
   for (int s = 0; s < steps; ++s) {
-    const int k = tile(s);
     const int t0 = token(s);
-    float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // the state before the tile
-    if (k >= 0) {
-      const float* mark = p.marks + (static_cast<int64_t>(b) * tiles + k) * D;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (channel<VEC>(c0, lane, j) < D) h[j] = mark[channel<VEC>(c0, lane, j)];
-    }
+    uint64_t mark = next_mark;
+    if (warp == 0) next_mark = mark_of(s + 1);
     if constexpr (VEC) {
-      in.issue(token(s + kStagesBwd - 1), slot == 0 ? kStagesBwd - 1 : slot - 1);
-      cp_wait<kStagesBwd - 1>();
+      in.issue(token(s + kStages - 1), slot == 0 ? kStages - 1 : slot - 1);
+      cp_wait<kStages - 1>();
     }
-    float a[R][4], keep[R][4], x[R][4], dy[R][4];
-    float A[4] = {1.0f, 1.0f, 1.0f, 1.0f}, H[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float P[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    V4 a[R], keep[R], x[R], dy[R], A, H, P;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float g[4];
-      in.get(0, r, slot, g);
-      in.get(1, r, slot, x[r]);
-      in.get(2, r, slot, dy[r]);
-      const bool there = t0 + r < len;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        gate<G>(g[j], a[r][j], keep[r][j]);
-        if (!there) {
-          a[r][j] = 1.0f;
-          keep[r][j] = x[r][j] = dy[r][j] = 0.0f;
-        }
-        H[j] = fmaf(a[r][j], H[j], G == SANATAN_GATE_LOG ? x[r][j] : keep[r][j] * x[r][j]);
-        A[j] *= a[r][j];
-      }
+      gate<G>(in.get(0, r, slot), a[r], keep[r]);
+      x[r] = in.get(1, r, slot);
+      dy[r] = in.get(2, r, slot);
     }
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) P[j] = a[r][j] * (P[j] + dy[r][j]);
-    if constexpr (!VEC) in.issue(token(s + 1), 0);
-    float oA[4], oH[4], oP[4], wA[4], wH[4], wP[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      oA[j] = __shfl_xor_sync(0xffffffffu, A[j], 16);
-      oH[j] = __shfl_xor_sync(0xffffffffu, H[j], 16);
-      oP[j] = __shfl_xor_sync(0xffffffffu, P[j], 16);
-      wA[j] = A[j] * oA[j];
-      wH[j] = upper ? fmaf(A[j], oH[j], H[j]) : fmaf(oA[j], H[j], oH[j]);
-      wP[j] = upper ? fmaf(oA[j], P[j], oP[j]) : fmaf(A[j], oP[j], P[j]);
-    }
-    if (!upper) {
-      sh.a[warp][lane] = f4(wA);
-      sh.h[warp][lane] = f4(wH);
-      sh.p[warp][lane] = f4(wP);
-    }
-    __syncthreads();
-    float pA[4] = {1.0f, 1.0f, 1.0f, 1.0f}, pP[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int w = 0; w < warp; ++w) {  // states: the warps before this one
-      float fa[4], fh[4];
-      unpack(sh.a[w][lane], fa);
-      unpack(sh.h[w][lane], fh);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = fmaf(fa[j], h[j], fh[j]);
-    }
-    for (int w = kWarps - 1; w > warp; --w)  // gradients: the warps after it
-      then(pA, pP, sh.a[w][lane], sh.p[w][lane]);
-    if (warp == 0) {
-      float tA[4], tP[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        tA[j] = pA[j] * wA[j];
-        tP[j] = fmaf(wA[j], pP[j], wP[j]);
-      }
-      for (int r = upper ? 1 : 0; r < cluster_size; r += 2) {
-        *cluster.map_shared_rank(&sh.all_a[s & 1][rank][lane], r) = f4(tA);
-        *cluster.map_shared_rank(&sh.all_h[s & 1][rank][lane], r) = f4(tP);
-      }
-    }
-    cluster.sync();
-    float d[4] = {carry[0], carry[1], carry[2], carry[3]};
-    for (int r = 0; r < cluster_size; ++r) {
-      float fa[4], fp[4];
-      unpack(sh.all_a[s & 1][r][lane], fa);
-      unpack(sh.all_h[s & 1][r][lane], fp);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (r == rank) d[j] = carry[j];
-        carry[j] = fmaf(fa[j], carry[j], fp[j]);
-      }
-    }
-    float before[R][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      d[j] = fmaf(pA[j], d[j], pP[j]);
-      if (!upper) d[j] = fmaf(oA[j], d[j], oP[j]);
-      if (upper) h[j] = fmaf(oA[j], h[j], oH[j]);
+    if (t0 + R > len) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        before[r][j] = h[j];
-        h[j] = fmaf(a[r][j], h[j], G == SANATAN_GATE_LOG ? x[r][j] : keep[r][j] * x[r][j]);
+        a[r] = select(t0 + r < len, a[r], v4(1.0f));
+        if (G == SANATAN_GATE_SIGMOID) keep[r] = select(t0 + r < len, keep[r], v4(0.0f));
+        x[r] = select(t0 + r < len, x[r], v4(0.0f));
+        dy[r] = select(t0 + r < len, dy[r], v4(0.0f));
       }
     }
+    A = v4(1.0f);
+    H = P = v4(0.0f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      H = fma(a[r], H, G == SANATAN_GATE_LOG ? x[r] : mul(keep[r], x[r]));
+      A = mul(a[r], A);
+    }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) P = mul(a[r], fma(P, v4(1.0f), dy[r]));
+    if constexpr (!VEC) in.issue(token(s + 1), 0);
+    V4 bA, bH, wA, wH, rA, rP, wP;
+    warp_scan<LANES, false>(tid, A, H, bA, bH, wA, wH);
+    warp_scan<LANES, true>(tid, A, P, rA, rP, wA, wP);
+    if ((tid & 31) < LANES) {
+      ex.a[warp][lane] = wA;
+      ex.h[warp][lane] = wH;
+      ex.p[warp][lane] = wP;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      uint64_t d = carry;
+      if (cluster_size > 1) {
+        uint64_t tA = pk2(1.0f, 1.0f), tP = pk2(0.0f, 0.0f);
+#pragma unroll
+        for (int w = kWarps - 1; w >= 0; --w) {
+          const uint64_t fa = pairs(ex.a[w])[at];
+          tP = ffma2(fa, tP, pairs(ex.p[w])[at]);
+          tA = fmul2(fa, tA);
+        }
+        cluster.share(s, tA, tP);
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        pairs(ex.in[w])[at] = mark;
+        mark = ffma2(pairs(ex.a[w])[at], mark, pairs(ex.h[w])[at]);
+      }
+      if (cluster_size > 1) d = cluster.arrive(s, carry);
+#pragma unroll
+      for (int w = kWarps - 1; w >= 0; --w) {
+        pairs(ex.in_p[w])[at] = d;
+        d = ffma2(pairs(ex.a[w])[at], d, pairs(ex.p[w])[at]);
+      }
+      if (cluster_size == 1) carry = d;
+    }
+    __syncthreads();
+    V4 h = fma(bA, ex.in[warp][lane], bH);
+    V4 before[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      before[r] = h;
+      h = fma(a[r], h, G == SANATAN_GATE_LOG ? x[r] : mul(keep[r], x[r]));
+    }
+    V4 d = fma(rA, ex.in_p[warp][lane], rP);
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      float ox[4], og[4];
-      const bool there = t0 + r < len;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float dh = dy[r][j] + d[j];
-        d[j] = a[r][j] * dh;
-        if (G == SANATAN_GATE_LOG) {
-          ox[j] = dh;
-          og[j] = d[j] * before[r][j];
-        } else {
-          ox[j] = dh * keep[r][j];
-          og[j] = dh * ((before[r][j] - x[r][j]) * (a[r][j] * keep[r][j]));
-        }
-        if (!there) ox[j] = og[j] = 0.0f;
+      const V4 dh = fma(d, v4(1.0f), dy[r]);
+      d = mul(a[r], dh);
+      V4 ox = dh, og;
+      if (G == SANATAN_GATE_LOG) {
+        og = mul(d, before[r]);
+      } else {
+        ox = mul(dh, keep[r]);
+        og = mul(dh, mul(sub(before[r], x[r]), mul(a[r], keep[r])));
       }
       if (t0 + r < T) {
-        store_row<E, VEC>(dx + static_cast<int64_t>(t0 + r) * D, c0, lane, D, ox);
-        store_row<E, VEC>(dg + static_cast<int64_t>(t0 + r) * D, c0, lane, D, og);
+        const bool there = t0 + r < len;
+        place.store(dx + (static_cast<int64_t>(t0) + r) * D, select(there, ox, v4(0.0f)));
+        place.store(dg + (static_cast<int64_t>(t0) + r) * D, select(there, og, v4(0.0f)));
       }
     }
-    slot = slot == kStagesBwd - 1 ? 0 : slot + 1;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
   }
-  if (p.dh0 != nullptr && rank == 0 && tid < 16)
-    store_row<float, VEC>(p.dh0 + static_cast<int64_t>(b) * D, c0, lane, D, carry);
+  if (p.dh0 != nullptr && rank == 0 && warp == 0)
+    pair.store(p.dh0 + static_cast<int64_t>(b) * D, carry);
+  cluster.finish();
 }
 
 template <typename E, int G>
@@ -559,32 +707,35 @@ __global__ void __launch_bounds__(256) scan_step_kernel(float* __restrict__ h,
                                                         E* __restrict__ y) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n) return;
-  float a, keep;
-  gate<G>(load_as_float(g + i), a, keep);
-  const float v = fmaf(a, h[i], keep * load_as_float(x + i));
-  h[i] = v;
-  y[i] = store_from_float<E>(v);
+  V4 a, keep;
+  gate<G>(v4(load_as_float(g + i)), a, keep);
+  V4 u = v4(load_as_float(x + i));
+  if (G == SANATAN_GATE_SIGMOID) u = mul(keep, u);
+  float v[4];
+  get(fma(a, v4(h[i]), u), v);
+  h[i] = v[0];
+  y[i] = store_from_float<E>(v[0]);
 }
 
-// CTAs of a cluster: enough of them for two on every SM, as far as the sequence
-// has tiles for them.
-int cluster_of(int64_t units, int tiles) {
-  int n = 1;
-  while (n < kMaxCluster && n < tiles && units * n < 2 * 152) n *= 2;
-  return n;
-}
+constexpr int kFill = 2 * 152;  // CTAs that keep every SM busy
 
 template <typename Args>
-cudaError_t launch(void (*kernel)(Args, int, int), const Args& a, int tile, int bytes,
+cudaError_t launch(void (*kernel)(Args, int, int), const Args& a, int lanes, int bytes,
                    cudaStream_t st) {
-  const int blocks = (a.D + kChannels - 1) / kChannels;
+  const int blocks = (a.D + 4 * lanes - 1) / (4 * lanes);
   const int64_t units = static_cast<int64_t>(a.B) * blocks;
-  const int n = cluster_of(units, (a.T + tile - 1) / tile);
-  if (bytes > 0) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-  }
+  const int tile = kThreads / lanes * R, tiles = (a.T + tile - 1) / tile;
+  // CTAs of a cluster: until there are enough, as far as the sequence has tiles
+  int n = 1;
+  while (n < kMaxCluster && n < tiles && units * n < kFill) n *= 2;
+  cudaError_t e = cudaSuccess;
+  if (bytes > 0)
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && n > 8)
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * n));
   cfg.blockDim = dim3(kThreads);
@@ -600,24 +751,34 @@ cudaError_t launch(void (*kernel)(Args, int, int), const Args& a, int tile, int 
   return cudaLaunchKernelEx(&cfg, kernel, a, blocks, n);
 }
 
-template <typename E, int G, bool VEC>
+// Channels of a CTA: 64 (16 lanes), or 32 where 64 leave too few CTAs even with
+// the largest clusters.
+bool narrow(int B, int D) {
+  return static_cast<int64_t>(B) * ((D + 63) / 64) * kMaxCluster < kFill;
+}
+
+template <typename E, int G, int LANES, bool VEC>
 cudaError_t fwd_of(const ScanArgs& a, cudaStream_t st) {
-  return launch<ScanArgs>(scan_fwd_kernel<E, G, VEC>, a, kRuns * kRunFwd<E>,
-                          Tiles<E, VEC, 2, kRunFwd<E>, kStagesFwd>::kBytes, st);
+  return launch<ScanArgs>(scan_fwd_kernel<E, G, LANES, VEC>, a, LANES,
+                          Tiles<E, LANES, VEC, 2, kStagesFwd<E, LANES>>::kBytes, st);
 }
 template <typename E, int G>
 cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
-  return a.D % 4 == 0 ? fwd_of<E, G, true>(a, st) : fwd_of<E, G, false>(a, st);
+  if (narrow(a.B, a.D))
+    return a.D % 4 == 0 ? fwd_of<E, G, 8, true>(a, st) : fwd_of<E, G, 8, false>(a, st);
+  return a.D % 4 == 0 ? fwd_of<E, G, 16, true>(a, st) : fwd_of<E, G, 16, false>(a, st);
 }
 
-template <typename E, int G, bool VEC>
+template <typename E, int G, int LANES, bool VEC>
 cudaError_t bwd_of(const ScanBwdArgs& a, cudaStream_t st) {
-  return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, VEC>, a, kMark,
-                             Tiles<E, VEC, 3, kRunBwd, kStagesBwd>::kBytes, st);
+  return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, LANES, VEC>, a, LANES,
+                             Tiles<E, LANES, VEC, 3, kStagesBwd<E, LANES>>::kBytes, st);
 }
 template <typename E, int G>
 cudaError_t bwd(const ScanBwdArgs& a, cudaStream_t st) {
-  return a.D % 4 == 0 ? bwd_of<E, G, true>(a, st) : bwd_of<E, G, false>(a, st);
+  if (narrow(a.B, a.D))
+    return a.D % 4 == 0 ? bwd_of<E, G, 8, true>(a, st) : bwd_of<E, G, 8, false>(a, st);
+  return a.D % 4 == 0 ? bwd_of<E, G, 16, true>(a, st) : bwd_of<E, G, 16, false>(a, st);
 }
 
 template <typename E, int G>
@@ -628,6 +789,22 @@ cudaError_t step(float* h, const void* x, const void* g, int64_t n, void* y, cud
 }
 
 }  // namespace
+
+int scan_read_and_clear_error(cudaStream_t st) {
+  int h = 0;
+  if (cudaMemcpyFromSymbolAsync(&h, g_scan_error, sizeof(int), 0, cudaMemcpyDeviceToHost, st) !=
+      cudaSuccess)
+    return -1;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return -1;
+  if (h != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbolAsync(g_scan_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st) !=
+        cudaSuccess)
+      return -1;
+    if (cudaStreamSynchronize(st) != cudaSuccess) return -1;
+  }
+  return h;
+}
 
 cudaError_t gated_scan_fwd_launch(const ScanArgs& a, cudaStream_t st) {
   using B16 = __nv_bfloat16;

@@ -244,6 +244,7 @@ struct ScanBwdArgs {
   float* dh0 = nullptr;           // [B, D] or null
 };
 cudaError_t gated_scan_fwd_launch(const ScanArgs& a, cudaStream_t st);
+int scan_read_and_clear_error(cudaStream_t st);
 cudaError_t gated_scan_bwd_launch(const ScanBwdArgs& a, cudaStream_t st);
 cudaError_t gated_scan_step_launch(float* h, const void* x, const void* g, int dtype, int gate,
                                    int64_t n, void* y, cudaStream_t st);
