@@ -41,7 +41,9 @@ constexpr int kMark = kScanMark;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int R = 4;  // consecutive tokens of a thread
+template <typename E>
+constexpr int kRunFwd = sizeof(E) == 2 ? 8 : 4;  // consecutive tokens of a thread
+constexpr int kRunBwd = 4;
 
 // Four channels as two packed pairs.
 struct V4 {
@@ -207,7 +209,7 @@ struct PairPlace {
 // The tensors' tiles on their way.  VEC: a ring of STAGES tiles in shared memory,
 // in which every thread has its own places (no barrier).  Otherwise the next tile
 // waits in registers.
-template <typename E, int LANES, bool VEC, int NT, int STAGES>
+template <typename E, int LANES, bool VEC, int NT, int R, int STAGES>
 struct Tiles {
   using Q = typename Quad<E>::type;
   static constexpr int kBytes = VEC ? STAGES * NT * R * kThreads * static_cast<int>(sizeof(Q)) : 0;
@@ -228,10 +230,16 @@ struct Tiles {
           const E* from = src[i] + static_cast<int64_t>(t0) * D;
           const uint32_t to = at + static_cast<uint32_t>((slot * NT + i) * R * kThreads *
                                                          static_cast<int>(sizeof(Q)));
+          if (t0 + R <= len) {
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (t0 + r < len)
-              cp_async<sizeof(Q)>(to + r * kThreads * static_cast<int>(sizeof(Q)), from + r * D);
+            for (int r = 0; r < R; ++r, from += D)
+              cp_async<sizeof(Q)>(to + r * kThreads * static_cast<int>(sizeof(Q)), from);
+          } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r, from += D)
+              if (t0 + r < len)
+                cp_async<sizeof(Q)>(to + r * kThreads * static_cast<int>(sizeof(Q)), from);
+          }
         }
       }
       cp_commit();
@@ -260,14 +268,13 @@ __device__ __forceinline__ uint64_t* pairs(V4* v) { return &v->lo; }
 
 // One step's exchange.  Channel pairs: lane l of a run has the pairs 2 l and 2 l + 1
 // (V4 rows read as pairs).
-template <int LANES>
+template <int LANES, bool BWD>
 struct Exchange {
   V4 a[kWarps][LANES];   // the maps of the CTA's warps
   V4 h[kWarps][LANES];
-  V4 p[kWarps][LANES];   // backward: in reverse time
   V4 in[kWarps][LANES];  // what comes into each warp
-  V4 in_p[kWarps][LANES];
-  ulonglong2 all[2][kMaxCluster][2 * LANES];  // (A, H) of the cluster's CTAs, by the step's parity
+  V4 p[BWD ? kWarps : 1][LANES];  // the same in reverse time
+  V4 in_p[BWD ? kWarps : 1][LANES];
   uint64_t full[2];      // mbarriers: all of a step's maps have come
 };
 
@@ -310,12 +317,16 @@ __device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes) {
 // for its own global stores), arrive() waits for all of them and takes carry over
 // them.  Buffers alternate: who sends step s + 2 has received step s + 1 from
 // every CTA, and they sent that after reading step s.
-template <int LANES>
+template <int LANES, bool BWD>
 struct Cluster {
-  Exchange<LANES>& ex;
+  Exchange<LANES, BWD>& ex;
+  ulonglong2* all;  // [2][size][2 * LANES]: (A, H) of the cluster's CTAs, by the step's parity
   int rank, size, steps, pair;
   bool dead = false;
 
+  __device__ __forceinline__ ulonglong2* of(int s, int r) const {
+    return all + ((s & 1) * size + r) * 2 * LANES + pair;
+  }
   __device__ __forceinline__ uint32_t bytes() const { return size * 2 * LANES * 16; }
   __device__ __forceinline__ void start() {  // all threads
     if (size == 1) return;
@@ -330,7 +341,7 @@ struct Cluster {
   }
   __device__ __forceinline__ void share(int s, uint64_t A, uint64_t H) {
     if (threadIdx.x >= 2 * LANES) return;
-    const uint32_t at = tc::smem_u32(&ex.all[s & 1][rank][pair]), bar = tc::smem_u32(&ex.full[s & 1]);
+    const uint32_t at = tc::smem_u32(of(s, rank)), bar = tc::smem_u32(&ex.full[s & 1]);
     for (int r = 0; r < size; ++r) {
       uint32_t to, to_bar;
       asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(r));
@@ -350,7 +361,7 @@ struct Cluster {
     }
     uint64_t in = carry;
     for (int r = 0; r < size; ++r) {
-      const ulonglong2 m = ex.all[s & 1][r][pair];
+      const ulonglong2 m = *of(s, r);
       if (r == rank) in = carry;
       carry = ffma2(m.x, carry, m.y);
     }
@@ -391,16 +402,17 @@ __device__ __forceinline__ void warp_scan(int tid, const V4& A, const V4& H, V4&
 }
 
 template <typename E, int LANES>
-constexpr int kStagesFwd = sizeof(E) == 2 ? 3 : 2;
+constexpr int kStagesFwd = 2;
 
 template <typename E, int G, int LANES, bool VEC>
-__global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs p, int blocks,
+__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs p, int blocks,
                                                                int cluster_size) {
+  constexpr int R = kRunFwd<E>;
   constexpr int kTile = kThreads / LANES * R;
   constexpr int kStages = kStagesFwd<E, LANES>;
-  using Ring = Tiles<E, LANES, VEC, 2, kStages>;
+  using Ring = Tiles<E, LANES, VEC, 2, R, kStages>;
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ __align__(16) Exchange<LANES> ex;
+  __shared__ __align__(16) Exchange<LANES, false> ex;
 
   const int rank = static_cast<int>(blockIdx.x % cluster_size);
   const int unit = static_cast<int>(blockIdx.x / cluster_size);
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs p,
   };
   if constexpr (VEC) {
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) in.issue(token(s), s);
+    for (int s = 0; s < kStages; ++s) in.issue(token(s), s);
   } else {
     in.issue(token(0), 0);
   }
@@ -440,16 +452,14 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs p,
   const int at = tid % (2 * LANES);
   const PairPlace<LANES, VEC> pair(place.c0, at, D);
   uint64_t carry = pair.load(p.h0 == nullptr ? nullptr : p.h0 + static_cast<int64_t>(b) * D);
-  Cluster<LANES> cluster{ex, rank, cluster_size, steps, at};
+  Cluster<LANES, false> cluster{ex, reinterpret_cast<ulonglong2*>(ring + Ring::kBytes), rank, cluster_size,
+                          steps, at};
   cluster.start();
 
   int slot = 0;
   for (int s = 0; s < steps; ++s) {
     const int t0 = token(s);
-    if constexpr (VEC) {
-      in.issue(token(s + kStages - 1), slot == 0 ? kStages - 1 : slot - 1);
-      cp_wait<kStages - 1>();
-    }
+    if constexpr (VEC) cp_wait<kStages - 1>();
     // The run's decays and inputs, and its map.
     V4 a[R], u[R], A, H;
 #pragma unroll
@@ -459,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs p,
       u[r] = in.get(1, r, slot);
       if (G == SANATAN_GATE_SIGMOID) u[r] = mul(keep, u[r]);
     }
+    in.issue(token(s + (VEC ? kStages : 1)), slot);
     if (t0 + R > len) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -473,7 +484,6 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs p,
       H = fma(a[r], H, u[r]);
       A = mul(a[r], A);
     }
-    if constexpr (!VEC) in.issue(token(s + 1), 0);
     // The runs of the warp, the warps of the CTA, the CTAs of the cluster.
     V4 bA, bH, wA, wH;
     warp_scan<LANES, false>(tid, A, H, bA, bH, wA, wH);
@@ -510,16 +520,15 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs p,
     E* row = y + static_cast<int64_t>(t0) * D;
     if (t0 + R <= len) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; ++r, row += D) {
         h = fma(a[r], h, u[r]);
-        place.store(row + static_cast<int64_t>(r) * D, h);
+        place.store(row, h);
       }
     } else {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; ++r, row += D) {
         h = fma(a[r], h, u[r]);
-        if (t0 + r < T)
-          place.store(row + static_cast<int64_t>(r) * D, select(t0 + r < len, h, v4(0.0f)));
+        if (t0 + r < T) place.store(row, select(t0 + r < len, h, v4(0.0f)));
       }
     }
     slot = slot == kStages - 1 ? 0 : slot + 1;
@@ -530,17 +539,18 @@ __global__ void __launch_bounds__(kThreads, 3) scan_fwd_kernel(const ScanArgs p,
 }
 
 template <typename E, int LANES>
-constexpr int kStagesBwd = sizeof(E) == 2 ? 3 : 2;
+constexpr int kStagesBwd = 2;
 
 template <typename E, int G, int LANES, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs p, int blocks,
                                                                int cluster_size) {
+  constexpr int R = kRunBwd;
   constexpr int kTile = kThreads / LANES * R;  // starts at a mark
   static_assert(kTile % kMark == 0, "tile");
   constexpr int kStages = kStagesBwd<E, LANES>;
-  using Ring = Tiles<E, LANES, VEC, 3, kStages>;
+  using Ring = Tiles<E, LANES, VEC, 3, R, kStages>;
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ __align__(16) Exchange<LANES> ex;
+  __shared__ __align__(16) Exchange<LANES, true> ex;
 
   const int rank = static_cast<int>(blockIdx.x % cluster_size);
   const int unit = static_cast<int>(blockIdx.x / cluster_size);
@@ -579,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
   };
   if constexpr (VEC) {
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) in.issue(token(s), s);
+    for (int s = 0; s < kStages; ++s) in.issue(token(s), s);
   } else {
     in.issue(token(0), 0);
   }
@@ -587,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
   const int at = tid % (2 * LANES);
   const PairPlace<LANES, VEC> pair(place.c0, at, D);
   uint64_t carry = pair.load(p.dh_out == nullptr ? nullptr : p.dh_out + static_cast<int64_t>(b) * D);
-  Cluster<LANES> cluster{ex, rank, cluster_size, steps, at};
+  Cluster<LANES, true> cluster{ex, reinterpret_cast<ulonglong2*>(ring + Ring::kBytes), rank, cluster_size,
+                          steps, at};
   cluster.start();
   // Warp 0: the state before the tile of step s, loaded a step ahead.
   auto mark_of = [&](int s) {
@@ -603,10 +614,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
     const int t0 = token(s);
     uint64_t mark = next_mark;
     if (warp == 0) next_mark = mark_of(s + 1);
-    if constexpr (VEC) {
-      in.issue(token(s + kStages - 1), slot == 0 ? kStages - 1 : slot - 1);
-      cp_wait<kStages - 1>();
-    }
+    if constexpr (VEC) cp_wait<kStages - 1>();
     V4 a[R], keep[R], x[R], dy[R], A, H, P;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -614,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
       x[r] = in.get(1, r, slot);
       dy[r] = in.get(2, r, slot);
     }
+    in.issue(token(s + (VEC ? kStages : 1)), slot);
     if (t0 + R > len) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -632,7 +641,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
     }
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) P = mul(a[r], fma(P, v4(1.0f), dy[r]));
-    if constexpr (!VEC) in.issue(token(s + 1), 0);
     V4 bA, bH, wA, wH, rA, rP, wP;
     warp_scan<LANES, false>(tid, A, H, bA, bH, wA, wH);
     warp_scan<LANES, true>(tid, A, P, rA, rP, wA, wP);
@@ -719,16 +727,19 @@ __global__ void __launch_bounds__(256) scan_step_kernel(float* __restrict__ h,
 
 constexpr int kFill = 2 * 152;  // CTAs that keep every SM busy
 
+constexpr int exchange_bytes(int cluster, int lanes) { return 2 * cluster * 2 * lanes * 16; }
+
 template <typename Args>
-cudaError_t launch(void (*kernel)(Args, int, int), const Args& a, int lanes, int bytes,
-                   cudaStream_t st) {
+cudaError_t launch(void (*kernel)(Args, int, int), const Args& a, int lanes, int run,
+                   int bytes, cudaStream_t st) {
   const int blocks = (a.D + 4 * lanes - 1) / (4 * lanes);
   const int64_t units = static_cast<int64_t>(a.B) * blocks;
-  const int tile = kThreads / lanes * R, tiles = (a.T + tile - 1) / tile;
+  const int tile = kThreads / lanes * run, tiles = (a.T + tile - 1) / tile;
   // CTAs of a cluster: until there are enough, as far as the sequence has tiles
   int n = 1;
   while (n < kMaxCluster && n < tiles && units * n < kFill) n *= 2;
   cudaError_t e = cudaSuccess;
+  bytes += exchange_bytes(n, lanes);
   if (bytes > 0)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -759,8 +770,8 @@ bool narrow(int B, int D) {
 
 template <typename E, int G, int LANES, bool VEC>
 cudaError_t fwd_of(const ScanArgs& a, cudaStream_t st) {
-  return launch<ScanArgs>(scan_fwd_kernel<E, G, LANES, VEC>, a, LANES,
-                          Tiles<E, LANES, VEC, 2, kStagesFwd<E, LANES>>::kBytes, st);
+  return launch<ScanArgs>(scan_fwd_kernel<E, G, LANES, VEC>, a, LANES, kRunFwd<E>,
+                          Tiles<E, LANES, VEC, 2, kRunFwd<E>, kStagesFwd<E, LANES>>::kBytes, st);
 }
 template <typename E, int G>
 cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
@@ -771,8 +782,8 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
 
 template <typename E, int G, int LANES, bool VEC>
 cudaError_t bwd_of(const ScanBwdArgs& a, cudaStream_t st) {
-  return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, LANES, VEC>, a, LANES,
-                             Tiles<E, LANES, VEC, 3, kStagesBwd<E, LANES>>::kBytes, st);
+  return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, LANES, VEC>, a, LANES, kRunBwd,
+                             Tiles<E, LANES, VEC, 3, kRunBwd, kStagesBwd<E, LANES>>::kBytes, st);
 }
 template <typename E, int G>
 cudaError_t bwd(const ScanBwdArgs& a, cudaStream_t st) {
