@@ -25,6 +25,8 @@
 // its rounding.  In reverse time the map of a tile on the gradient that comes
 // from later tokens is (A, P) with the same A.
 #include <cooperative_groups.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "f32x2.cuh"
 #include "sanatan_internal.h"
@@ -40,10 +42,12 @@ using namespace f2;
 constexpr int kMark = kScanMark;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kIssuer = kThreads - 32;  // the thread that issues the copies
 constexpr int kMaxCluster = 16;
 template <typename E>
 constexpr int kRunFwd = sizeof(E) == 2 ? 8 : 4;  // consecutive tokens of a thread
 constexpr int kRunBwd = 4;
+constexpr int kStages = 2;  // tiles of a ring
 
 // Four channels as two packed pairs.
 struct V4 {
@@ -120,16 +124,6 @@ __device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
   return n < 0 ? 0 : (n > T ? T : static_cast<int>(n));
 }
 
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Four values of a row in memory.
 template <typename E>
 struct Quad;
@@ -156,19 +150,19 @@ struct Quad<__nv_bfloat16> {
   }
 };
 
-// A thread's four channels of the CTA's 4 * LANES.  VEC (D a multiple of 4): four
+// A thread's four channels of the CTA's 4 * LANES.  TMA (D a multiple of 4): four
 // neighbours, one load or store a row.  Otherwise rows start at any element:
 // channels LANES apart, so that the lanes of a load are neighbours.
-template <int LANES, bool VEC>
+template <int LANES, bool TMA>
 struct Place {
   int c0, lane, D;
   __device__ __forceinline__ int channel(int j) const {
-    return VEC ? c0 + 4 * lane + j : c0 + lane + LANES * j;
+    return TMA ? c0 + 4 * lane + j : c0 + lane + LANES * j;
   }
   __device__ __forceinline__ bool there(int j) const { return channel(j) < D; }
   template <typename E>
   __device__ __forceinline__ void store(E* row, const V4& v) const {
-    if (VEC) {
+    if (TMA) {
       if (there(0)) *reinterpret_cast<typename Quad<E>::type*>(row + channel(0)) = Quad<E>::put(v);
     } else {
       float f[4];
@@ -182,12 +176,12 @@ struct Place {
 
 // The same channels in pairs, pair < 2 * LANES, for the lanes of warp 0 (with 8
 // LANES its upper half does what the lower one does).
-template <int LANES, bool VEC>
+template <int LANES, bool TMA>
 struct PairPlace {
   int c[2];
   bool ok[2];
   __device__ __forceinline__ PairPlace(int c0, int pair, int D) {
-    const Place<LANES, VEC> p{c0, pair / 2, D};
+    const Place<LANES, TMA> p{c0, pair / 2, D};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       c[i] = p.channel(pair % 2 * 2 + i);
@@ -206,58 +200,81 @@ struct PairPlace {
   }
 };
 
-// The tensors' tiles on their way.  VEC: a ring of STAGES tiles in shared memory,
-// in which every thread has its own places (no barrier).  Otherwise the next tile
-// waits in registers.
-template <typename E, int LANES, bool VEC, int NT, int R, int STAGES>
-struct Tiles {
-  using Q = typename Quad<E>::type;
-  static constexpr int kBytes = VEC ? STAGES * NT * R * kThreads * static_cast<int>(sizeof(Q)) : 0;
-  const E* src[NT];  // the thread's first channel of token 0
-  int64_t D;
-  int len;
-  uint32_t at;       // the thread's first place in the ring
-  const Q* places;
-  Place<LANES, VEC> place;
-  E next[VEC ? 1 : NT][VEC ? 1 : R][4];
+struct Maps {
+  CUtensorMap of[3];
+};
 
-  // Loads the thread's tokens t0 ... of a tile; those from len on are not there.
-  __device__ __forceinline__ void issue(int t0, int slot) {
-    if constexpr (VEC) {
-      if (place.there(0)) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const E* from = src[i] + static_cast<int64_t>(t0) * D;
-          const uint32_t to = at + static_cast<uint32_t>((slot * NT + i) * R * kThreads *
-                                                         static_cast<int>(sizeof(Q)));
-          if (t0 + R <= len) {
-#pragma unroll
-            for (int r = 0; r < R; ++r, from += D)
-              cp_async<sizeof(Q)>(to + r * kThreads * static_cast<int>(sizeof(Q)), from);
-          } else {
-#pragma unroll
-            for (int r = 0; r < R; ++r, from += D)
-              if (t0 + r < len)
-                cp_async<sizeof(Q)>(to + r * kThreads * static_cast<int>(sizeof(Q)), from);
-          }
-        }
-      }
-      cp_commit();
-    } else {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            next[i][r][j] = t0 + r < len && place.there(j)
-                                ? src[i][(static_cast<int64_t>(t0) + r) * D + LANES * j]
-                                : store_from_float<E>(0.0f);
+__device__ int g_scan_error;  // a bounded wait gave up
+
+// The tensors' tiles on their way.  TMA (rows of a multiple of 16 bytes): a ring
+// of STAGES tiles in shared memory, each tensor's tile one box copy that one
+// thread issues (rows past T and channels past D come as zeros).  Otherwise the
+// next tile waits in registers.
+template <typename E, int LANES, bool TMA, int NT, int R, int STAGES>
+struct Tiles {
+  static constexpr int kTile = kThreads / LANES * R;
+  static constexpr int kWidth = 4 * LANES;
+  static constexpr int kBox = kTile * kWidth * static_cast<int>(sizeof(E));
+  static constexpr int kBytes = TMA ? STAGES * NT * kBox : 0;
+  using Q = typename Quad<E>::type;
+  const E* src[NT];  // registers: the thread's first channel of token 0
+  int64_t D;
+  int b, len;
+  Place<LANES, TMA> place;
+  unsigned char* ring;
+  uint64_t* full;    // [STAGES] mbarriers
+  const unsigned char* own;  // the thread's first values of a tile
+  const Maps* maps;
+  bool* dead;
+  E next[TMA ? 1 : NT][TMA ? 1 : R][4];
+
+  __device__ __forceinline__ void start(int tid) {
+    if constexpr (TMA) {
+      own = ring + (tid / LANES * R * kWidth + 4 * (tid % LANES)) * static_cast<int>(sizeof(E));
+      if (tid == 0)
+        for (int i = 0; i < STAGES; ++i) tc::mbar_init(&full[i], 1);
+      tc::fence_mbar_init();
     }
   }
+  // TMA, one thread: fetch the tile that starts at token t (none of it present:
+  // only complete the phase).
+  __device__ __forceinline__ void fetch(int t, int slot) {
+    if (t >= len) {
+      tc::mbar_arrive(&full[slot]);
+      return;
+    }
+    tc::mbar_arrive_expect_tx(&full[slot], NT * kBox);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+          " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(ring + (slot * NT + i) * kBox)),
+          "l"(reinterpret_cast<uint64_t>(&maps->of[i])), "r"(place.c0), "r"(t), "r"(b),
+          "r"(tc::smem_u32(&full[slot]))
+          : "memory");
+  }
+  __device__ __forceinline__ void wait(int slot, uint32_t parity) {
+    if (!*dead && !tc::mbar_wait_bounded(&full[slot], parity)) {
+      *dead = true;
+      g_scan_error = 1;
+    }
+  }
+  // Registers: the thread's tokens t0 ... of a tile.
+  __device__ __forceinline__ void prefetch(int t0) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          next[i][r][j] = t0 + r < len && place.there(j)
+                              ? src[i][(static_cast<int64_t>(t0) + r) * D + LANES * j]
+                              : store_from_float<E>(0.0f);
+  }
   __device__ __forceinline__ V4 get(int i, int r, int slot) const {
-    if constexpr (VEC)
-      return Quad<E>::get(places[((slot * NT + i) * R + r) * kThreads]);
+    if constexpr (TMA)
+      return Quad<E>::get(*reinterpret_cast<const Q*>(
+          own + (slot * NT + i) * kBox + r * kWidth * static_cast<int>(sizeof(E))));
     else
       return v4(load_as_float(&next[i][r][0]), load_as_float(&next[i][r][1]),
                 load_as_float(&next[i][r][2]), load_as_float(&next[i][r][3]));
@@ -276,29 +293,8 @@ struct Exchange {
   V4 p[BWD ? kWarps : 1][LANES];  // the same in reverse time
   V4 in_p[BWD ? kWarps : 1][LANES];
   uint64_t full[2];      // mbarriers: all of a step's maps have come
+  uint64_t ring[kStages];  // mbarriers: a tile has come
 };
-
-__device__ int g_scan_error;  // a bounded wait gave up
-
-// Wait for a phase of `bar` that other CTAs of the cluster complete with st.async;
-// false after about two seconds.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) {
-  const uint32_t at = tc::smem_u32(bar);
-  uint64_t t0 = 0;
-  for (uint32_t n = 0;; ++n) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(at), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (n == 0) t0 = tc::globaltimer_ns();
-    if (n % 64 == 63 && tc::globaltimer_ns() - t0 > 2000000000ull) return false;
-  }
-}
 
 // Phase `bar` completes once `bytes` have come.  Relaxed: nothing the thread did
 // before has to be seen by anyone (a release would wait for its global stores).
@@ -322,14 +318,17 @@ struct Cluster {
   Exchange<LANES, BWD>& ex;
   ulonglong2* all;  // [2][size][2 * LANES]: (A, H) of the cluster's CTAs, by the step's parity
   int rank, size, steps, pair;
-  bool dead = false;
+  bool dead = false;  // a wait gave up: no more waiting
 
   __device__ __forceinline__ ulonglong2* of(int s, int r) const {
     return all + ((s & 1) * size + r) * 2 * LANES + pair;
   }
   __device__ __forceinline__ uint32_t bytes() const { return size * 2 * LANES * 16; }
   __device__ __forceinline__ void start() {  // all threads
-    if (size == 1) return;
+    if (size == 1) {
+      __syncthreads();
+      return;
+    }
     if (threadIdx.x == 0) {
       tc::mbar_init(&ex.full[0], 1);
       tc::mbar_init(&ex.full[1], 1);
@@ -355,7 +354,7 @@ struct Cluster {
   }
   // Returns what comes into this CTA's tile.
   __device__ __forceinline__ uint64_t arrive(int s, uint64_t& carry) {
-    if (!dead && !wait_cluster(&ex.full[s & 1], (s >> 1) & 1)) {
+    if (!dead && !tc::mbar_wait_bounded(&ex.full[s & 1], (s >> 1) & 1)) {
       dead = true;
       g_scan_error = 1;
     }
@@ -369,10 +368,10 @@ struct Cluster {
     if (threadIdx.x == 0 && s + 2 < steps) expect(&ex.full[s & 1], bytes());
     return in;
   }
-  // No CTA leaves while another may still send to it.
+  // No CTA leaves while another may still send to it, or its own copies are under way.
   __device__ __forceinline__ void finish() {
+    if (dead) __nanosleep(1000000);  // copies under way land
     if (size == 1) return;
-    if (dead) __nanosleep(1000000);
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     asm volatile("barrier.cluster.wait;" ::: "memory");
   }
@@ -401,17 +400,13 @@ __device__ __forceinline__ void warp_scan(int tid, const V4& A, const V4& H, V4&
   }
 }
 
-template <typename E, int LANES>
-constexpr int kStagesFwd = 2;
-
-template <typename E, int G, int LANES, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs p, int blocks,
-                                                               int cluster_size) {
+template <typename E, int G, int LANES, bool TMA>
+__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(
+    const ScanArgs p, const __grid_constant__ Maps maps, int blocks, int cluster_size) {
   constexpr int R = kRunFwd<E>;
   constexpr int kTile = kThreads / LANES * R;
-  constexpr int kStages = kStagesFwd<E, LANES>;
-  using Ring = Tiles<E, LANES, VEC, 2, R, kStages>;
-  extern __shared__ __align__(16) unsigned char ring[];
+  using Ring = Tiles<E, LANES, TMA, 2, R, kStages>;
+  extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(16) Exchange<LANES, false> ex;
 
   const int rank = static_cast<int>(blockIdx.x % cluster_size);
@@ -419,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs p,
   const int b = unit / blocks;
   const int tid = threadIdx.x, lane = tid % LANES, warp = tid >> 5;
   const int T = p.T, D = p.D;
-  const Place<LANES, VEC> place{(unit % blocks) * 4 * LANES, lane, D};
+  const Place<LANES, TMA> place{(unit % blocks) * 4 * LANES, lane, D};
   const int len = length_of(p.lens, b, T);
   const int tiles = (T + kTile - 1) / kTile;
   const int steps = (tiles + cluster_size - 1) / cluster_size;
@@ -430,36 +425,39 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs p,
   in.src[1] = static_cast<const E*>(p.x) + base;
   in.D = D;
   in.len = len;
-  in.at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
-          tid * static_cast<int>(sizeof(typename Ring::Q));
-  in.places = reinterpret_cast<const typename Ring::Q*>(ring) + tid;
+  in.b = b;
   in.place = place;
+  in.ring = ring;
+  in.full = ex.ring;
+  in.maps = &maps;
   E* y = static_cast<E*>(p.y) + static_cast<int64_t>(b) * T * D;
 
-  const int64_t first = static_cast<int64_t>(rank) * kTile + tid / LANES * R;
-  // The thread's first token in step s; T past the last step.
-  auto token = [&](int s) {
-    const int64_t t = first + static_cast<int64_t>(s) * cluster_size * kTile;
-    return t < T ? static_cast<int>(t) : T;
-  };
-  if constexpr (VEC) {
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) in.issue(token(s), s);
-  } else {
-    in.issue(token(0), 0);
-  }
+  // First token of the CTA's tile in step s, and of the thread's run; T or more past
+  // the last one (T is at most 2^30, so a few tiles more fit an int).
+  const int run = tid / LANES * R;
+  auto begin = [&](int s) { return (s * cluster_size + rank) * kTile; };
+  auto token = [&](int s) { return begin(s) + run; };
   // Warp 0: the state before the step's first tile.
   const int at = tid % (2 * LANES);
-  const PairPlace<LANES, VEC> pair(place.c0, at, D);
+  const PairPlace<LANES, TMA> pair(place.c0, at, D);
   uint64_t carry = pair.load(p.h0 == nullptr ? nullptr : p.h0 + static_cast<int64_t>(b) * D);
   Cluster<LANES, false> cluster{ex, reinterpret_cast<ulonglong2*>(ring + Ring::kBytes), rank, cluster_size,
                           steps, at};
+  in.dead = &cluster.dead;
+  in.start(tid);
   cluster.start();
+  if constexpr (TMA) {
+    if (tid == kIssuer)
+      for (int s = 0; s < kStages; ++s) in.fetch(begin(s), s);
+  } else {
+    in.prefetch(token(0));
+  }
 
   int slot = 0;
+  uint32_t phase = 0;
   for (int s = 0; s < steps; ++s) {
     const int t0 = token(s);
-    if constexpr (VEC) cp_wait<kStages - 1>();
+    if constexpr (TMA) in.wait(slot, phase);
     // The run's decays and inputs, and its map.
     V4 a[R], u[R], A, H;
 #pragma unroll
@@ -469,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs p,
       u[r] = in.get(1, r, slot);
       if (G == SANATAN_GATE_SIGMOID) u[r] = mul(keep, u[r]);
     }
-    in.issue(token(s + (VEC ? kStages : 1)), slot);
+    if constexpr (!TMA) in.prefetch(token(s + 1));
     if (t0 + R > len) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -492,6 +490,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs p,
       ex.h[warp][lane] = wH;
     }
     __syncthreads();
+    if constexpr (TMA) {  // every warp has read the slot
+      if (tid == kIssuer && s + kStages < steps) in.fetch(begin(s + kStages), slot);
+    }
     if (warp == 0) {
       uint64_t h = carry;
       if (cluster_size > 1) {
@@ -531,25 +532,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(const ScanArgs p,
         if (t0 + r < T) place.store(row, select(t0 + r < len, h, v4(0.0f)));
       }
     }
-    slot = slot == kStages - 1 ? 0 : slot + 1;
+    if (++slot == kStages) {
+      slot = 0;
+      phase ^= 1;
+    }
   }
   if (p.h_out != nullptr && rank == 0 && warp == 0)
     pair.store(p.h_out + static_cast<int64_t>(b) * D, carry);
   cluster.finish();
 }
 
-template <typename E, int LANES>
-constexpr int kStagesBwd = 2;
-
-template <typename E, int G, int LANES, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs p, int blocks,
-                                                               int cluster_size) {
+template <typename E, int G, int LANES, bool TMA>
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
+    const ScanBwdArgs p, const __grid_constant__ Maps maps, int blocks, int cluster_size) {
   constexpr int R = kRunBwd;
   constexpr int kTile = kThreads / LANES * R;  // starts at a mark
   static_assert(kTile % kMark == 0, "tile");
-  constexpr int kStages = kStagesBwd<E, LANES>;
-  using Ring = Tiles<E, LANES, VEC, 3, R, kStages>;
-  extern __shared__ __align__(16) unsigned char ring[];
+  using Ring = Tiles<E, LANES, TMA, 3, R, kStages>;
+  extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(16) Exchange<LANES, true> ex;
 
   const int rank = static_cast<int>(blockIdx.x % cluster_size);
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
   const int b = unit / blocks;
   const int tid = threadIdx.x, lane = tid % LANES, warp = tid >> 5;
   const int T = p.T, D = p.D;
-  const Place<LANES, VEC> place{(unit % blocks) * 4 * LANES, lane, D};
+  const Place<LANES, TMA> place{(unit % blocks) * 4 * LANES, lane, D};
   const int len = length_of(p.lens, b, T);
   const int tiles = (T + kTile - 1) / kTile;
   const int steps = (tiles + cluster_size - 1) / cluster_size;
@@ -569,10 +569,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
   in.src[2] = static_cast<const E*>(p.dy) + base;
   in.D = D;
   in.len = len;
-  in.at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
-          tid * static_cast<int>(sizeof(typename Ring::Q));
-  in.places = reinterpret_cast<const typename Ring::Q*>(ring) + tid;
+  in.b = b;
   in.place = place;
+  in.ring = ring;
+  in.full = ex.ring;
+  in.maps = &maps;
   E* dx = static_cast<E*>(p.dx) + static_cast<int64_t>(b) * T * D;
   E* dg = static_cast<E*>(p.dg) + static_cast<int64_t>(b) * T * D;
   const float* marks = p.marks + static_cast<int64_t>(b) * ((T + kMark - 1) / kMark) * D;
@@ -583,23 +584,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
     const int64_t k = tiles - 1 - (static_cast<int64_t>(s) * cluster_size + rank);
     return k < 0 ? -1 : static_cast<int>(k);
   };
-  auto token = [&](int s) {
-    const int k = tile(s);
-    return k < 0 ? T : min(k * kTile + tid / LANES * R, T);
-  };
-  if constexpr (VEC) {
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) in.issue(token(s), s);
-  } else {
-    in.issue(token(0), 0);
-  }
+  const int run = tid / LANES * R;
+  auto begin = [&](int s) { return tile(s) < 0 ? T : tile(s) * kTile; };
+  auto token = [&](int s) { return min(begin(s) + run, T); };
   // Warp 0: the gradient that comes into the step's last token from later ones.
   const int at = tid % (2 * LANES);
-  const PairPlace<LANES, VEC> pair(place.c0, at, D);
+  const PairPlace<LANES, TMA> pair(place.c0, at, D);
   uint64_t carry = pair.load(p.dh_out == nullptr ? nullptr : p.dh_out + static_cast<int64_t>(b) * D);
   Cluster<LANES, true> cluster{ex, reinterpret_cast<ulonglong2*>(ring + Ring::kBytes), rank, cluster_size,
                           steps, at};
+  in.dead = &cluster.dead;
+  in.start(tid);
   cluster.start();
+  if constexpr (TMA) {
+    if (tid == kIssuer)
+      for (int s = 0; s < kStages; ++s) in.fetch(begin(s), s);
+  } else {
+    in.prefetch(token(0));
+  }
   // Warp 0: the state before the tile of step s, loaded a step ahead.
   auto mark_of = [&](int s) {
     const int k = tile(s);
@@ -610,11 +612,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
   uint64_t next_mark = warp == 0 ? mark_of(0) : 0;
 
   int slot = 0;
+  uint32_t phase = 0;
   for (int s = 0; s < steps; ++s) {
     const int t0 = token(s);
     uint64_t mark = next_mark;
     if (warp == 0) next_mark = mark_of(s + 1);
-    if constexpr (VEC) cp_wait<kStages - 1>();
+    if constexpr (TMA) in.wait(slot, phase);
     V4 a[R], keep[R], x[R], dy[R], A, H, P;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
       x[r] = in.get(1, r, slot);
       dy[r] = in.get(2, r, slot);
     }
-    in.issue(token(s + (VEC ? kStages : 1)), slot);
+    if constexpr (!TMA) in.prefetch(token(s + 1));
     if (t0 + R > len) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -650,6 +653,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
       ex.p[warp][lane] = wP;
     }
     __syncthreads();
+    if constexpr (TMA) {  // every warp has read the slot
+      if (tid == kIssuer && s + kStages < steps) in.fetch(begin(s + kStages), slot);
+    }
     if (warp == 0) {
       uint64_t d = carry;
       if (cluster_size > 1) {
@@ -701,7 +707,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(const ScanBwdArgs
         place.store(dg + (static_cast<int64_t>(t0) + r) * D, select(there, og, v4(0.0f)));
       }
     }
-    slot = slot == kStages - 1 ? 0 : slot + 1;
+    if (++slot == kStages) {
+      slot = 0;
+      phase ^= 1;
+    }
   }
   if (p.dh0 != nullptr && rank == 0 && warp == 0)
     pair.store(p.dh0 + static_cast<int64_t>(b) * D, carry);
@@ -729,9 +738,43 @@ constexpr int kFill = 2 * 152;  // CTAs that keep every SM busy
 
 constexpr int exchange_bytes(int cluster, int lanes) { return 2 * cluster * 2 * lanes * 16; }
 
+// cuTensorMapEncodeTiled, looked up once through the runtime.
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                     cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+  }();
+  return fn;
+}
+
+// The map of a [B, T, D] tensor with boxes of `rows` tokens x `width` channels;
+// false where none can be made (rows that are no multiple of 16 bytes, sizes out
+// of the format's range).
+bool encode(CUtensorMap* map, const void* p, int dtype, int B, int T, int D, int rows, int width) {
+  const cuuint64_t e = dtype == SANATAN_F32 ? 4 : 2;
+  if (D * e % 16 != 0 || map_encoder() == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[2] = {D * e, static_cast<cuuint64_t>(T) * D * e};
+  if (strides[1] >= (1ull << 40)) return false;
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return map_encoder()(map,
+                       dtype == SANATAN_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       3, const_cast<void*>(p), dims, strides, box, step,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename Args>
-cudaError_t launch(void (*kernel)(Args, int, int), const Args& a, int lanes, int run,
-                   int bytes, cudaStream_t st) {
+cudaError_t launch(void (*kernel)(Args, Maps, int, int), const Args& a, const Maps& maps, int lanes,
+                   int run, int bytes, cudaStream_t st) {
   const int blocks = (a.D + 4 * lanes - 1) / (4 * lanes);
   const int64_t units = static_cast<int64_t>(a.B) * blocks;
   const int tile = kThreads / lanes * run, tiles = (a.T + tile - 1) / tile;
@@ -759,7 +802,7 @@ cudaError_t launch(void (*kernel)(Args, int, int), const Args& a, int lanes, int
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, blocks, n);
+  return cudaLaunchKernelEx(&cfg, kernel, a, maps, blocks, n);
 }
 
 // Channels of a CTA: 64 (16 lanes), or 32 where 64 leave too few CTAs even with
@@ -768,28 +811,35 @@ bool narrow(int B, int D) {
   return static_cast<int64_t>(B) * ((D + 63) / 64) * kMaxCluster < kFill;
 }
 
-template <typename E, int G, int LANES, bool VEC>
+template <typename E, int G, int LANES>
 cudaError_t fwd_of(const ScanArgs& a, cudaStream_t st) {
-  return launch<ScanArgs>(scan_fwd_kernel<E, G, LANES, VEC>, a, LANES, kRunFwd<E>,
-                          Tiles<E, LANES, VEC, 2, kRunFwd<E>, kStagesFwd<E, LANES>>::kBytes, st);
+  using Ring = Tiles<E, LANES, true, 2, kRunFwd<E>, kStages>;
+  Maps m;
+  if (a.T > 0 && encode(&m.of[0], a.g, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth) &&
+      encode(&m.of[1], a.x, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth))
+    return launch<ScanArgs>(scan_fwd_kernel<E, G, LANES, true>, a, m, LANES, kRunFwd<E>,
+                            Ring::kBytes, st);
+  return launch<ScanArgs>(scan_fwd_kernel<E, G, LANES, false>, a, m, LANES, kRunFwd<E>, 0, st);
 }
 template <typename E, int G>
 cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
-  if (narrow(a.B, a.D))
-    return a.D % 4 == 0 ? fwd_of<E, G, 8, true>(a, st) : fwd_of<E, G, 8, false>(a, st);
-  return a.D % 4 == 0 ? fwd_of<E, G, 16, true>(a, st) : fwd_of<E, G, 16, false>(a, st);
+  return narrow(a.B, a.D) ? fwd_of<E, G, 8>(a, st) : fwd_of<E, G, 16>(a, st);
 }
 
-template <typename E, int G, int LANES, bool VEC>
+template <typename E, int G, int LANES>
 cudaError_t bwd_of(const ScanBwdArgs& a, cudaStream_t st) {
-  return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, LANES, VEC>, a, LANES, kRunBwd,
-                             Tiles<E, LANES, VEC, 3, kRunBwd, kStagesBwd<E, LANES>>::kBytes, st);
+  using Ring = Tiles<E, LANES, true, 3, kRunBwd, kStages>;
+  Maps m;
+  if (a.T > 0 && encode(&m.of[0], a.g, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth) &&
+      encode(&m.of[1], a.x, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth) &&
+      encode(&m.of[2], a.dy, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth))
+    return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, LANES, true>, a, m, LANES, kRunBwd,
+                               Ring::kBytes, st);
+  return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, LANES, false>, a, m, LANES, kRunBwd, 0, st);
 }
 template <typename E, int G>
 cudaError_t bwd(const ScanBwdArgs& a, cudaStream_t st) {
-  if (narrow(a.B, a.D))
-    return a.D % 4 == 0 ? bwd_of<E, G, 8, true>(a, st) : bwd_of<E, G, 8, false>(a, st);
-  return a.D % 4 == 0 ? bwd_of<E, G, 16, true>(a, st) : bwd_of<E, G, 16, false>(a, st);
+  return narrow(a.B, a.D) ? bwd_of<E, G, 8>(a, st) : bwd_of<E, G, 16>(a, st);
 }
 
 template <typename E, int G>
