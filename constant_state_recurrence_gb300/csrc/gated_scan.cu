@@ -28,6 +28,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "f32x2.cuh"
 #include "sanatan_internal.h"
 #include "sanatan_math.cuh"
@@ -401,7 +403,7 @@ __device__ __forceinline__ void warp_scan(int tid, const V4& A, const V4& H, V4&
 }
 
 template <typename E, int G, int LANES, bool TMA>
-__global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(
+__global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_fwd_kernel(
     const ScanArgs p, const __grid_constant__ Maps maps, int blocks, int cluster_size) {
   constexpr int R = kRunFwd<E>;
   constexpr int kTile = kThreads / LANES * R;
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_fwd_kernel(
 }
 
 template <typename E, int G, int LANES, bool TMA>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
+__global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_bwd_kernel(
     const ScanBwdArgs p, const __grid_constant__ Maps maps, int blocks, int cluster_size) {
   constexpr int R = kRunBwd;
   constexpr int kTile = kThreads / LANES * R;  // starts at a mark
@@ -717,24 +719,43 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
   cluster.finish();
 }
 
+// One token: four elements a thread (the tensors are dense, so rows do not matter),
+// the last n % 4 by a thread each.
 template <typename E, int G>
-__global__ void __launch_bounds__(256) scan_step_kernel(float* __restrict__ h,
-                                                        const E* __restrict__ x,
-                                                        const E* __restrict__ g, int64_t n,
-                                                        E* __restrict__ y) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n) return;
+__global__ void __launch_bounds__(kThreads) scan_step_kernel(float* __restrict__ h,
+                                                             const E* __restrict__ x,
+                                                             const E* __restrict__ g, int64_t n,
+                                                             E* __restrict__ y) {
+  using Q = Quad<E>;
+  using QF = Quad<float>;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t quads = n / 4;
+  V4 gv, xv, hv;
+  const int64_t last = 4 * quads + (i - quads);
+  if (i < quads) {
+    hv = QF::get(reinterpret_cast<const QF::type*>(h)[i]);
+    gv = Q::get(reinterpret_cast<const typename Q::type*>(g)[i]);
+    xv = Q::get(reinterpret_cast<const typename Q::type*>(x)[i]);
+  } else if (last < n) {
+    hv = v4(h[last]);
+    gv = v4(load_as_float(g + last));
+    xv = v4(load_as_float(x + last));
+  } else {
+    return;
+  }
   V4 a, keep;
-  gate<G>(v4(load_as_float(g + i)), a, keep);
-  V4 u = v4(load_as_float(x + i));
-  if (G == SANATAN_GATE_SIGMOID) u = mul(keep, u);
-  float v[4];
-  get(fma(a, v4(h[i]), u), v);
-  h[i] = v[0];
-  y[i] = store_from_float<E>(v[0]);
+  gate<G>(gv, a, keep);
+  hv = fma(a, hv, G == SANATAN_GATE_SIGMOID ? mul(keep, xv) : xv);
+  if (i < quads) {
+    reinterpret_cast<QF::type*>(h)[i] = QF::put(hv);
+    reinterpret_cast<typename Q::type*>(y)[i] = Q::put(hv);
+  } else {
+    float f[4];
+    get(hv, f);
+    h[last] = f[0];
+    y[last] = store_from_float<E>(f[0]);
+  }
 }
-
-constexpr int kFill = 2 * 152;  // CTAs that keep every SM busy
 
 constexpr int exchange_bytes(int cluster, int lanes) { return 2 * cluster * 2 * lanes * 16; }
 
@@ -751,12 +772,12 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return fn;
 }
 
-// The map of a [B, T, D] tensor with boxes of `rows` tokens x `width` channels;
-// false where none can be made (rows that are no multiple of 16 bytes, sizes out
-// of the format's range).
+// The map of a [B, T, D] tensor (rows of a multiple of 16 bytes) with boxes of `rows`
+// tokens x `width` channels; false where none can be made (sizes out of the
+// format's range).
 bool encode(CUtensorMap* map, const void* p, int dtype, int B, int T, int D, int rows, int width) {
   const cuuint64_t e = dtype == SANATAN_F32 ? 4 : 2;
-  if (D * e % 16 != 0 || map_encoder() == nullptr) return false;
+  if (map_encoder() == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T),
                               static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[2] = {D * e, static_cast<cuuint64_t>(T) * D * e};
@@ -772,79 +793,158 @@ bool encode(CUtensorMap* map, const void* p, int dtype, int B, int T, int D, int
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch shape: CTAs of a cluster, and the steps that the longest CTA takes (over
+// all waves of clusters).
+struct Shape {
+  int cluster;
+  int64_t steps;
+};
+
 template <typename Args>
-cudaError_t launch(void (*kernel)(Args, Maps, int, int), const Args& a, const Maps& maps, int lanes,
-                   int run, int bytes, cudaStream_t st) {
-  const int blocks = (a.D + 4 * lanes - 1) / (4 * lanes);
-  const int64_t units = static_cast<int64_t>(a.B) * blocks;
-  const int tile = kThreads / lanes * run, tiles = (a.T + tile - 1) / tile;
-  // CTAs of a cluster: until there are enough, as far as the sequence has tiles
-  int n = 1;
-  while (n < kMaxCluster && n < tiles && units * n < kFill) n *= 2;
-  cudaError_t e = cudaSuccess;
-  bytes += exchange_bytes(n, lanes);
-  if (bytes > 0)
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && n > 8)
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
+cudaLaunchConfig_t config(void (*kernel)(Args, Maps, int, int), int64_t ctas, int cluster, int bytes,
+                          cudaLaunchAttribute* attr, cudaStream_t st, cudaError_t* e) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * n));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = n;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, maps, blocks, n);
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (*e == cudaSuccess && cluster > 8)
+    *e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return cfg;
 }
 
-// Channels of a CTA: 64 (16 lanes), or 32 where 64 leave too few CTAs even with
-// the largest clusters.
-bool narrow(int B, int D) {
-  return static_cast<int64_t>(B) * ((D + 63) / 64) * kMaxCluster < kFill;
+// Clusters of n CTAs of a kernel that the current device holds at once (asked of the
+// runtime once).
+template <auto Kernel, typename Args, typename Ring>
+int clusters_held(int n) {
+  constexpr int kDevices = 16;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const bool keep = dev >= 0 && dev < kDevices;
+  int held = keep ? known[dev][n].load(std::memory_order_relaxed) : 0;
+  if (held == 0) {
+    cudaLaunchAttribute attr;
+    cudaError_t e;
+    const cudaLaunchConfig_t cfg =
+        config<Args>(Kernel, n, n, Ring::kBytes + exchange_bytes(n, Ring::kWidth / 4), &attr,
+                     nullptr, &e);
+    if (e != cudaSuccess || cudaOccupancyMaxActiveClusters(&held, Kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      held = 0;
+    }
+    if (held <= 0) held = -1;
+    if (keep) known[dev][n].store(held, std::memory_order_relaxed);
+  }
+  return held;
 }
 
-template <typename E, int G, int LANES>
-cudaError_t fwd_of(const ScanArgs& a, cudaStream_t st) {
-  using Ring = Tiles<E, LANES, true, 2, kRunFwd<E>, kStages>;
+// Few sequences: the largest cluster with which all clusters still run at once (a
+// second wave would cost more than it splits), and of those with the same
+// number of steps the smallest.  Training shape (B 8, T 4096, D 768, bf16: 96
+// blocks of 64 channels), forward us by cluster size: 1: 32.6, 2: 30.5, 3: 26.7 (288
+// of 291 places), 4: 31.6, 8: 34.0.
+template <auto Kernel, typename Args, typename Ring>
+Shape shape_of(const Args& a) {
+  const int64_t units = static_cast<int64_t>(a.B) * ((a.D + Ring::kWidth - 1) / Ring::kWidth);
+  const int64_t tiles = (static_cast<int64_t>(a.T) + Ring::kTile - 1) / Ring::kTile;
+  const int one = clusters_held<Kernel, Args, Ring>(1);
+  Shape best{1, tiles * (one > 0 ? (units + one - 1) / one : units)};
+  for (int n = 2; n <= kMaxCluster && n <= tiles; ++n) {
+    const int64_t steps = (tiles + n - 1) / n;
+    if (units <= clusters_held<Kernel, Args, Ring>(n) && steps < best.steps) best = {n, steps};
+  }
+  return best;
+}
+
+template <auto Kernel, typename Args, typename Ring>
+cudaError_t launch(const Args& a, const Maps& maps, int cluster, cudaStream_t st) {
+  const int blocks = (a.D + Ring::kWidth - 1) / Ring::kWidth;
+  cudaLaunchAttribute attr;
+  cudaError_t e;
+  const cudaLaunchConfig_t cfg =
+      config<Args>(Kernel, static_cast<int64_t>(a.B) * blocks * cluster, cluster,
+                   Ring::kBytes + exchange_bytes(cluster, Ring::kWidth / 4), &attr, st, &e);
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, Kernel, a, maps, blocks, cluster);
+}
+
+// Channels of a CTA: 64 or 32, whichever takes fewer steps (tiles of 32 channels have
+// twice the tokens; they let few sequences fill the GPU).
+template <auto Wide, auto Narrow, typename Args, typename WideRing, typename NarrowRing>
+cudaError_t launch_best(const Args& a, bool (*encode_all)(Maps*, const Args&, int, int),
+                        cudaStream_t st, bool* encoded) {
+  const Shape w = shape_of<Wide, Args, WideRing>(a), n = shape_of<Narrow, Args, NarrowRing>(a);
   Maps m;
-  if (a.T > 0 && encode(&m.of[0], a.g, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth) &&
-      encode(&m.of[1], a.x, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth))
-    return launch<ScanArgs>(scan_fwd_kernel<E, G, LANES, true>, a, m, LANES, kRunFwd<E>,
-                            Ring::kBytes, st);
-  return launch<ScanArgs>(scan_fwd_kernel<E, G, LANES, false>, a, m, LANES, kRunFwd<E>, 0, st);
+  if (n.steps < w.steps) {
+    *encoded = encode_all(&m, a, NarrowRing::kTile, NarrowRing::kWidth);
+    return *encoded ? launch<Narrow, Args, NarrowRing>(a, m, n.cluster, st) : cudaSuccess;
+  }
+  *encoded = encode_all(&m, a, WideRing::kTile, WideRing::kWidth);
+  return *encoded ? launch<Wide, Args, WideRing>(a, m, w.cluster, st) : cudaSuccess;
+}
+
+bool encode_fwd(Maps* m, const ScanArgs& a, int rows, int width) {
+  return encode(&m->of[0], a.g, a.dtype, a.B, a.T, a.D, rows, width) &&
+         encode(&m->of[1], a.x, a.dtype, a.B, a.T, a.D, rows, width);
+}
+bool encode_bwd(Maps* m, const ScanBwdArgs& a, int rows, int width) {
+  return encode(&m->of[0], a.g, a.dtype, a.B, a.T, a.D, rows, width) &&
+         encode(&m->of[1], a.x, a.dtype, a.B, a.T, a.D, rows, width) &&
+         encode(&m->of[2], a.dy, a.dtype, a.B, a.T, a.D, rows, width);
+}
+template <typename Args>
+bool encode_none(Maps*, const Args&, int, int) {
+  return true;
+}
+
+template <typename E, int G, bool TMA>
+cudaError_t fwd_of(const ScanArgs& a, cudaStream_t st, bool* done) {
+  return launch_best<scan_fwd_kernel<E, G, 16, TMA>, scan_fwd_kernel<E, G, 8, TMA>, ScanArgs,
+                     Tiles<E, 16, TMA, 2, kRunFwd<E>, kStages>,
+                     Tiles<E, 8, TMA, 2, kRunFwd<E>, kStages>>(
+      a, TMA ? encode_fwd : encode_none<ScanArgs>, st, done);
 }
 template <typename E, int G>
 cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
-  return narrow(a.B, a.D) ? fwd_of<E, G, 8>(a, st) : fwd_of<E, G, 16>(a, st);
+  bool done = false;
+  if (a.T > 0 && a.D * sizeof(E) % 16 == 0) {
+    const cudaError_t e = fwd_of<E, G, true>(a, st, &done);
+    if (done) return e;
+  }
+  return fwd_of<E, G, false>(a, st, &done);
 }
 
-template <typename E, int G, int LANES>
-cudaError_t bwd_of(const ScanBwdArgs& a, cudaStream_t st) {
-  using Ring = Tiles<E, LANES, true, 3, kRunBwd, kStages>;
-  Maps m;
-  if (a.T > 0 && encode(&m.of[0], a.g, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth) &&
-      encode(&m.of[1], a.x, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth) &&
-      encode(&m.of[2], a.dy, a.dtype, a.B, a.T, a.D, Ring::kTile, Ring::kWidth))
-    return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, LANES, true>, a, m, LANES, kRunBwd,
-                               Ring::kBytes, st);
-  return launch<ScanBwdArgs>(scan_bwd_kernel<E, G, LANES, false>, a, m, LANES, kRunBwd, 0, st);
+template <typename E, int G, bool TMA>
+cudaError_t bwd_of(const ScanBwdArgs& a, cudaStream_t st, bool* done) {
+  return launch_best<scan_bwd_kernel<E, G, 16, TMA>, scan_bwd_kernel<E, G, 8, TMA>, ScanBwdArgs,
+                     Tiles<E, 16, TMA, 3, kRunBwd, kStages>,
+                     Tiles<E, 8, TMA, 3, kRunBwd, kStages>>(
+      a, TMA ? encode_bwd : encode_none<ScanBwdArgs>, st, done);
 }
 template <typename E, int G>
 cudaError_t bwd(const ScanBwdArgs& a, cudaStream_t st) {
-  return narrow(a.B, a.D) ? bwd_of<E, G, 8>(a, st) : bwd_of<E, G, 16>(a, st);
+  bool done = false;
+  if (a.T > 0 && a.D * sizeof(E) % 16 == 0) {
+    const cudaError_t e = bwd_of<E, G, true>(a, st, &done);
+    if (done) return e;
+  }
+  return bwd_of<E, G, false>(a, st, &done);
 }
 
 template <typename E, int G>
 cudaError_t step(float* h, const void* x, const void* g, int64_t n, void* y, cudaStream_t st) {
-  scan_step_kernel<E, G><<<static_cast<unsigned>((n + 255) / 256), 256, 0, st>>>(
+  const int64_t threads = n / 4 + n % 4;
+  scan_step_kernel<E, G><<<static_cast<unsigned>((threads + kThreads - 1) / kThreads), kThreads, 0,
+                           st>>>(
       h, static_cast<const E*>(x), static_cast<const E*>(g), n, static_cast<E*>(y));
   return cudaGetLastError();
 }
