@@ -28,7 +28,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <atomic>
+#include <mutex>
 
 #include "f32x2.cuh"
 #include "sanatan_internal.h"
@@ -800,13 +800,12 @@ struct Shape {
   int64_t steps;
 };
 
-template <typename Args>
-cudaLaunchConfig_t config(void (*kernel)(Args, Maps, int, int), int64_t ctas, int cluster, int bytes,
-                          cudaLaunchAttribute* attr, cudaStream_t st, cudaError_t* e) {
+template <typename Args, typename Ring>
+cudaLaunchConfig_t config(int64_t ctas, int cluster, cudaLaunchAttribute* attr, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
+  cfg.dynamicSmemBytes = Ring::kBytes + exchange_bytes(cluster, Ring::kWidth / 4);
   cfg.stream = st;
   attr->id = cudaLaunchAttributeClusterDimension;
   attr->val.clusterDim.x = cluster;
@@ -814,37 +813,45 @@ cudaLaunchConfig_t config(void (*kernel)(Args, Maps, int, int), int64_t ctas, in
   attr->val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const void* fn = reinterpret_cast<const void*>(kernel);
-  *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (*e == cudaSuccess && cluster > 8)
-    *e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return cfg;
 }
 
-// Clusters of n CTAs of a kernel that the current device holds at once (asked of the
-// runtime once).
+// held[n]: clusters of n CTAs of a kernel that the current device holds at once.  The
+// runtime is asked once a device, when the kernel's attributes are set too.
+struct Held {
+  int held[kMaxCluster + 1] = {};
+};
 template <auto Kernel, typename Args, typename Ring>
-int clusters_held(int n) {
-  constexpr int kDevices = 16;
-  static std::atomic<int> known[kDevices][kMaxCluster + 1];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  const bool keep = dev >= 0 && dev < kDevices;
-  int held = keep ? known[dev][n].load(std::memory_order_relaxed) : 0;
-  if (held == 0) {
+cudaError_t ask(Held* out) {
+  const void* fn = reinterpret_cast<const void*>(Kernel);
+  cudaError_t e =
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Ring::kBytes + exchange_bytes(kMaxCluster, Ring::kWidth / 4));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int n = 1; e == cudaSuccess && n <= kMaxCluster; ++n) {
     cudaLaunchAttribute attr;
-    cudaError_t e;
-    const cudaLaunchConfig_t cfg =
-        config<Args>(Kernel, n, n, Ring::kBytes + exchange_bytes(n, Ring::kWidth / 4), &attr,
-                     nullptr, &e);
-    if (e != cudaSuccess || cudaOccupancyMaxActiveClusters(&held, Kernel, &cfg) != cudaSuccess) {
+    const cudaLaunchConfig_t cfg = config<Args, Ring>(n, n, &attr, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&out->held[n], Kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      held = 0;
+      out->held[n] = 0;
     }
-    if (held <= 0) held = -1;
-    if (keep) known[dev][n].store(held, std::memory_order_relaxed);
   }
-  return held;
+  return e;
+}
+template <auto Kernel, typename Args, typename Ring>
+cudaError_t held_by(Held* out) {
+  constexpr int kDevices = 16;
+  static std::once_flag once[kDevices];
+  static Held known[kDevices];
+  static cudaError_t failed[kDevices];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kDevices) return ask<Kernel, Args, Ring>(out);
+  std::call_once(once[dev], [&] { failed[dev] = ask<Kernel, Args, Ring>(&known[dev]); });
+  *out = known[dev];
+  return failed[dev];
 }
 
 // Few sequences: the largest cluster with which all clusters still run at once (a
@@ -853,27 +860,26 @@ int clusters_held(int n) {
 // blocks of 64 channels), forward us by cluster size: 1: 32.6, 2: 30.5, 3: 26.7 (288
 // of 291 places), 4: 31.6, 8: 34.0.
 template <auto Kernel, typename Args, typename Ring>
-Shape shape_of(const Args& a) {
+cudaError_t shape_of(const Args& a, Shape* best) {
+  Held h;
+  const cudaError_t e = held_by<Kernel, Args, Ring>(&h);
+  if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.B) * ((a.D + Ring::kWidth - 1) / Ring::kWidth);
   const int64_t tiles = (static_cast<int64_t>(a.T) + Ring::kTile - 1) / Ring::kTile;
-  const int one = clusters_held<Kernel, Args, Ring>(1);
-  Shape best{1, tiles * (one > 0 ? (units + one - 1) / one : units)};
+  *best = {1, tiles * (h.held[1] > 0 ? (units + h.held[1] - 1) / h.held[1] : units)};
   for (int n = 2; n <= kMaxCluster && n <= tiles; ++n) {
     const int64_t steps = (tiles + n - 1) / n;
-    if (units <= clusters_held<Kernel, Args, Ring>(n) && steps < best.steps) best = {n, steps};
+    if (units <= h.held[n] && steps < best->steps) *best = {n, steps};
   }
-  return best;
+  return cudaSuccess;
 }
 
 template <auto Kernel, typename Args, typename Ring>
 cudaError_t launch(const Args& a, const Maps& maps, int cluster, cudaStream_t st) {
   const int blocks = (a.D + Ring::kWidth - 1) / Ring::kWidth;
   cudaLaunchAttribute attr;
-  cudaError_t e;
   const cudaLaunchConfig_t cfg =
-      config<Args>(Kernel, static_cast<int64_t>(a.B) * blocks * cluster, cluster,
-                   Ring::kBytes + exchange_bytes(cluster, Ring::kWidth / 4), &attr, st, &e);
-  if (e != cudaSuccess) return e;
+      config<Args, Ring>(static_cast<int64_t>(a.B) * blocks * cluster, cluster, &attr, st);
   return cudaLaunchKernelEx(&cfg, Kernel, a, maps, blocks, cluster);
 }
 
@@ -882,7 +888,13 @@ cudaError_t launch(const Args& a, const Maps& maps, int cluster, cudaStream_t st
 template <auto Wide, auto Narrow, typename Args, typename WideRing, typename NarrowRing>
 cudaError_t launch_best(const Args& a, bool (*encode_all)(Maps*, const Args&, int, int),
                         cudaStream_t st, bool* encoded) {
-  const Shape w = shape_of<Wide, Args, WideRing>(a), n = shape_of<Narrow, Args, NarrowRing>(a);
+  Shape w, n;
+  cudaError_t e = shape_of<Wide, Args, WideRing>(a, &w);
+  if (e == cudaSuccess) e = shape_of<Narrow, Args, NarrowRing>(a, &n);
+  if (e != cudaSuccess) {
+    *encoded = true;
+    return e;
+  }
   Maps m;
   if (n.steps < w.steps) {
     *encoded = encode_all(&m, a, NarrowRing::kTile, NarrowRing::kWidth);

@@ -19,8 +19,40 @@ namespace sanatan {
 namespace {
 
 constexpr int kGroup = 64;
-constexpr uint32_t kTiny = 0x0d800000u;  // 2^-100: smaller groups are stored as zeros
-constexpr uint32_t kLarge = 0x7f000000u; // 2^127: there a code times its scale could overflow
+constexpr int kThreads = 256;
+constexpr int kBatch = 8;                             // groups of 16 lanes, loaded together
+constexpr int kPart = kThreads / 16 * kBatch;         // groups of a thread block
+constexpr uint32_t kTiny = 0x0d800000u;   // 2^-100: smaller groups are stored as zeros
+constexpr uint32_t kLarge = 0x7f000000u;  // 2^127: there a code times its scale could overflow
+
+// The integers nearest to the exact quotients v / scale, ties to even, as bytes.
+// fl(v / scale) itself would round a quotient next to a tie to the tie.  v * inv
+// lies within 2e-5 of the quotient, so its nearest integer c (the low bits of v inv
+// + 1.5 2^23) is right or one off, and the remainder v - c scale, exact in one
+// FMA, says which: a remainder of half a scale or more is rare.
+__device__ __forceinline__ uint32_t nearest(const float (&v)[4], float scale) {
+  constexpr float kMagic = 12582912.0f;
+  const float inv = __frcp_rn(scale);
+  uint32_t bits[4];
+  float r[4], most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float t = fmaf(v[i], inv, kMagic);
+    bits[i] = __float_as_uint(t);
+    r[i] = fmaf(kMagic - t, scale, v[i]);
+    most = fmaxf(most, fabsf(r[i]));
+  }
+  if (2.0f * most >= scale) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float two = 2.0f * fabsf(r[i]);
+      if (two > scale || (two == scale && (bits[i] & 1)))
+        bits[i] += r[i] > 0.0f ? 1u : 0xffffffffu;
+    }
+  }
+  return __byte_perm(__byte_perm(bits[0], bits[1], 0x0040), __byte_perm(bits[2], bits[3], 0x0040),
+                     0x5410);
+}
 
 // 16 lanes hold a group, four values each.  A group with a value that is not
 // finite, or is 2^127 or more, has the scale NaN, so that it reads back as NaN.
@@ -39,41 +71,29 @@ __device__ __forceinline__ uint32_t quantise(const float (&v)[4], float& scale) 
     scale = 0.0f;
     return 0;
   }
-  uint32_t word = 0;
   if (F == SANATAN_CACHE_INT8) {
     scale = __fdiv_rn(__uint_as_float(top), 127.0f);
-    const float inv = __frcp_rn(scale);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // v * inv is within 2e-5 of the quotient, so its nearest integer c is right or
-      // one off; the remainder v - c s is exact in one FMA and says which.
-      float c = rintf(v[i] * inv);
-      const float r = fmaf(-c, scale, v[i]);
-      const float two = 2.0f * fabsf(r);
-      if (two > scale || (two == scale && (static_cast<int>(c) & 1))) c += copysignf(1.0f, r);
-      word |= (static_cast<uint32_t>(static_cast<int>(c)) & 0xffu) << (8 * i);
-    }
-  } else {
-    // 448 = 1.75 * 2^8: the exponent of max|x|, less 8, one more where the
-    // mantissa is above 1.75.
-    const uint32_t e = (top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    scale = __uint_as_float(e << 23);
-    const float inv = __uint_as_float((254u - e) << 23);
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    word = lo | (hi << 16);
+    return nearest(v, scale);
   }
-  return word;
+  // 448 = 1.75 * 2^8: the exponent of max|x|, less 8, one more where the mantissa is
+  // above 1.75.
+  const uint32_t e = (top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  scale = __uint_as_float(e << 23);
+  const float inv = __uint_as_float((254u - e) << 23);
+  const uint32_t lo =
+      __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi =
+      __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
 }
 
 template <int F>
 __device__ __forceinline__ void restore(uint32_t word, float scale, float (&v)[4]) {
   if (F == SANATAN_CACHE_INT8) {
+    const uint32_t up = word ^ 0x80808080u;  // codes + 128, the low byte of 2^23 + code + 128
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = static_cast<float>(static_cast<int>(word << (24 - 8 * i)) >> 24) * scale;
+      v[i] = (__uint_as_float(__byte_perm(up, 0x4b000000u, 0x7540 | i)) - 8388736.0f) * scale;
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -86,66 +106,109 @@ __device__ __forceinline__ void restore(uint32_t word, float scale, float (&v)[4
   }
 }
 
-// The page of sequence b, or -1: none, or a later sequence of the call writes it.
-__device__ int64_t page_of(const CacheArgs& a, int b, bool writing) {
+// The page of sequence b, or -1: none, or a later sequence of the call writes it.  By
+// all threads of the block.
+__device__ __forceinline__ int64_t page_of(const CacheArgs& a, int b, bool writing) {
   const int64_t p = a.pages[b];
   if (p < 0 || p >= a.num_pages) return -1;
-  if (writing)
-    for (int i = b + 1; i < a.B; ++i)
-      if (a.pages[i] == p) return -1;
+  if (writing) {
+    bool later = false;
+    for (int i = b + 1 + static_cast<int>(threadIdx.x); i < a.B; i += kThreads)
+      later |= a.pages[i] == p;
+    if (__syncthreads_or(later)) return -1;
+  }
   return p;
 }
 
-template <int F, bool WRITE>
-__global__ void __launch_bounds__(256) cache_kernel(CacheArgs a) {
+// One part (128 groups, 32 KB of values) of a stretch.  The values of all of a
+// thread's groups are under way before the first is used: eight 16-byte loads
+// (VEC, inner a multiple of 4), 16 lanes a group, so that a warp reads 512 and
+// writes 128 neighbouring bytes at a time.
+template <int F, bool WRITE, bool VEC>
+__global__ void __launch_bounds__(kThreads) cache_kernel(const CacheArgs a) {
   const unsigned stretch = blockIdx.x / a.blocks, part = blockIdx.x % a.blocks;
   const int b = static_cast<int>(stretch % a.B), l = static_cast<int>(stretch / a.B);
-  const int64_t p = page_of(a, b, WRITE);
-  if (p < 0) return;
   const int64_t groups = (a.inner + kGroup - 1) / kGroup;
-  const int64_t gi = static_cast<int64_t>(part) * 16 + threadIdx.x / 16;
+  const int64_t g0 = static_cast<int64_t>(part) * kPart + threadIdx.x / 16;
   const int lane = threadIdx.x % 16;
   const int64_t row = static_cast<int64_t>(l) * a.B + b;  // stretch of the state
-  const int64_t at = (p * a.layers + l) * groups + gi;    // group of the cache
-  const bool there = gi < groups;
   float* x = a.state + row * a.inner;
-  uint32_t* code = reinterpret_cast<uint32_t*>(a.codes) + at * 16 + lane;
-  float v[4];
+
   if (WRITE) {
+    float v[kBatch][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t k = gi * kGroup + lane * 4 + i;
-      v[i] = there && k < a.inner ? x[k] : 0.0f;
-    }
-    float scale;
-    const uint32_t word = quantise<F>(v, scale);
-    if (there) {
-      *code = word;
-      if (lane == 0) a.scales[at] = scale;
-    }
-  } else if (there) {
-    restore<F>(*code, a.scales[at], v);
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t k = (g0 + u * (kThreads / 16)) * kGroup + lane * 4;
+      if (VEC) {
+        const float4 f = k < a.inner ? __ldcs(reinterpret_cast<const float4*>(x + k))
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        v[u][0] = f.x;
+        v[u][1] = f.y;
+        v[u][2] = f.z;
+        v[u][3] = f.w;
+      } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t k = gi * kGroup + lane * 4 + i;
-      if (k < a.inner) x[k] = v[i];
+        for (int i = 0; i < 4; ++i) v[u][i] = k + i < a.inner ? x[k + i] : 0.0f;
+      }
+    }
+    const int64_t p = page_of(a, b, true);
+    if (p < 0) return;
+    const int64_t page = (p * a.layers + l) * groups;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t g = g0 + u * (kThreads / 16);
+      float scale;
+      const uint32_t word = quantise<F>(v[u], scale);
+      if (g < groups) {
+        reinterpret_cast<uint32_t*>(a.codes)[(page + g) * 16 + lane] = word;
+        if (lane == 0) a.scales[page + g] = scale;
+      }
+    }
+    for (int64_t k = static_cast<int64_t>(part) * kThreads + threadIdx.x; k < a.exact_inner;
+         k += static_cast<int64_t>(a.blocks) * kThreads)
+      a.exact_cache[(p * a.layers + l) * a.exact_inner + k] = a.exact[row * a.exact_inner + k];
+    return;
+  }
+  const int64_t p = page_of(a, b, false);
+  if (p < 0) return;
+  const int64_t page = (p * a.layers + l) * groups;
+  uint32_t word[kBatch];
+  float scale[kBatch];
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int64_t g = g0 + u * (kThreads / 16);
+    if (g < groups) {
+      word[u] = reinterpret_cast<const uint32_t*>(a.codes)[(page + g) * 16 + lane];
+      scale[u] = a.scales[page + g];
     }
   }
-  // the values kept in float32, by the same blocks
-  for (int64_t k = static_cast<int64_t>(part) * 256 + threadIdx.x; k < a.exact_inner;
-       k += static_cast<int64_t>(a.blocks) * 256) {
-    float* z = a.exact + row * a.exact_inner + k;
-    float* c = a.exact_cache + (p * a.layers + l) * a.exact_inner + k;
-    if (WRITE)
-      *c = *z;
-    else
-      *z = *c;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int64_t g = g0 + u * (kThreads / 16), k = g * kGroup + lane * 4;
+    if (g < groups) {
+      float v[4];
+      restore<F>(word[u], scale[u], v);
+      if (VEC) {
+        if (k < a.inner) *reinterpret_cast<float4*>(x + k) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (k + i < a.inner) x[k + i] = v[i];
+      }
+    }
   }
+  for (int64_t k = static_cast<int64_t>(part) * kThreads + threadIdx.x; k < a.exact_inner;
+       k += static_cast<int64_t>(a.blocks) * kThreads)
+    a.exact[row * a.exact_inner + k] = a.exact_cache[(p * a.layers + l) * a.exact_inner + k];
 }
 
 template <int F, bool WRITE>
-cudaError_t launch(CacheArgs a, cudaStream_t st) {
-  cache_kernel<F, WRITE><<<a.blocks * a.layers * a.B, 256, 0, st>>>(a);
+cudaError_t launch(const CacheArgs& a, cudaStream_t st) {
+  const unsigned grid = a.blocks * static_cast<unsigned>(a.layers) * static_cast<unsigned>(a.B);
+  if (a.inner % 4 == 0)
+    cache_kernel<F, WRITE, true><<<grid, kThreads, 0, st>>>(a);
+  else
+    cache_kernel<F, WRITE, false><<<grid, kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -153,7 +216,7 @@ cudaError_t launch(CacheArgs a, cudaStream_t st) {
 
 int64_t state_cache_blocks(int64_t inner) {
   const int64_t groups = (inner + kGroup - 1) / kGroup;
-  return groups < 16 ? 1 : (groups + 15) / 16;
+  return groups < kPart ? 1 : (groups + kPart - 1) / kPart;
 }
 
 cudaError_t state_cache_launch(const CacheArgs& a, bool write, cudaStream_t st) {

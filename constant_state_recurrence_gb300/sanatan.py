@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "lib", "libsanatan.so")
 SANATAN_F32 = 0
 SANATAN_BF16 = 1
 _DT = {torch.float32: SANATAN_F32, torch.bfloat16: SANATAN_BF16}
+_FLOATS = (torch.float32, torch.bfloat16)
 
 _c_int, _c_i64, _c_f, _c_sz, _c_p = (ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                                      ctypes.c_size_t, ctypes.c_void_p)
@@ -753,31 +754,43 @@ def _gate(gate):
     return SCAN_GATES[gate]
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _fit(t, name, dtype, shape, dev):
+    """t on the device, contiguous, of this type and shape (_need's checks, the
+    usual answer first: small calls are bound by the host)."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape and \
+            t.device == dev and t.is_contiguous():
+        return t
+    _need(t, name, (dtype,), shape)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return t
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _call(name, dev, *args):
     """Call a library function with the tensors' device current, on its stream."""
     fn = getattr(lib(), name)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, _stream(dev))
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(dev))
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     _check(name, st)
 
 
-def _scan_args(x, g, gate, lens):
-    _need(x, "x", (torch.float32, torch.bfloat16))
-    if x.dim() != 3:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, T, D]")
-    _need(g, "g", (x.dtype,), x.shape)
+def _scan_args(x, g, gate, lens, dims):
+    """x, g and lens fit; returns (x's shape, device, dtype code, gate code)."""
+    _need(x, "x", _FLOATS)
+    if x.dim() != dims:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected {dims} dimensions")
+    shape, dev = x.shape, x.device
+    _fit(g, "g", x.dtype, shape, dev)
     if lens is not None:
-        _need(lens, "lens", (torch.int64,), (x.shape[0],))
-    return _gate(gate)
+        _fit(lens, "lens", torch.int64, (shape[0],), dev)
+    return shape, dev, _DT[x.dtype], _gate(gate)
 
 
 def sanatan_gated_scan_fwd(x, g, gate="log", h0=None, lens=None, want_state=False,
@@ -789,54 +802,45 @@ def sanatan_gated_scan_fwd(x, g, gate="log", h0=None, lens=None, want_state=Fals
 
     Returns (y [B,T,D] in x's dtype, the last state [B,D] f32 or None, marks
     [B, ceil(T/64), D] f32 (states for the backward) or None)."""
-    gt = _scan_args(x, g, gate, lens)
-    B, T, D = x.shape
-    dev = x.device
-    y = torch.empty_like(x) if out is None else _need(out, "out", (x.dtype,), x.shape)
+    (B, T, D), dev, dt, gt = _scan_args(x, g, gate, lens, 3)
+    y = torch.empty_like(x) if out is None else _fit(out, "out", x.dtype, x.shape, dev)
     if h0 is not None:
-        _need(h0, "h0", (torch.float32,), (B, D))
+        _fit(h0, "h0", torch.float32, (B, D), dev)
     if h_out is not None:
-        _need(h_out, "h_out", (torch.float32,), (B, D))
+        _fit(h_out, "h_out", torch.float32, (B, D), dev)
     elif want_state:
         h_out = torch.empty(B, D, dtype=torch.float32, device=dev)
     marks = torch.empty(B, -(-T // SCAN_MARK), D, dtype=torch.float32, device=dev) \
         if want_marks else None
-    _same_device(dev, g=g, h0=h0, lens=lens, out=y, h_out=h_out)
-    _call("sanatan_gated_scan_fwd", dev, _ptr(x), _ptr(g), _DT[x.dtype], gt, _ptr(lens), B, T, D,
-          _ptr(h0), _ptr(y), _ptr(h_out), _ptr(marks))
+    _call("sanatan_gated_scan_fwd", dev, x.data_ptr(), g.data_ptr(), dt, gt, _at(lens), B, T, D,
+          _at(h0), y.data_ptr(), _at(h_out), _at(marks))
     return y, h_out, marks
 
 
 def sanatan_gated_scan_bwd(x, g, dy, marks, gate="log", lens=None, dh_last=None, want_dh0=False):
     """Gradients of sum(y * dy) + sum(h_last * dh_last) for
     sanatan_gated_scan_fwd: dict(dx, dg, dh0); marks are the forward's."""
-    gt = _scan_args(x, g, gate, lens)
-    B, T, D = x.shape
-    dev = x.device
-    _need(dy, "dy", (x.dtype,), x.shape)
-    _need(marks, "marks", (torch.float32,), (B, -(-T // SCAN_MARK), D))
+    (B, T, D), dev, dt, gt = _scan_args(x, g, gate, lens, 3)
+    _fit(dy, "dy", x.dtype, x.shape, dev)
+    _fit(marks, "marks", torch.float32, (B, -(-T // SCAN_MARK), D), dev)
     if dh_last is not None:
-        _need(dh_last, "dh_last", (torch.float32,), (B, D))
-    _same_device(dev, g=g, dy=dy, marks=marks, lens=lens, dh_last=dh_last)
+        _fit(dh_last, "dh_last", torch.float32, (B, D), dev)
     dx, dg = torch.empty_like(x), torch.empty_like(g)
     dh0 = torch.empty(B, D, dtype=torch.float32, device=dev) if want_dh0 else None
-    _call("sanatan_gated_scan_bwd", dev, _ptr(x), _ptr(g), _ptr(dy), _DT[x.dtype], gt, _ptr(lens),
-          B, T, D, _ptr(marks), _ptr(dh_last), _ptr(dx), _ptr(dg), _ptr(dh0))
+    _call("sanatan_gated_scan_bwd", dev, x.data_ptr(), g.data_ptr(), dy.data_ptr(), dt, gt,
+          _at(lens), B, T, D, marks.data_ptr(), _at(dh_last), dx.data_ptr(), dg.data_ptr(),
+          _at(dh0))
     return dict(dx=dx, dg=dg, dh0=dh0)
 
 
 def sanatan_gated_scan_step(h, x, g, gate="log", out=None):
     """One token of the gated recurrence for N sequences: h [N, D] f32 is
     updated in place, x and g [N, D] f32 or bf16.  Returns y [N, D]."""
-    _need(x, "x", (torch.float32, torch.bfloat16))
-    if x.dim() != 2:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [N, D]")
-    _need(g, "g", (x.dtype,), x.shape)
-    _need(h, "h", (torch.float32,), x.shape)
-    y = torch.empty_like(x) if out is None else _need(out, "out", (x.dtype,), x.shape)
-    _same_device(x.device, h=h, g=g, out=y)
-    _call("sanatan_gated_scan_step", x.device, _ptr(h), _ptr(x), _ptr(g), _DT[x.dtype],
-          _gate(gate), x.shape[0], x.shape[1], _ptr(y))
+    (N, D), dev, dt, gt = _scan_args(x, g, gate, None, 2)
+    _fit(h, "h", torch.float32, x.shape, dev)
+    y = torch.empty_like(x) if out is None else _fit(out, "out", x.dtype, x.shape, dev)
+    _call("sanatan_gated_scan_step", dev, h.data_ptr(), x.data_ptr(), g.data_ptr(), dt, gt, N, D,
+          y.data_ptr())
     return y
 
 
@@ -867,34 +871,38 @@ class GatedScan(torch.autograd.Function):
         return d["dx"], d["dg"], None, d["dh0"], None
 
 
+def _stretch(t, name, layers, B):
+    """Values of one sequence's layer in t, read as [layers, B, ...]."""
+    n, total = layers * B, t.numel()
+    if n == 0 and total == 0:
+        return 0
+    if n == 0 or total % n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: not {layers} layers of {B} "
+                         "sequences")
+    return total // n
+
+
 def _cache_args(state, pages, codes, scales, z, z_cache, layers, name):
     """Checks shared by the two directions; returns (B, inner, z's inner, P, format)."""
     _need(state, name, (torch.float32,))
-    _need(pages, "pages", (torch.int64,))
-    _need(codes, "codes", tuple(_CACHE_FMT))
-    if pages.dim() != 1 or codes.dim() != 4:
-        raise ValueError("pages must be [B] and codes [P, layers, groups, 64]")
+    dev = state.device
+    if layers < 1 or pages.dim() != 1 or codes.dim() != 4 or codes.dtype not in _CACHE_FMT:
+        raise ValueError("layers must be 1 or more, pages [B] and codes [P, layers, groups, 64] "
+                         f"of a type in {tuple(_CACHE_FMT)}")
     B, P = pages.shape[0], codes.shape[0]
-    n = int(layers) * B
-    if layers < 1 or (n and state.numel() % n) or (not n and state.numel()):
-        raise ValueError(f"{name} has shape {tuple(state.shape)}: not {layers} layers of {B} "
-                         "sequences")
-    inner = state.numel() // n if n else 0
-    groups = -(-inner // CACHE_GROUP)
-    if n:
-        _need(codes, "codes", None, (P, layers, groups, CACHE_GROUP))
-        _need(scales, "scales", (torch.float32,), (P, layers, groups))
+    _fit(pages, "pages", torch.int64, (B,), dev)
+    inner, zi = _stretch(state, name, layers, B), 0
+    if B:
+        groups = -(-inner // CACHE_GROUP)
+        _fit(codes, "codes", codes.dtype, (P, layers, groups, CACHE_GROUP), dev)
+        _fit(scales, "scales", torch.float32, (P, layers, groups), dev)
     if (z is None) != (z_cache is None):
         raise ValueError("z and z_cache go together")
-    zi = 0
     if z is not None:
-        _need(z, "z", (torch.float32,))
-        if (n and z.numel() % n) or (not n and z.numel()):
-            raise ValueError(f"z has shape {tuple(z.shape)}: not {layers} layers of {B} sequences")
-        zi = z.numel() // n if n else 0
-        if n:
-            _need(z_cache, "z_cache", (torch.float32,), (P, layers, zi))
-    _same_device(state.device, pages=pages, codes=codes, scales=scales, z=z, z_cache=z_cache)
+        _fit(z, "z", torch.float32, z.shape, dev)
+        zi = _stretch(z, "z", layers, B)
+        if B:
+            _fit(z_cache, "z_cache", torch.float32, (P, layers, zi), dev)
     return B, inner, zi, P, _CACHE_FMT[codes.dtype]
 
 
@@ -920,8 +928,8 @@ def sanatan_state_cache_write(state, pages, codes, scales, z=None, z_cache=None,
     int64, where a value outside the pool leaves the sequence out.  See
     include/sanatan.h for the formats."""
     B, inner, zi, P, fmt = _cache_args(state, pages, codes, scales, z, z_cache, layers, "state")
-    _call("sanatan_state_cache_write", state.device, _ptr(state), _ptr(z), layers, B, inner, zi,
-          _ptr(pages), P, fmt, _ptr(codes), _ptr(scales), _ptr(z_cache))
+    _call("sanatan_state_cache_write", state.device, state.data_ptr(), _at(z), layers, B, inner,
+          zi, pages.data_ptr(), P, fmt, codes.data_ptr(), scales.data_ptr(), _at(z_cache))
 
 
 def sanatan_state_cache_read(codes, scales, pages, state, z_cache=None, z=None, layers=1):
@@ -930,8 +938,8 @@ def sanatan_state_cache_read(codes, scales, pages, state, z_cache=None, z=None, 
     several sequences; sequences whose page is outside the pool keep what state
     holds.  Returns state."""
     B, inner, zi, P, fmt = _cache_args(state, pages, codes, scales, z, z_cache, layers, "state")
-    _call("sanatan_state_cache_read", state.device, _ptr(codes), _ptr(scales), _ptr(z_cache), P,
-          fmt, _ptr(pages), layers, B, inner, zi, _ptr(state), _ptr(z))
+    _call("sanatan_state_cache_read", state.device, codes.data_ptr(), scales.data_ptr(),
+          _at(z_cache), P, fmt, pages.data_ptr(), layers, B, inner, zi, state.data_ptr(), _at(z))
     return state
 
 
