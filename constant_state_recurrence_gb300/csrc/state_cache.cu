@@ -32,7 +32,8 @@ constexpr uint32_t kLarge = 0x7f000000u;  // 2^127: there a code times its scale
 // FMA, says which: a remainder of half a scale or more is rare.
 __device__ __forceinline__ uint32_t nearest(const float (&v)[4], float scale) {
   constexpr float kMagic = 12582912.0f;
-  const float inv = __frcp_rn(scale);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
   uint32_t bits[4];
   float r[4], most = 0.0f;
 #pragma unroll
@@ -72,7 +73,12 @@ __device__ __forceinline__ uint32_t quantise(const float (&v)[4], float& scale) 
     return 0;
   }
   if (F == SANATAN_CACHE_INT8) {
-    scale = __fdiv_rn(__uint_as_float(top), 127.0f);
+    // top / 127 rounded: with the rounded reciprocal y of 127 and q = fl(top y), the
+    // remainder r = top - 127 q is exact and fl(q + r y) is the rounded quotient
+    // (Markstein's theorem).
+    constexpr float y = 1.0f / 127.0f;
+    const float t = __uint_as_float(top), q = t * y;
+    scale = fmaf(fmaf(-127.0f, q, t), y, q);
     return nearest(v, scale);
   }
   // 448 = 1.75 * 2^8: the exponent of max|x|, less 8, one more where the mantissa is

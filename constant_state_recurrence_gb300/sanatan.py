@@ -771,14 +771,16 @@ def _at(t):
 
 
 def _call(name, dev, *args):
-    """Call a library function with the tensors' device current, on its stream."""
+    """Call a library function with the tensors' device current, on its stream
+    (asked for raw: a Stream object costs as much as the launch)."""
     fn = getattr(lib(), name)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(name, st)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        raise SanatanError(name, st)
 
 
 def _scan_args(x, g, gate, lens, dims):
