@@ -19,9 +19,9 @@ namespace sanatan {
 namespace {
 
 constexpr int kGroup = 64;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kBatch = 8;                             // groups of 16 lanes, loaded together
-constexpr int kPart = kThreads / 16 * kBatch;         // groups of a thread block
+constexpr int kPart = kThreads / 16 * kBatch;         // groups of a thread block: 64
 constexpr uint32_t kTiny = 0x0d800000u;   // 2^-100: smaller groups are stored as zeros
 constexpr uint32_t kLarge = 0x7f000000u;  // 2^127: there a code times its scale could overflow
 
@@ -126,7 +126,7 @@ __device__ __forceinline__ int64_t page_of(const CacheArgs& a, int b, bool writi
   return p;
 }
 
-// One part (128 groups, 32 KB of values) of a stretch.  The values of all of a
+// One part (64 groups, 16 KB of values) of a stretch.  The values of all of a
 // thread's groups are under way before the first is used: eight 16-byte loads
 // (VEC, inner a multiple of 4), 16 lanes a group, so that a warp reads 512 and
 // writes 128 neighbouring bytes at a time.
