@@ -126,6 +126,14 @@ __device__ __forceinline__ void gate(const V4& g, V4& a, V4& keep) {
   }
 }
 
+// Programmatic dependent launch: the kernel starts while the one before it in the
+// stream ends, and touches memory only after that one's results are visible; the next
+// one may start as soon as every CTA of this one runs.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
   if (lens == nullptr) return T;
   const int64_t n = lens[b];
@@ -423,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_fwd_kernel(
   const int tid = threadIdx.x, lane = tid % LANES, warp = tid >> 5;
   const int T = p.T, D = p.D;
   const Place<LANES, TMA> place{(unit % blocks) * 4 * LANES, lane, D};
+  wait_for_previous();
   const int len = length_of(p.lens, b, T);
   const int tiles = (T + kTile - 1) / kTile;
   const int steps = (tiles + cluster_size - 1) / cluster_size;
@@ -566,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_bwd_kernel(
   const int tid = threadIdx.x, lane = tid % LANES, warp = tid >> 5;
   const int T = p.T, D = p.D;
   const Place<LANES, TMA> place{(unit % blocks) * 4 * LANES, lane, D};
+  wait_for_previous();
   const int len = length_of(p.lens, b, T);
   const int tiles = (T + kTile - 1) / kTile;
   const int steps = (tiles + cluster_size - 1) / cluster_size;
@@ -736,6 +746,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(float* __restrict__
   using QF = Quad<float>;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t quads = n / 4;
+  wait_for_previous();
   V4 gv, xv, hv;
   const int64_t last = 4 * quads + (i - quads);
   if (i < quads) {
@@ -817,8 +828,10 @@ cudaLaunchConfig_t config(int64_t ctas, int cluster, cudaLaunchAttribute* attr, 
   attr->val.clusterDim.x = cluster;
   attr->val.clusterDim.y = 1;
   attr->val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -836,8 +849,8 @@ cudaError_t ask(Held* out) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   for (int n = 1; e == cudaSuccess && n <= kMaxCluster; ++n) {
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config<Args, Ring>(n, n, &attr, nullptr);
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config<Args, Ring>(n, n, attr, nullptr);
     if (cudaOccupancyMaxActiveClusters(&out->held[n], Kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
       out->held[n] = 0;
@@ -883,9 +896,9 @@ cudaError_t shape_of(const Args& a, Shape* best) {
 template <auto Kernel, typename Args, typename Ring>
 cudaError_t launch(const Args& a, const Maps& maps, int cluster, cudaStream_t st) {
   const int blocks = (a.D + Ring::kWidth - 1) / Ring::kWidth;
-  cudaLaunchAttribute attr;
+  cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg =
-      config<Args, Ring>(static_cast<int64_t>(a.B) * blocks * cluster, cluster, &attr, st);
+      config<Args, Ring>(static_cast<int64_t>(a.B) * blocks * cluster, cluster, attr, st);
   return cudaLaunchKernelEx(&cfg, Kernel, a, maps, blocks, cluster);
 }
 
@@ -961,10 +974,17 @@ cudaError_t bwd(const ScanBwdArgs& a, cudaStream_t st) {
 template <typename E, int G>
 cudaError_t step(float* h, const void* x, const void* g, int64_t n, void* y, cudaStream_t st) {
   const int64_t threads = n / 4 + n % 4;
-  scan_step_kernel<E, G><<<static_cast<unsigned>((threads + kThreads - 1) / kThreads), kThreads, 0,
-                           st>>>(
-      h, static_cast<const E*>(x), static_cast<const E*>(g), n, static_cast<E*>(y));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, scan_step_kernel<E, G>, h, static_cast<const E*>(x),
+                            static_cast<const E*>(g), n, static_cast<E*>(y));
 }
 
 }  // namespace
