@@ -31,6 +31,7 @@
 #include <mutex>
 
 #include "f32x2.cuh"
+#include "pdl.cuh"
 #include "sanatan_internal.h"
 #include "sanatan_math.cuh"
 #include "tc_ptx.cuh"
@@ -124,14 +125,6 @@ __device__ __forceinline__ void gate(const V4& g, V4& a, V4& keep) {
     a = v4(rcp(s[0]), rcp(s[1]), rcp(s[2]), rcp(s[3]));
     keep = mul(e, a);
   }
-}
-
-// Programmatic dependent launch: the kernel starts while the one before it in the
-// stream ends, and touches memory only after that one's results are visible; the next
-// one may start as soon as every CTA of this one runs.
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
@@ -708,8 +701,12 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_bwd_kernel(
       h = fma(a[r], h, G == SANATAN_GATE_LOG ? x[r] : mul(keep[r], x[r]));
     }
     V4 d = fma(rA, ex.in_p[warp][lane], rP);
+    const int64_t last = (static_cast<int64_t>(t0) + R - 1) * D;
+    E* to_x = dx + last;
+    E* to_g = dg + last;
+    const bool whole = t0 + R <= len;
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
+    for (int r = R - 1; r >= 0; --r, to_x -= D, to_g -= D) {
       const V4 dh = fma(d, v4(1.0f), dy[r]);
       d = mul(a[r], dh);
       V4 ox = dh, og;
@@ -719,10 +716,12 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_bwd_kernel(
         ox = mul(dh, keep[r]);
         og = mul(dh, mul(sub(before[r], x[r]), mul(a[r], keep[r])));
       }
-      if (t0 + r < T) {
-        const bool there = t0 + r < len;
-        place.store(dx + (static_cast<int64_t>(t0) + r) * D, select(there, ox, v4(0.0f)));
-        place.store(dg + (static_cast<int64_t>(t0) + r) * D, select(there, og, v4(0.0f)));
+      if (whole) {
+        place.store(to_x, ox);
+        place.store(to_g, og);
+      } else if (t0 + r < T) {
+        place.store(to_x, select(t0 + r < len, ox, v4(0.0f)));
+        place.store(to_g, select(t0 + r < len, og, v4(0.0f)));
       }
     }
     if (++slot == kStages) {
@@ -828,8 +827,7 @@ cudaLaunchConfig_t config(int64_t ctas, int cluster, cudaLaunchAttribute* attr, 
   attr->val.clusterDim.x = cluster;
   attr->val.clusterDim.y = 1;
   attr->val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[1] = pdl_attribute();
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cfg;
@@ -978,10 +976,8 @@ cudaError_t step(float* h, const void* x, const void* g, int64_t n, void* y, cud
   cfg.gridDim = dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
+  cudaLaunchAttribute attr = pdl_attribute();
+  cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, scan_step_kernel<E, G>, h, static_cast<const E*>(x),
                             static_cast<const E*>(g), n, static_cast<E*>(y));

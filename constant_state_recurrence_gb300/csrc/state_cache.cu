@@ -13,6 +13,7 @@
 // output is divided by Phi(q) . z, and they are 1/64 of the values.
 #include <cuda_fp8.h>
 
+#include "pdl.cuh"
 #include "sanatan_internal.h"
 
 namespace sanatan {
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const CacheArgs a) {
   const int lane = threadIdx.x % 16;
   const int64_t row = static_cast<int64_t>(l) * a.B + b;  // stretch of the state
   float* x = a.state + row * a.inner;
+  wait_for_previous();
 
   if (WRITE) {
     float v[kBatch][4];
@@ -210,12 +212,15 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const CacheArgs a) {
 
 template <int F, bool WRITE>
 cudaError_t launch(const CacheArgs& a, cudaStream_t st) {
-  const unsigned grid = a.blocks * static_cast<unsigned>(a.layers) * static_cast<unsigned>(a.B);
-  if (a.inner % 4 == 0)
-    cache_kernel<F, WRITE, true><<<grid, kThreads, 0, st>>>(a);
-  else
-    cache_kernel<F, WRITE, false><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.blocks * static_cast<unsigned>(a.layers) * static_cast<unsigned>(a.B));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = pdl_attribute();
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return a.inner % 4 == 0 ? cudaLaunchKernelEx(&cfg, cache_kernel<F, WRITE, true>, a)
+                          : cudaLaunchKernelEx(&cfg, cache_kernel<F, WRITE, false>, a);
 }
 
 }  // namespace
