@@ -439,9 +439,10 @@ int sanatan_device_status(void* stream) {
   const int hp = pow_tc_read_and_clear_error(static_cast<cudaStream_t>(stream));
   const int hpb = pow_bwd_tc_read_and_clear_error(static_cast<cudaStream_t>(stream));
   const int hs = stack_read_and_clear_error(static_cast<cudaStream_t>(stream));
-  const int hg = scan_read_and_clear_error(static_cast<cudaStream_t>(stream));
-  if (h < 0 || hb < 0 || hp < 0 || hpb < 0 || hs < 0 || hg < 0) return SANATAN_ERR_CUDA;
-  if (hb || hp || hpb || hs || hg) return SANATAN_ERR_TIMEOUT;
+  const int hg = scan_fwd_read_and_clear_error(static_cast<cudaStream_t>(stream));
+  const int hgb = scan_bwd_read_and_clear_error(static_cast<cudaStream_t>(stream));
+  if (h < 0 || hb < 0 || hp < 0 || hpb < 0 || hs < 0 || hg < 0 || hgb < 0) return SANATAN_ERR_CUDA;
+  if (hb || hp || hpb || hs || hg || hgb) return SANATAN_ERR_TIMEOUT;
   return h ? SANATAN_ERR_TIMEOUT : SANATAN_OK;
 }
 

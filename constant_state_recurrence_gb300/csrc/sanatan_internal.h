@@ -217,7 +217,7 @@ cudaError_t pow_bwd_tc_launch(const PowBwdArgs& a, cudaStream_t st);
 int pow_bwd_tc_read_and_clear_error(cudaStream_t st);
 int pow_tc_read_and_clear_error(cudaStream_t st);
 
-// Gated linear recurrence over [B, T, D] (gated_scan.cu).
+// Gated linear recurrence over [B, T, D] (gated_scan_fwd.cu, gated_scan_bwd.cu).
 constexpr int kScanMark = 64;  // tokens between two marks (saved states)
 struct ScanArgs {
   const void* x = nullptr;
@@ -244,7 +244,8 @@ struct ScanBwdArgs {
   float* dh0 = nullptr;           // [B, D] or null
 };
 cudaError_t gated_scan_fwd_launch(const ScanArgs& a, cudaStream_t st);
-int scan_read_and_clear_error(cudaStream_t st);
+int scan_fwd_read_and_clear_error(cudaStream_t st);
+int scan_bwd_read_and_clear_error(cudaStream_t st);
 cudaError_t gated_scan_bwd_launch(const ScanBwdArgs& a, cudaStream_t st);
 cudaError_t gated_scan_step_launch(float* h, const void* x, const void* g, int dtype, int gate,
                                    int64_t n, void* y, cudaStream_t st);
