@@ -104,19 +104,31 @@ __device__ __forceinline__ float at_most(float x, float most) {
   return r;
 }
 
-// a and 1 - a of four gate values.  The hardware's powers of two are as near
-// as expf while |g| < 1 (mean error -0.3 to 0.2, r.m.s. 0.7 steps of 2^-24 either
-// way, so that long memories keep their digits); beyond, the rounded argument
-// costs |g| steps of a decay that is small.  Sigmoid: with e = exp(-g) the sides are
-// 1 / (1 + e) and e / (1 + e), each with all its digits, also where the other is
-// next to 1 (for g in 1 ... 10 the decay's mean error is 0.02, its r.m.s. 0.7 steps);
-// e stops at 2^126, so that neither is 0 times infinity: decays are at least 2^-126.
+// a and 1 - a of four gate values.  A memory of n tokens multiplies the mean error of
+// the decays by n, so decays next to 1 need more than the hardware's power of two,
+// which is 0.3 steps of 2^-24 low there.  Log gate: exp(g) is the sum of its first five
+// terms while |g| < 1/16 (the next is below 2^-27), the power of two beyond, where the
+// rounded argument costs |g| steps of a small decay.  Sigmoid: with e = exp(-g) the
+// sides are 1 / (1 + e) and e / (1 + e), each with all its digits, also where the
+// other is next to 1 (for g in 1 ... 10 the decay's mean error is 0.02, its r.m.s. 0.7
+// steps); e stops at 2^126, so that neither is 0 times infinity: decays are at least
+// 2^-126.
 template <int G>
 __device__ __forceinline__ void gate(const V4& g, V4& a, V4& keep) {
   float t[4];
   if (G == SANATAN_GATE_LOG) {
+    const V4 one = v4(1.0f);
+    V4 sum = fma(g, v4(1.0f / 24), v4(1.0f / 6));
+    sum = fma(sum, g, v4(0.5f));
+    sum = fma(sum, g, one);
+    sum = fma(sum, g, one);
+    float near[4], f[4];
     get(mul(g, v4(kLog2e)), t);
-    a = v4(ex2(t[0]), ex2(t[1]), ex2(t[2]), ex2(t[3]));
+    get(sum, near);
+    get(g, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = fabsf(f[j]) < 0.0625f ? near[j] : ex2(t[j]);
+    a = v4(t[0], t[1], t[2], t[3]);
   } else {
     get(mul(g, v4(-kLog2e)), t);
 #pragma unroll
