@@ -57,6 +57,17 @@ int check_scan(int dtype, int gate, int B, int T, int D) {
   return SANATAN_OK;
 }
 
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// Whether two ranges share bytes (null: no range).
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
 // Argument checks and launch of the state cache's two directions.
 int state_cache(float* state, float* exact, int layers, int B, int64_t inner, int64_t exact_inner,
                 const int64_t* pages, int64_t num_pages, int fmt, void* codes, float* scales,
@@ -76,7 +87,8 @@ int state_cache(float* state, float* exact, int layers, int B, int64_t inner, in
     return SANATAN_ERR_UNSUPPORTED;
   const int64_t blocks = state_cache_blocks(inner);
   if (blocks > most / (static_cast<int64_t>(layers) * B)) return SANATAN_ERR_UNSUPPORTED;
-  if (static_cast<double>(num_pages) * layers * (inner + exact_inner + 64.0) > 1e18)
+  if (static_cast<double>(num_pages) * layers * (inner + exact_inner + 64.0) > 1e18 ||
+      static_cast<double>(B) * layers * (inner + exact_inner + 64.0) > 1e18)
     return SANATAN_ERR_UNSUPPORTED;
   if (int s = check_arch()) return s;
   CacheArgs a;
@@ -617,6 +629,19 @@ int sanatan_gated_scan_fwd(const void* x, const void* g, int dtype, int gate, co
   if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
   if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || !ok_ptr(y))) return SANATAN_ERR_INVALID;
   if (T == 0 && h_out == nullptr) return SANATAN_OK;
+  const size_t state = static_cast<size_t>(B) * D * 4;
+  const size_t all = static_cast<size_t>(B) * T * D * (dtype == SANATAN_F32 ? 4 : 2);
+  const size_t nm = sanatan_gated_scan_marks_size(B, T, D);
+  const size_t len = static_cast<size_t>(B) * 8;
+  const Range in[] = {{x, all}, {g, all}, {lens, len}, {h0, state}};
+  const Range out[] = {{y, all}, {marks, nm}, {h_out, state}};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 4; ++i)  // (h_out may be h0)
+      if (overlap(out[o].p, out[o].n, in[i].p, in[i].n) && !(o == 2 && i == 3 && h_out == h0))
+        return SANATAN_ERR_INVALID;
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o].p, out[o].n, out[i].p, out[i].n)) return SANATAN_ERR_INVALID;
+  }
   if (int s = check_arch()) return s;
   ScanArgs a;
   a.x = x;
@@ -644,6 +669,19 @@ int sanatan_gated_scan_bwd(const void* x, const void* g, const void* dy, int dty
                 !ok_ptr(dg)))
     return SANATAN_ERR_INVALID;
   if (T == 0 && dh0 == nullptr) return SANATAN_OK;
+  const size_t state = static_cast<size_t>(B) * D * 4;
+  const size_t all = static_cast<size_t>(B) * T * D * (dtype == SANATAN_F32 ? 4 : 2);
+  const size_t nm = sanatan_gated_scan_marks_size(B, T, D);
+  const size_t len = static_cast<size_t>(B) * 8;
+  const Range in[] = {{x, all}, {g, all}, {dy, all}, {lens, len}, {marks, nm}, {dh_out, state}};
+  const Range out[] = {{dx, all}, {dg, all}, {dh0, state}};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 6; ++i)  // (dh0 may be dh_out)
+      if (overlap(out[o].p, out[o].n, in[i].p, in[i].n) && !(o == 2 && i == 5 && dh0 == dh_out))
+        return SANATAN_ERR_INVALID;
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o].p, out[o].n, out[i].p, out[i].n)) return SANATAN_ERR_INVALID;
+  }
   if (int s = check_arch()) return s;
   ScanBwdArgs a;
   a.x = x;
@@ -669,6 +707,11 @@ int sanatan_gated_scan_step(float* h, const void* x, const void* g, int dtype, i
   const int64_t n = static_cast<int64_t>(N) * D;
   if (n == 0) return SANATAN_OK;
   if (!ok_ptr(h) || !ok_ptr(x) || !ok_ptr(g) || !ok_ptr(y)) return SANATAN_ERR_INVALID;
+  const size_t all = static_cast<size_t>(n) * (dtype == SANATAN_F32 ? 4 : 2);
+  const size_t state = static_cast<size_t>(n) * 4;
+  if (overlap(y, all, x, all) || overlap(y, all, g, all) || overlap(y, all, h, state) ||
+      overlap(h, state, x, all) || overlap(h, state, g, all))
+    return SANATAN_ERR_INVALID;
   if (int s = check_arch()) return s;
   return from_cuda(gated_scan_step_launch(h, x, g, dtype, gate, n, y,
                                           static_cast<cudaStream_t>(stream)));

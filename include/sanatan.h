@@ -440,8 +440,8 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  * attention); the pages give no formula for a gate, these are the plain ones.
  *   x, g    [B, T, D]  dtype;   y [B, T, D] dtype (the float32 state rounded once)
  *   lens    [B] int64 or NULL: tokens of each sequence (values outside [0, T]
- *           are taken as the nearest of the two).  Tokens from lens[b] on are
- *           not read; their y, dx and dg are written as zeros, and the state
+ *           are taken as the nearest of the two).  Tokens from lens[b] on
+ *           have no effect; their y, dx and dg are written as zeros, and the state
  *           passes them unchanged.  NULL: all T tokens.
  *   h0      [B, D] f32 or NULL (zero): the state before the first token
  *   h_out   [B, D] f32 or NULL: the state after the last token
@@ -466,8 +466,9 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  *   in place, x, g, y [N, D] dtype.
  * Errors: SANATAN_ERR_INVALID for an unknown dtype or gate, a negative size, a
  * null (where not allowed) or misaligned pointer; SANATAN_ERR_UNSUPPORTED for
- * B * D (N * D) of 2^31 or more or T above 2^30.  Outputs must not overlap inputs (the step's h
- * excepted).
+ * B * D (N * D) of 2^31 or more or T above 2^30.  Outputs share no bytes with
+ * inputs or each other (SANATAN_ERR_INVALID), except that h_out may be h0 and dh0
+ * may be dh_out.
  */
 SANATAN_API size_t sanatan_gated_scan_marks_size(int B, int T, int D);
 SANATAN_API int sanatan_gated_scan_fwd(const void* x, const void* g, int dtype, int gate,

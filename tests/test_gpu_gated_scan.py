@@ -10,6 +10,10 @@ every token adds a multiplication and an addition, and a scan in pieces at most
 bounds the state's error up to 40 e Hm_t, and the same in reverse time bounds
 dh's.  Products of both add up.  An output in bf16 is off by half a step more,
 2^-8 of its value (float32: 2^-24); 1e-36 stands for underflow."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -380,6 +384,78 @@ def test_captured_training_step_replays_with_new_inputs():
     assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_states_updated_in_place():
+    """h_out may be h0 (and dh0 dh_last): a serving state that stays where it is."""
+    for B, T, D in ((1, 4000, 64), (3, 700, 100), (40, 3, 768)):
+        x, g, dy, h, dh = (t.to(dev()) for t in make(B, T, D, F32, "log", T))
+        y, last, marks = S.sanatan_gated_scan_fwd(x, g, h0=h, want_state=True, want_marks=True)
+        state = h.clone()
+        y2, _, _ = S.sanatan_gated_scan_fwd(x, g, h0=state, h_out=state)
+        assert torch.equal(y, y2) and torch.equal(last, state)
+
+
+def test_captured_on_joined_streams():
+    """A scan that depends on two branches of a graph, and one that two depend on."""
+    x, g, _, h, _ = (t.to(dev()) for t in make(2, 500, 64, F32, "sigmoid", 24))
+    a, b = x.clone(), g.clone()
+    S.sanatan_gated_scan_fwd(a, b, "sigmoid", h0=h)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        other.wait_stream(main)
+        a.copy_(x)
+        with torch.cuda.stream(other):
+            b.copy_(g)
+            b.mul_(2)
+        main.wait_stream(other)
+        y, last, _ = S.sanatan_gated_scan_fwd(a, b, "sigmoid", h0=h, want_state=True)
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            twice = y * 2
+        step = S.sanatan_gated_scan_step(last, y[:, -1].contiguous(), h, "sigmoid")
+        main.wait_stream(other)
+    for scale in (1.0, -0.5):
+        x.mul_(scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, state, _ = S.sanatan_gated_scan_fwd(x, 2 * g, "sigmoid", h0=h, want_state=True)
+        assert torch.equal(y, want) and torch.equal(twice, 2 * want)
+        assert torch.equal(step, S.sanatan_gated_scan_step(state, want[:, -1].contiguous(), h,
+                                                           "sigmoid"))
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """What the library asks of the runtime once is asked while a stream captures."""
+    code = """
+import torch
+from constant_state_recurrence_gb300 import sanatan as S
+x = torch.randn(2, 300, 64, device="cuda")
+g = -torch.rand(2, 300, 64, device="cuda")
+state, pages = torch.randn(1, 2, 640, device="cuda"), torch.tensor([1, 0], device="cuda")
+codes, scales, _ = S.state_cache_empty(2, 640)
+out = torch.zeros_like(state)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y, h, m = S.sanatan_gated_scan_fwd(x, g, want_state=True, want_marks=True)
+    d = S.sanatan_gated_scan_bwd(x, g, y, m)
+    S.sanatan_state_cache_write(state, pages, codes, scales)
+    S.sanatan_state_cache_read(codes, scales, pages, out)
+graph.replay()
+torch.cuda.synchronize()
+y2, h2, m2 = S.sanatan_gated_scan_fwd(x, g, want_state=True, want_marks=True)
+d2 = S.sanatan_gated_scan_bwd(x, g, y2, m2)
+assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(d["dg"], d2["dg"])
+assert ((out - state).abs() <= state.abs().amax() / 250).all()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_two_streams_at_once():
     a = [t.to(dev()) for t in make(2, 3000, 96, F32, "log", 22)]
     b = [t.to(dev()) for t in make(3, 2500, 64, F32, "sigmoid", 23)]
@@ -420,3 +496,6 @@ def test_refusals_of_the_binding():
         S.sanatan_gated_scan_step(h.to(BF16), h, h)
     with pytest.raises(ValueError):
         S.sanatan_gated_scan_step(x, x, x)
+    with pytest.raises(S.SanatanError) as e:        # an output over an input
+        S.sanatan_gated_scan_fwd(x, x, out=x)
+    assert e.value.status == 1

@@ -129,10 +129,12 @@ def lib():
 
 
 def test_scan_refusals(lib):
+    """Every call here is refused on the host: one thing is wrong with each."""
     P = ctypes.c_void_p
-    ok = P(1 << 20)
+    at = [P((i + 1) << 20) for i in range(9)]      # ranges that share nothing
 
-    def fwd(x=ok, g=ok, dt=0, gate=0, lens=None, B=2, T=3, D=4, h0=None, y=ok, h=None, m=None):
+    def fwd(x=at[0], g=at[1], dt=0, gate=0, lens=None, B=2, T=3, D=4, h0=None, y=at[2], h=None,
+            m=None):
         return lib.sanatan_gated_scan_fwd(x, g, dt, gate, lens, B, T, D, h0, y, h, m, None)
 
     assert fwd(dt=2) == 1 and fwd(gate=2) == 1 and fwd(gate=-1) == 1
@@ -141,21 +143,31 @@ def test_scan_refusals(lib):
     assert fwd(lens=P(8)) == 1 and fwd(h0=P(4)) == 1 and fwd(h=P(8)) == 1 and fwd(m=P(8)) == 1
     assert fwd(B=1 << 20, D=1 << 11) == 2 and fwd(T=(1 << 30) + 1) == 2
     assert fwd(B=0) == 0 and fwd(D=0) == 0 and fwd(T=0, x=None, g=None, y=None) == 0
+    # outputs that share bytes with inputs or each other (x: 96 bytes from 1 << 20 on)
+    assert fwd(y=at[0]) == 1 and fwd(y=P((1 << 20) + 80)) == 1 and fwd(y=P((1 << 20) - 16)) == 1
+    assert fwd(y=at[1]) == 1 and fwd(h=at[0]) == 1 and fwd(m=at[1]) == 1 and fwd(h=at[2]) == 1
+    assert fwd(lens=at[3], h=at[3]) == 1 and fwd(m=at[4], h=at[4]) == 1
+    assert fwd(h0=at[5], h=P((6 << 20) + 16)) == 1 and fwd(h0=at[5], m=at[5]) == 1
 
-    def bwd(x=ok, dy=ok, dt=1, gate=1, B=2, T=3, D=4, m=ok, dh=None, dx=ok, dg=ok, dh0=None):
-        return lib.sanatan_gated_scan_bwd(x, ok, dy, dt, gate, None, B, T, D, m, dh, dx, dg, dh0,
+    def bwd(x=at[0], g=at[1], dy=at[2], dt=1, gate=1, lens=None, B=2, T=3, D=4, m=at[3], dh=None,
+            dx=at[4], dg=at[5], dh0=None):
+        return lib.sanatan_gated_scan_bwd(x, g, dy, dt, gate, lens, B, T, D, m, dh, dx, dg, dh0,
                                           None)
 
     assert bwd(dt=-1) == 1 and bwd(gate=3) == 1 and bwd(T=-2) == 1
     assert bwd(dy=None) == 1 and bwd(m=None) == 1 and bwd(dx=None) == 1 and bwd(dg=P(8)) == 1
-    assert bwd(dh=P(8)) == 1 and bwd(dh0=P(12)) == 1
+    assert bwd(dh=P(8)) == 1 and bwd(dh0=P(12)) == 1 and bwd(lens=P(24)) == 1
     assert bwd(B=1 << 30, D=2) == 2 and bwd(B=0) == 0
+    assert bwd(dx=at[0]) == 1 and bwd(dx=at[5]) == 1 and bwd(dg=at[2]) == 1 and bwd(dg=at[3]) == 1
+    assert bwd(dh0=at[4]) == 1 and bwd(dh=at[6], dh0=P((7 << 20) + 16)) == 1
+    assert bwd(dh0=at[3]) == 1 and bwd(lens=at[7], dh0=at[7]) == 1
 
-    def step(h=ok, x=ok, dt=0, gate=0, N=2, D=4, y=ok):
-        return lib.sanatan_gated_scan_step(h, x, ok, dt, gate, N, D, y, None)
+    def step(h=at[0], x=at[1], g=at[2], dt=0, gate=0, N=2, D=4, y=at[3]):
+        return lib.sanatan_gated_scan_step(h, x, g, dt, gate, N, D, y, None)
 
     assert step(h=None) == 1 and step(x=P(2)) == 1 and step(y=None) == 1 and step(N=-1) == 1
     assert step(dt=5) == 1 and step(gate=5) == 1 and step(N=1 << 30, D=4) == 2 and step(N=0) == 0
+    assert step(y=at[0]) == 1 and step(y=at[1]) == 1 and step(h=at[2]) == 1 and step(x=at[0]) == 1
     assert lib.sanatan_gated_scan_marks_size(3, 65, 5) == 3 * 2 * 5 * 4
     assert lib.sanatan_gated_scan_marks_size(3, 0, 5) == 0
     assert lib.sanatan_gated_scan_marks_size(-1, 1, 5) == 0
