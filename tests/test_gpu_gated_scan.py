@@ -117,7 +117,7 @@ def check(B, T, D, dtype, gate, seed=0, h0=True, lens=None, bias=1.0):
 
 SHAPES = [(1, 1, 1), (1, 1, 64), (2, 2, 3), (1, 7, 4), (3, 63, 65), (2, 64, 64), (2, 65, 130),
           (1, 127, 768), (2, 128, 12), (3, 129, 100), (1, 1000, 33), (5, 300, 257), (70, 5, 64),
-          (2, 2049, 72)]
+          (2, 2049, 72), (400, 9, 65), (330, 70, 64)]
 
 
 @pytest.mark.parametrize("gate", ["log", "sigmoid"])
