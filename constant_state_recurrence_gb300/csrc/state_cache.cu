@@ -20,9 +20,8 @@ namespace sanatan {
 namespace {
 
 constexpr int kGroup = 64;
-constexpr int kThreads = 128;
-constexpr int kBatch = 8;                             // groups of 16 lanes, loaded together
-constexpr int kPart = kThreads / 16 * kBatch;         // groups of a thread block: 64
+constexpr int threads_of(bool write) { return write ? 128 : 256; }
+constexpr int kPart = 64;  // groups of a block
 constexpr uint32_t kTiny = 0x0d800000u;   // 2^-100: smaller groups are stored as zeros
 constexpr uint32_t kLarge = 0x7f000000u;  // 2^127: there a code times its scale could overflow
 
@@ -56,37 +55,27 @@ __device__ __forceinline__ uint32_t nearest(const float (&v)[4], float scale) {
                      0x5410);
 }
 
-// 16 lanes hold a group, four values each.  A group with a value that is not
-// finite, or is 2^127 or more, has the scale NaN, so that it reads back as NaN.
+// The scale of a group whose largest magnitude has the bits `top`.  A group with a value that is not finite, or is 2^127 or more,
+// has the scale NaN, so that it reads back as NaN; its codes are zeros.
 template <int F>
-__device__ __forceinline__ uint32_t quantise(const float (&v)[4], float& scale) {
-  uint32_t top = 0;  // bit patterns of |v| order like the values, NaN above all
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-  for (int off = 8; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (top >= kLarge) {
-    scale = __uint_as_float(0x7fffffffu);
-    return 0;
-  }
-  if (top < kTiny) {
-    scale = 0.0f;
-    return 0;
-  }
+__device__ __forceinline__ float scale_of(uint32_t top) {
   if (F == SANATAN_CACHE_INT8) {
     // top / 127 rounded: with the rounded reciprocal y of 127 and q = fl(top y), the
     // remainder r = top - 127 q is exact and fl(q + r y) is the rounded quotient
     // (Markstein's theorem).
     constexpr float y = 1.0f / 127.0f;
     const float t = __uint_as_float(top), q = t * y;
-    scale = fmaf(fmaf(-127.0f, q, t), y, q);
-    return nearest(v, scale);
+    return fmaf(fmaf(-127.0f, q, t), y, q);
   }
   // 448 = 1.75 * 2^8: the exponent of max|x|, less 8, one more where the mantissa is
   // above 1.75.
-  const uint32_t e = (top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-  scale = __uint_as_float(e << 23);
-  const float inv = __uint_as_float((254u - e) << 23);
+  return __uint_as_float(((top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0)) << 23);
+}
+
+template <int F>
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[4], float scale) {
+  if (F == SANATAN_CACHE_INT8) return nearest(v, scale);
+  const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // a power of two
   const uint32_t lo =
       __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi =
@@ -116,6 +105,7 @@ __device__ __forceinline__ void restore(uint32_t word, float scale, float (&v)[4
 // The page of sequence b, or -1: none, or a later sequence of the call writes it.  By
 // all threads of the block.
 __device__ __forceinline__ int64_t page_of(const CacheArgs& a, int b, bool writing) {
+  constexpr int kThreads = threads_of(true);
   const int64_t p = a.pages[b];
   if (p < 0 || p >= a.num_pages) return -1;
   if (writing) {
@@ -127,49 +117,96 @@ __device__ __forceinline__ int64_t page_of(const CacheArgs& a, int b, bool writi
   return p;
 }
 
-// One part (64 groups, 16 KB of values) of a stretch.  The values of all of a
-// thread's groups are under way before the first is used: eight 16-byte loads
-// (VEC, inner a multiple of 4), 16 lanes a group, so that a warp reads 512 and
-// writes 128 neighbouring bytes at a time.
+// Four values from x on, of which `left` are there (VEC: all or none).
+template <bool VEC>
+__device__ __forceinline__ void load(const float* x, int left, float (&v)[4]) {
+  if (VEC) {
+    const float4 f = left > 0 ? __ldcs(reinterpret_cast<const float4*>(x))
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < left ? x[i] : 0.0f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store(float* x, int left, const float (&v)[4]) {
+  if (VEC) {
+    if (left > 0) *reinterpret_cast<float4*>(x) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) x[i] = v[i];
+  }
+}
+
+// One part (64 groups, 16 KB of values) of a stretch.  kLanes lanes have a group; lane
+// l its words (four values) l, l + kLanes, ..., so that a warp reads whole lines of
+// values and whole sectors of codes.  All of a thread's loads are under way before the
+// first is used: eight of 16 bytes when writing (VEC, inner a multiple of 4).  Writing
+// takes eight lanes a group (three exchanges for eight values; with sixteen lanes 184
+// instead of 168 us), reading sixteen and twice the threads (whole lines of codes, four loads
+// a thread: one sequence 4.9 instead of 5.9 us).  Bound: bytes.  64 sequences of 144 states (0.9 GB), int8, GB300: written in
+// 168 us, 7.0 TB/s, read in 169 us, 7.0 TB/s (the copy rate is 6.8).
 template <int F, bool WRITE, bool VEC>
-__global__ void __launch_bounds__(kThreads) cache_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(threads_of(WRITE)) cache_kernel(const CacheArgs a) {
+  constexpr int kThreads = threads_of(WRITE);
+  constexpr int kLanes = WRITE ? 8 : 16;
+  constexpr int kWords = kGroup / 4 / kLanes;   // of a lane
+  constexpr int kRows = kThreads / kLanes;      // groups that the block has in hand at a time
+  constexpr int kBatch = kPart / kRows;
   const unsigned stretch = blockIdx.x / a.blocks, part = blockIdx.x % a.blocks;
   const int b = static_cast<int>(stretch % a.B), l = static_cast<int>(stretch / a.B);
   const int64_t groups = (a.inner + kGroup - 1) / kGroup;
-  const int64_t g0 = static_cast<int64_t>(part) * kPart + threadIdx.x / 16;
-  const int lane = threadIdx.x % 16;
+  const int64_t g0 = static_cast<int64_t>(part) * kPart;  // the block's first group
   const int64_t row = static_cast<int64_t>(l) * a.B + b;  // stretch of the state
-  float* x = a.state + row * a.inner;
+  const int here = static_cast<int>(min(groups - g0, static_cast<int64_t>(kPart)));
+  const int values = static_cast<int>(min(a.inner - g0 * kGroup, int64_t{kPart * kGroup}));
+  const int lane = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+  float* x = a.state + row * a.inner + g0 * kGroup;
   wait_for_previous();
 
   if (WRITE) {
-    float v[kBatch][4];
+    float v[kBatch][kWords][4];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t k = (g0 + u * (kThreads / 16)) * kGroup + lane * 4;
-      if (VEC) {
-        const float4 f = k < a.inner ? __ldcs(reinterpret_cast<const float4*>(x + k))
-                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        v[u][0] = f.x;
-        v[u][1] = f.y;
-        v[u][2] = f.z;
-        v[u][3] = f.w;
-      } else {
+    for (int u = 0; u < kBatch; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[u][i] = k + i < a.inner ? x[k + i] : 0.0f;
+      for (int i = 0; i < kWords; ++i) {
+        const int k = (first + u * kRows) * kGroup + 4 * (lane + i * kLanes);
+        load<VEC>(x + k, values - k, v[u][i]);
       }
-    }
     const int64_t p = page_of(a, b, true);
     if (p < 0) return;
-    const int64_t page = (p * a.layers + l) * groups;
+    const int64_t page = (p * a.layers + l) * groups + g0;
+    uint32_t* codes = reinterpret_cast<uint32_t*>(a.codes) + page * 16;
+    float* scales = a.scales + page;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int64_t g = g0 + u * (kThreads / 16);
-      float scale;
-      const uint32_t word = quantise<F>(v[u], scale);
-      if (g < groups) {
-        reinterpret_cast<uint32_t*>(a.codes)[(page + g) * 16 + lane] = word;
-        if (lane == 0) a.scales[page + g] = scale;
+      const int g = first + u * kRows;
+      uint32_t top = 0;  // bit patterns of |v| order like the values, NaN above all
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(v[u][i][j]) & 0x7fffffffu);
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off /= 2)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+      float scale = scale_of<F>(top);
+      uint32_t word[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) word[i] = codes_of<F>(v[u][i], scale);
+      if (top < kTiny || top >= kLarge) {
+        scale = top < kTiny ? 0.0f : __uint_as_float(0x7fffffffu);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) word[i] = 0;
+      }
+      if (g < here) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) codes[g * 16 + lane + i * kLanes] = word[i];
+        if (lane == 0) scales[g] = scale;
       }
     }
     for (int64_t k = static_cast<int64_t>(part) * kThreads + threadIdx.x; k < a.exact_inner;
@@ -179,29 +216,30 @@ __global__ void __launch_bounds__(kThreads) cache_kernel(const CacheArgs a) {
   }
   const int64_t p = page_of(a, b, false);
   if (p < 0) return;
-  const int64_t page = (p * a.layers + l) * groups;
-  uint32_t word[kBatch];
+  const int64_t page = (p * a.layers + l) * groups + g0;
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes) + page * 16;
+  const float* scales = a.scales + page;
+  uint32_t word[kBatch][kWords];
   float scale[kBatch];
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
-    const int64_t g = g0 + u * (kThreads / 16);
-    if (g < groups) {
-      word[u] = reinterpret_cast<const uint32_t*>(a.codes)[(page + g) * 16 + lane];
-      scale[u] = a.scales[page + g];
+    const int g = first + u * kRows;
+    if (g < here) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) word[u][i] = codes[g * 16 + lane + i * kLanes];
+      scale[u] = scales[g];
     }
   }
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) {
-    const int64_t g = g0 + u * (kThreads / 16), k = g * kGroup + lane * 4;
-    if (g < groups) {
-      float v[4];
-      restore<F>(word[u], scale[u], v);
-      if (VEC) {
-        if (k < a.inner) *reinterpret_cast<float4*>(x + k) = make_float4(v[0], v[1], v[2], v[3]);
-      } else {
+    const int g = first + u * kRows;
+    if (g < here) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (k + i < a.inner) x[k + i] = v[i];
+      for (int i = 0; i < kWords; ++i) {
+        const int k = g * kGroup + 4 * (lane + i * kLanes);
+        float v[4];
+        restore<F>(word[u][i], scale[u], v);
+        store<VEC>(x + k, values - k, v);
       }
     }
   }
@@ -214,7 +252,7 @@ template <int F, bool WRITE>
 cudaError_t launch(const CacheArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(a.blocks * static_cast<unsigned>(a.layers) * static_cast<unsigned>(a.B));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of(WRITE));
   cfg.stream = st;
   cudaLaunchAttribute attr = pdl_attribute();
   cfg.attrs = &attr;
