@@ -436,8 +436,8 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  *     h_t = a_t h_{t-1} + u_t,   y_t = h_t,
  *     SANATAN_GATE_LOG:      a = exp(g),           u = x        (g: log of the decay)
  *     SANATAN_GATE_SIGMOID:  a = 1 / (1 + exp(-g)), u = (1 - a) x
- * The sequence mixers are the notes' own comparison (§4.1 names gated linear
- * attention); the pages give no formula for a gate, these are the plain ones.
+ * (The notes compare the method with gated linear attention, Table 1; the pages
+ * give no formula for a gate, these are the plain ones.)
  *   x, g    [B, T, D]  dtype;   y [B, T, D] dtype (the float32 state rounded once)
  *   lens    [B] int64 or NULL: tokens of each sequence (values outside [0, T]
  *           are taken as the nearest of the two).  Tokens from lens[b] on
