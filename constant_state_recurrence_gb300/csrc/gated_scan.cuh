@@ -68,7 +68,9 @@ constexpr int kStages = 2;  // tiles of a ring
 struct V4 {
   uint64_t lo, hi;
 };
-__device__ __forceinline__ V4 v4(float a, float b, float c, float d) { return {pk2(a, b), pk2(c, d)}; }
+__device__ __forceinline__ V4 v4(float a, float b, float c, float d) {
+  return {pk2(a, b), pk2(c, d)};
+}
 __device__ __forceinline__ V4 v4(float a) { return v4(a, a, a, a); }
 __device__ __forceinline__ V4 mul(const V4& a, const V4& b) {
   return {fmul2(a.lo, b.lo), fmul2(a.hi, b.hi)};
@@ -164,7 +166,9 @@ template <>
 struct Quad<float> {
   using type = ulonglong2;
   __device__ __forceinline__ static V4 get(const ulonglong2& v) { return {v.x, v.y}; }
-  __device__ __forceinline__ static ulonglong2 put(const V4& v) { return make_ulonglong2(v.lo, v.hi); }
+  __device__ __forceinline__ static ulonglong2 put(const V4& v) {
+    return make_ulonglong2(v.lo, v.hi);
+  }
 };
 template <>
 struct Quad<__nv_bfloat16> {
@@ -379,8 +383,8 @@ struct Cluster {
       asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(r));
       asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to_bar) : "r"(bar), "r"(r));
       asm volatile(
-          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::
-              "r"(to),
+          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64"
+          " [%0], {%1, %2}, [%3];" ::"r"(to),
           "l"(A), "l"(H), "r"(to_bar)
           : "memory");
     }

@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_bwd_kernel(
   // Warp 0: the gradient that comes into the step's last token from later ones.
   const int at = tid % (2 * LANES);
   const PairPlace<LANES, TMA> pair(place.c0, at, D);
-  uint64_t carry = pair.load(p.dh_out == nullptr ? nullptr : p.dh_out + static_cast<int64_t>(b) * D);
+  uint64_t carry =
+      pair.load(p.dh_out == nullptr ? nullptr : p.dh_out + static_cast<int64_t>(b) * D);
   // (in hand before any CTA of the cluster goes on: the last state may go where it was)
   if (warp == 0) pairs(ex.in[0])[at] = carry;
   Cluster<LANES, true> cluster{ex,   reinterpret_cast<ulonglong2*>(ring + Ring::kBytes),

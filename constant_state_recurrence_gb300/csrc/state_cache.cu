@@ -55,8 +55,9 @@ __device__ __forceinline__ uint32_t nearest(const float (&v)[4], float scale) {
                      0x5410);
 }
 
-// The scale of a group whose largest magnitude has the bits `top`.  A group with a value that is not finite, or is 2^127 or more,
-// has the scale NaN, so that it reads back as NaN; its codes are zeros.
+// The scale of a group whose largest magnitude has the bits `top` (2^-100 to 2^127; the
+// kernel gives smaller groups the scale 0 and larger ones, or those with a value that
+// is not finite, the scale NaN, with codes of 0).
 template <int F>
 __device__ __forceinline__ float scale_of(uint32_t top) {
   if (F == SANATAN_CACHE_INT8) {
@@ -147,10 +148,11 @@ __device__ __forceinline__ void store(float* x, int left, const float (&v)[4]) {
 // l its words (four values) l, l + kLanes, ..., so that a warp reads whole lines of
 // values and whole sectors of codes.  All of a thread's loads are under way before the
 // first is used: eight of 16 bytes when writing (VEC, inner a multiple of 4).  Writing
-// takes eight lanes a group (three exchanges for eight values; with sixteen lanes 184
-// instead of 168 us), reading sixteen and twice the threads (whole lines of codes, four loads
-// a thread: one sequence 4.9 instead of 5.9 us).  Bound: bytes.  64 sequences of 144 states (0.9 GB), int8, GB300: written in
-// 168 us, 7.0 TB/s, read in 169 us, 7.0 TB/s (the copy rate is 6.8).
+// takes eight lanes a group (three exchanges for eight values: 168 us where sixteen
+// lanes took 184), reading sixteen and twice the threads (whole lines of codes, four
+// loads a thread: one sequence in 5.0 us instead of 5.9).
+// Bound: bytes.  64 sequences of 144 states (0.9 GB), int8, GB300: written in 168 us,
+// 7.0 TB/s, read in 169 us, 7.0 TB/s (a plain copy: 6.8).
 template <int F, bool WRITE, bool VEC>
 __global__ void __launch_bounds__(threads_of(WRITE)) cache_kernel(const CacheArgs a) {
   constexpr int kThreads = threads_of(WRITE);
@@ -270,8 +272,10 @@ int64_t state_cache_blocks(int64_t inner) {
 
 cudaError_t state_cache_launch(const CacheArgs& a, bool write, cudaStream_t st) {
   if (a.fmt == SANATAN_CACHE_INT8)
-    return write ? launch<SANATAN_CACHE_INT8, true>(a, st) : launch<SANATAN_CACHE_INT8, false>(a, st);
-  return write ? launch<SANATAN_CACHE_E4M3, true>(a, st) : launch<SANATAN_CACHE_E4M3, false>(a, st);
+    return write ? launch<SANATAN_CACHE_INT8, true>(a, st)
+                 : launch<SANATAN_CACHE_INT8, false>(a, st);
+  return write ? launch<SANATAN_CACHE_E4M3, true>(a, st)
+               : launch<SANATAN_CACHE_E4M3, false>(a, st);
 }
 
 }  // namespace sanatan

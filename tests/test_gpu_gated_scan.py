@@ -78,7 +78,8 @@ def bounds(x, g, gate, h0, dy=None, dh_last=None, lens=None):
     else:
         w = Hb + np.abs(x)
         out["dx"] = keep * (Ed + (k + 2 * E) * Dm)
-        out["dg"] = a * keep * (w * Ed + Dm * (Eb + 2 * E * w)) + (2 * k + 6 * E) * a * keep * Dm * w
+        out["dg"] = a * keep * (w * Ed + Dm * (Eb + 2 * E * w)) \
+            + (2 * k + 6 * E) * a * keep * Dm * w
     return out
 
 

@@ -125,8 +125,8 @@ def test_sequences_left_out_and_pages_named_twice():
     pages = torch.tensor([2, -1, 0, 2, P, 1 << 40], device=dev())
     S.sanatan_state_cache_write(x, pages, codes, scales, z, zc)
     alone = S.state_cache_empty(P, inner, 10)
-    S.sanatan_state_cache_write(x[:, 2:4].contiguous(), torch.tensor([0, 2], device=dev()), *alone[:2],
-                                z[:, 2:4].contiguous(), alone[2])
+    S.sanatan_state_cache_write(x[:, 2:4].contiguous(), torch.tensor([0, 2], device=dev()),
+                                *alone[:2], z[:, 2:4].contiguous(), alone[2])
     assert torch.equal(codes, alone[0]) and torch.equal(scales, alone[1])
     assert torch.equal(zc, alone[2]) and not scales[1].any() and not scales[3].any()
     out = torch.full((1, B, inner), 5.0, device=dev())
@@ -272,7 +272,8 @@ def test_refusals_of_the_binding():
     z = torch.zeros(1, 2, 4, device=dev())
     W_ = S.sanatan_state_cache_write
     for bad in ((x[..., :100], pages, codes, scales), (x.to(torch.bfloat16), pages, codes, scales),
-                (x, pages.to(torch.int32), codes, scales), (x, pages, codes.to(torch.uint8), scales),
+                (x, pages.to(torch.int32), codes, scales),
+                (x, pages, codes.to(torch.uint8), scales),
                 (x, pages, codes[:, :, :1], scales), (x, pages, codes, scales[:2]),
                 (x, pages, codes, scales, z), (x, pages, codes, scales, z, zc[..., :3]),
                 (x, pages, codes, scales, z, zc, 2), (x, pages, codes, scales, z, zc, 0),
