@@ -271,6 +271,11 @@ struct Tiles {
       if (tid == 0)
         for (int i = 0; i < STAGES; ++i) tc::mbar_init(&full[i], 1);
       tc::fence_mbar_init();
+      if (tid == kIssuer)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps->of[i]))
+                       : "memory");
     }
   }
   // TMA, one thread: fetch the tile that starts at token t (none of it present:

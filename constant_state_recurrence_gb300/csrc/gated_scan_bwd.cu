@@ -21,12 +21,23 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_bwd_kernel(
   const int tid = threadIdx.x, lane = tid % LANES, warp = tid >> 5;
   const int T = p.T, D = p.D;
   const Place<LANES, TMA> place{(unit % blocks) * 4 * LANES, lane, D};
-  wait_for_previous();
-  const int len = length_of(p.lens, b, T);
   const int tiles = (T + kTile - 1) / kTile;
   const int steps = (tiles + cluster_size - 1) / cluster_size;
 
+  // What touches no tensor comes before the wait for the kernel before.
+  const int at = tid % (2 * LANES);
+  Cluster<LANES, true> cluster{ex,   reinterpret_cast<ulonglong2*>(ring + Ring::kBytes),
+                                rank, cluster_size, steps, at};
   Ring in;
+  in.ring = ring;
+  in.full = ex.ring;
+  in.maps = &maps;
+  in.dead = &cluster.dead;
+  in.start(tid);
+  cluster.start();
+  wait_for_previous();
+
+  const int len = length_of(p.lens, b, T);
   const int64_t base = static_cast<int64_t>(b) * T * D + place.channel(0);
   in.src[0] = static_cast<const E*>(p.g) + base;
   in.src[1] = static_cast<const E*>(p.x) + base;
@@ -35,9 +46,6 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_bwd_kernel(
   in.len = len;
   in.b = b;
   in.place = place;
-  in.ring = ring;
-  in.full = ex.ring;
-  in.maps = &maps;
   E* dx = static_cast<E*>(p.dx) + static_cast<int64_t>(b) * T * D;
   E* dg = static_cast<E*>(p.dg) + static_cast<int64_t>(b) * T * D;
   const float* marks = p.marks + static_cast<int64_t>(b) * ((T + kMark - 1) / kMark) * D;
@@ -52,17 +60,11 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_bwd_kernel(
   auto begin = [&](int s) { return tile(s) < 0 ? T : tile(s) * kTile; };
   auto token = [&](int s) { return min(begin(s) + run, T); };
   // Warp 0: the gradient that comes into the step's last token from later ones.
-  const int at = tid % (2 * LANES);
   const PairPlace<LANES, TMA> pair(place.c0, at, D);
   uint64_t carry =
       pair.load(p.dh_out == nullptr ? nullptr : p.dh_out + static_cast<int64_t>(b) * D);
-  // (in hand before any CTA of the cluster goes on: the last state may go where it was)
+  // (in hand before this CTA's first map leaves: the last state may go where it was)
   if (warp == 0) pairs(ex.in[0])[at] = carry;
-  Cluster<LANES, true> cluster{ex,   reinterpret_cast<ulonglong2*>(ring + Ring::kBytes),
-                                rank, cluster_size, steps, at};
-  in.dead = &cluster.dead;
-  in.start(tid);
-  cluster.start();
   if constexpr (TMA) {
     if (tid == kIssuer)
       for (int s = 0; s < kStages; ++s) in.fetch(begin(s), s);

@@ -20,12 +20,23 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_fwd_kernel(
   const int tid = threadIdx.x, lane = tid % LANES, warp = tid >> 5;
   const int T = p.T, D = p.D;
   const Place<LANES, TMA> place{(unit % blocks) * 4 * LANES, lane, D};
-  wait_for_previous();
-  const int len = length_of(p.lens, b, T);
   const int tiles = (T + kTile - 1) / kTile;
   const int steps = (tiles + cluster_size - 1) / cluster_size;
 
+  // What touches no tensor comes before the wait for the kernel before.
+  const int at = tid % (2 * LANES);
+  Cluster<LANES, false> cluster{ex,   reinterpret_cast<ulonglong2*>(ring + Ring::kBytes),
+                                 rank, cluster_size, steps, at};
   Ring in;
+  in.ring = ring;
+  in.full = ex.ring;
+  in.maps = &maps;
+  in.dead = &cluster.dead;
+  in.start(tid);
+  cluster.start();
+  wait_for_previous();
+
+  const int len = length_of(p.lens, b, T);
   const int64_t base = static_cast<int64_t>(b) * T * D + place.channel(0);
   in.src[0] = static_cast<const E*>(p.g) + base;
   in.src[1] = static_cast<const E*>(p.x) + base;
@@ -33,9 +44,6 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_fwd_kernel(
   in.len = len;
   in.b = b;
   in.place = place;
-  in.ring = ring;
-  in.full = ex.ring;
-  in.maps = &maps;
   E* y = static_cast<E*>(p.y) + static_cast<int64_t>(b) * T * D;
 
   // First token of the CTA's tile in step s, and of the thread's run; T or more past
@@ -44,16 +52,10 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_fwd_kernel(
   auto begin = [&](int s) { return (s * cluster_size + rank) * kTile; };
   auto token = [&](int s) { return begin(s) + run; };
   // Warp 0: the state before the step's first tile.
-  const int at = tid % (2 * LANES);
   const PairPlace<LANES, TMA> pair(place.c0, at, D);
   uint64_t carry = pair.load(p.h0 == nullptr ? nullptr : p.h0 + static_cast<int64_t>(b) * D);
-  // (in hand before any CTA of the cluster goes on: the last state may go where it was)
+  // (in hand before this CTA's first map leaves: the last state may go where it was)
   if (warp == 0) pairs(ex.in[0])[at] = carry;
-  Cluster<LANES, false> cluster{ex,   reinterpret_cast<ulonglong2*>(ring + Ring::kBytes),
-                                 rank, cluster_size, steps, at};
-  in.dead = &cluster.dead;
-  in.start(tid);
-  cluster.start();
   if constexpr (TMA) {
     if (tid == kIssuer)
       for (int s = 0; s < kStages; ++s) in.fetch(begin(s), s);
