@@ -385,6 +385,31 @@ def test_captured_training_step_replays_with_new_inputs():
     assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_captured_autograd():
+    """GatedScan's forward and backward captured as a user captures a training step."""
+    x, g, dy, h, dh = (t.to(dev()) for t in make(2, 200, 72, F32, "sigmoid", 25))
+    x, g, h = (t.requires_grad_() for t in (x, g, h))
+
+    def step():
+        y, last = S.GatedScan.apply(x, g, "sigmoid", h)
+        return torch.autograd.grad((y * dy).sum() + (last * dh).sum(), (x, g, h))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    with torch.no_grad():
+        x.mul_(0.5)
+        g.add_(0.25)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
 def test_states_updated_in_place():
     """h_out may be h0 (and dh0 dh_last): a serving state that stays where it is."""
     for B, T, D in ((1, 4000, 64), (3, 700, 100), (40, 3, 768)):
