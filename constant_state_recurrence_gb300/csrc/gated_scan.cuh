@@ -21,13 +21,14 @@
 //
 // Bound: bytes (three tensors forward, five backward), and beside them the latency of
 // a step: map, exchange, tokens.  Hence two CTAs an SM, and few steps rather than many
-// warps: half the run and three or four CTAs an SM took 30 and 35 us where this takes
-// 27 (training shape below), a third stage 28.  st.async with a counting mbarrier
-// instead of a cluster barrier took 44 instead of 60 us (the barrier's release waits for
-// every thread's global stores), TMA instead of cp.async 27 instead of 32 us.
-// Device time, GB300, bf16, of the measured copy rate: B 8 T 4096 D 768 log gate forward
-// 28 us, 5.4 TB/s (0.79); backward 47 us, 5.3 TB/s (0.79); B 1 T 32768 D 768 sigmoid
+// warps.  Forward, training shape (B 8 T 4096 D 768, bf16, log gate), GB300: 28.4 us;
+// half the run and three or four CTAs an SM 34 and 37 us, a third stage 29.4; as
+// first built, a cluster barrier instead of st.async with a counting mbarrier made
+// 44 us into 60 (the barrier's release waits for every thread's global stores), cp.async
+// instead of TMA 27 into 32.  Device times of the measured copy rate: this forward
+// 5.3 TB/s (0.78), its backward 48 us, 5.2 TB/s (0.77); B 1 T 32768 D 768, sigmoid,
 // forward 36 us, 4.2 TB/s (0.62: one sequence's clusters do not fill the SMs evenly).
+// The same work without exchanges (24 sequences of 1408 tokens) takes 26.4 and 43.4 us.
 //
 // The backward needs h_{t-1}: the forward leaves the state before every 64th
 // token (a mark, 1/64 of the elements in float32), from which a tile's states are
@@ -543,8 +544,8 @@ cudaError_t held_by(Held* out) {
 // Few sequences: the largest cluster with which all clusters still run at once (a
 // second wave would cost more than it splits), and of those with the same
 // number of steps the smallest.  Training shape (B 8, T 4096, D 768, bf16: 96
-// blocks of 64 channels), forward us by cluster size: 1: 32.6, 2: 30.5, 3: 26.7 (288
-// of 291 places), 4: 31.6, 8: 34.0.
+// blocks of 64 channels), forward and backward us by cluster size: 1: 35 and 73, 2: 35
+// and 63, 3: 28 and 49 (288 of 291 places), 4: 32 and 58, 8: 36 and 58.
 template <auto Kernel, typename Args, typename Ring>
 cudaError_t shape_of(const Args& a, Shape* best) {
   Held h;
