@@ -53,7 +53,8 @@ int check_scan(int dtype, int gate, int B, int T, int D) {
   if (B < 0 || T < 0 || D < 0) return SANATAN_ERR_INVALID;
   // Elements index with 64-bit arithmetic; thread blocks must fit a grid.
   if (static_cast<int64_t>(B) * D > (1LL << 31) - 1) return SANATAN_ERR_UNSUPPORTED;
-  if (T > (1 << 30)) return SANATAN_ERR_UNSUPPORTED;  // token indexes are ints, a tile past T too
+  // Token and channel indexes are ints, also those of a tile that reaches past the end.
+  if (T > (1 << 30) || D > (1 << 30)) return SANATAN_ERR_UNSUPPORTED;
   return SANATAN_OK;
 }
 

@@ -466,7 +466,7 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  *   in place, x, g, y [N, D] dtype.
  * Errors: SANATAN_ERR_INVALID for an unknown dtype or gate, a negative size, a
  * null (where not allowed) or misaligned pointer; SANATAN_ERR_UNSUPPORTED for
- * B * D (N * D) of 2^31 or more or T above 2^30.  Outputs share no bytes with
+ * B * D (N * D) of 2^31 or more, or T or D above 2^30.  Outputs share no bytes with
  * inputs or each other (SANATAN_ERR_INVALID), except that h_out may be h0 and dh0
  * may be dh_out.
  */

@@ -142,6 +142,7 @@ def test_scan_refusals(lib):
     assert fwd(x=None) == 1 and fwd(g=P(24)) == 1 and fwd(y=None) == 1
     assert fwd(lens=P(8)) == 1 and fwd(h0=P(4)) == 1 and fwd(h=P(8)) == 1 and fwd(m=P(8)) == 1
     assert fwd(B=1 << 20, D=1 << 11) == 2 and fwd(T=(1 << 30) + 1) == 2
+    assert fwd(B=1, T=1, D=(1 << 30) + 1) == 2
     assert fwd(B=0) == 0 and fwd(D=0) == 0 and fwd(T=0, x=None, g=None, y=None) == 0
     # outputs that share bytes with inputs or each other (x: 96 bytes from 1 << 20 on)
     assert fwd(y=at[0]) == 1 and fwd(y=P((1 << 20) + 80)) == 1 and fwd(y=P((1 << 20) - 16)) == 1
