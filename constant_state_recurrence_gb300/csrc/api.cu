@@ -14,6 +14,10 @@ constexpr int kMaxPower = 8;   // largest p of sanatan_power_fwd
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
 bool ok_nullable(const void* p) { return p == nullptr || aligned16(p); }
+// Null, or where an element of `size` bytes may start: what kernels touch element by element.
+bool at_element(const void* p, size_t size) {
+  return reinterpret_cast<uintptr_t>(p) % size == 0;
+}
 bool ok_dtype(int t) { return t == SANATAN_F32 || t == SANATAN_BF16; }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? SANATAN_OK : SANATAN_ERR_CUDA; }
@@ -664,9 +668,10 @@ int sanatan_gated_scan_bwd(const void* x, const void* g, const void* dy, int dty
                            const int64_t* lens, int B, int T, int D, const float* marks,
                            const float* dh_out, void* dx, void* dg, float* dh0, void* stream) {
   if (int s = check_scan(dtype, gate, B, T, D)) return s;
-  if (!ok_nullable(lens) || !ok_nullable(dh_out) || !ok_nullable(dh0)) return SANATAN_ERR_INVALID;
+  if (!ok_nullable(lens) || !at_element(dh_out, 4) || !ok_nullable(dh0)) return SANATAN_ERR_INVALID;
   if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
-  if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || !ok_ptr(dy) || !ok_ptr(marks) || !ok_ptr(dx) ||
+  if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || dy == nullptr ||
+                !at_element(dy, dtype == SANATAN_F32 ? 4 : 2) || !ok_ptr(marks) || !ok_ptr(dx) ||
                 !ok_ptr(dg)))
     return SANATAN_ERR_INVALID;
   if (T == 0 && dh0 == nullptr) return SANATAN_OK;

@@ -208,7 +208,9 @@ cudaError_t bwd_of(const ScanBwdArgs& a, cudaStream_t st, bool* done) {
 template <typename E, int G>
 cudaError_t bwd(const ScanBwdArgs& a, cudaStream_t st) {
   bool done = false;
-  if (a.T > 0 && a.D * sizeof(E) % 16 == 0) {
+  // TMA: rows of 16 bytes, from a dy that starts at 16 bytes (a slice of a larger gradient
+  // may start at any element, and is read by the element).
+  if (a.T > 0 && a.D * sizeof(E) % 16 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0) {
     const cudaError_t e = bwd_of<E, G, true>(a, st, &done);
     if (done) return e;
   }

@@ -21,7 +21,8 @@
  *    The library allocates no device memory and keeps no state between calls
  *    except cached device attributes.
  *  - Tensors are dense and row-major (C order) with the shapes given below;
- *    pointers must be 16-byte aligned (SANATAN_ERR_INVALID otherwise).
+ *    pointers must be 16-byte aligned, unless a call says less of one
+ *    (SANATAN_ERR_INVALID otherwise).
  *  - Work is enqueued on `stream` (a cudaStream_t; NULL = legacy default
  *    stream).  No call synchronises the device; a status of SANATAN_OK means
  *    the launches were enqueued without a launch error.
@@ -457,7 +458,8 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  *
  * sanatan_gated_scan_bwd -- gradients of sum(y * dy) + sum(h_out * dh_out):
  *   marks as the forward wrote them for the same x, g, h0 and lens (h0 is their
- *   first row); dy [B, T, D] dtype; dh_out [B, D] f32 or NULL (zero);
+ *   first row); dy [B, T, D] dtype; dh_out [B, D] f32 or NULL (zero): both may start at
+ *   any element (the gradients of joined outputs come as slices of a larger one);
  *   dx, dg [B, T, D] dtype outputs; dh0 [B, D] f32 output or NULL.
  *     dh_t = dy_t + a_{t+1} dh_{t+1};  dh0 = a_0 dh_0;
  *     log: dx = dh, dg = dh a h_{t-1};

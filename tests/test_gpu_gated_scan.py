@@ -525,3 +525,28 @@ def test_refusals_of_the_binding():
     with pytest.raises(S.SanatanError) as e:        # an output over an input
         S.sanatan_gated_scan_fwd(x, x, out=x)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,D", [(1, 40, 7), (2, 70, 64), (3, 200, 771), (2, 130, 768)])
+def test_autograd_with_gradients_at_any_address(B, T, D, dtype):
+    """Outputs that are joined behind others get slices of one gradient back: contiguous,
+    but at any element."""
+    x, g, dy, h, dh = make(B, T, D, dtype, "sigmoid", 26)
+    xs, gs, h0 = (t.to(dev()).requires_grad_() for t in (x, g, h))
+    y, last = S.GatedScan.apply(xs, gs, "sigmoid", h0)
+    where = []
+    y.register_hook(lambda t: where.append(t.data_ptr() % 16))
+    last.register_hook(lambda t: where.append(t.data_ptr() % 16))
+    ys = torch.cat([torch.zeros(3, dtype=dtype, device=dev()), y.flatten()])
+    ls = torch.cat([torch.zeros(1, device=dev()), last.flatten()])
+    front = torch.ones(3, dtype=dtype)
+    wy = torch.cat([front, dy.flatten()]).to(dev())
+    wl = torch.cat([torch.ones(1), dh.flatten()]).to(dev())
+    torch.autograd.backward([ys, ls], [wy, wl])
+    assert len(where) == 2 and all(where)
+    dx, dg, dh0 = R.gated_scan_backward(f64(x), f64(g), "sigmoid", f64(dy), f64(h), None, f64(dh))
+    b = bounds(f64(x), f64(g), "sigmoid", f64(h), f64(dy), f64(dh))
+    close(xs.grad, dx, b["dx"], dtype, "dx")
+    close(gs.grad, dg, b["dg"], dtype, "dg")
+    close(h0.grad, dh0, b["dh0"], F32, "dh0")
