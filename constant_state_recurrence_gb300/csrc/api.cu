@@ -82,7 +82,7 @@ int state_cache(float* state, float* exact, int layers, int B, int64_t inner, in
     return SANATAN_ERR_INVALID;
   if (static_cast<int64_t>(layers) * B == 0 || (inner == 0 && exact_inner == 0) || num_pages == 0)
     return SANATAN_OK;
-  if (!ok_ptr(pages)) return SANATAN_ERR_INVALID;
+  if (pages == nullptr || !at_element(pages, 8)) return SANATAN_ERR_INVALID;
   if (inner > 0 && (!ok_ptr(state) || !ok_ptr(codes) || !ok_ptr(scales)))
     return SANATAN_ERR_INVALID;
   if (exact_inner > 0 && (!ok_ptr(exact) || !ok_ptr(exact_cache))) return SANATAN_ERR_INVALID;
@@ -629,7 +629,7 @@ int sanatan_gated_scan_fwd(const void* x, const void* g, int dtype, int gate, co
                            int B, int T, int D, const float* h0, void* y, float* h_out,
                            float* marks, void* stream) {
   if (int s = check_scan(dtype, gate, B, T, D)) return s;
-  if (!ok_nullable(lens) || !ok_nullable(h0) || !ok_nullable(h_out) || !ok_nullable(marks))
+  if (!at_element(lens, 8) || !ok_nullable(h0) || !ok_nullable(h_out) || !ok_nullable(marks))
     return SANATAN_ERR_INVALID;
   if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
   if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || !ok_ptr(y))) return SANATAN_ERR_INVALID;
@@ -668,7 +668,7 @@ int sanatan_gated_scan_bwd(const void* x, const void* g, const void* dy, int dty
                            const int64_t* lens, int B, int T, int D, const float* marks,
                            const float* dh_out, void* dx, void* dg, float* dh0, void* stream) {
   if (int s = check_scan(dtype, gate, B, T, D)) return s;
-  if (!ok_nullable(lens) || !at_element(dh_out, 4) || !ok_nullable(dh0)) return SANATAN_ERR_INVALID;
+  if (!at_element(lens, 8) || !at_element(dh_out, 4) || !ok_nullable(dh0)) return SANATAN_ERR_INVALID;
   if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
   if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || dy == nullptr ||
                 !at_element(dy, dtype == SANATAN_F32 ? 4 : 2) || !ok_ptr(marks) || !ok_ptr(dx) ||

@@ -440,8 +440,9 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  * (The notes compare the method with gated linear attention, Table 1; the pages
  * give no formula for a gate, these are the plain ones.)
  *   x, g    [B, T, D]  dtype;   y [B, T, D] dtype (the float32 state rounded once)
- *   lens    [B] int64 or NULL: tokens of each sequence (values outside [0, T]
- *           are taken as the nearest of the two).  Tokens from lens[b] on
+ *   lens    [B] int64 or NULL, at 8 bytes (lens + 1 of a longer list will do): tokens
+ *           of each sequence (values outside [0, T] are taken as the nearest of
+ *           the two).  Tokens from lens[b] on
  *           have no effect; their y, dx and dg are written as zeros, and the state
  *           passes them unchanged.  NULL: all T tokens.
  *   h0      [B, D] f32 or NULL (zero): the state before the first token
@@ -499,7 +500,8 @@ SANATAN_API int sanatan_gated_scan_step(float* h, const void* x, const void* g, 
  *   exact   [layers, B, exact_inner] f32 or NULL (exact_inner = 0): values that
  *           are kept in float32: z, which every output is divided by through
  *           Phi(q) . z.
- *   pages   [B] int64: the page of each sequence, in [0, num_pages); any other
+ *   pages   [B] int64, at 8 bytes (pages + 1 of a longer list will do): the
+ *           page of each sequence, in [0, num_pages); any other
  *           value (-1) leaves that sequence out: nothing of it is read or
  *           written.  Where a write names a page twice the last of the call's
  *           sequences is kept; a read may name a page any number of times.

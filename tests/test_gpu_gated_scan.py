@@ -550,3 +550,19 @@ def test_autograd_with_gradients_at_any_address(B, T, D, dtype):
     close(xs.grad, dx, b["dx"], dtype, "dx")
     close(gs.grad, dg, b["dg"], dtype, "dg")
     close(h0.grad, dh0, b["dh0"], F32, "dh0")
+
+
+@pytest.mark.parametrize("D", [64, 70])
+def test_lengths_out_of_a_longer_list(D):
+    """lens[1:] of a batch's list starts at 8 bytes, not at 16."""
+    x, g, dy, h, _ = (t.to(dev()) for t in make(3, 150, D, F32, "sigmoid", 27))
+    lens = torch.tensor([9, 150, 31, 0], device=dev())
+    assert lens[1:].data_ptr() % 16 == 8
+
+    def both(n):
+        y, last, marks = S.sanatan_gated_scan_fwd(x, g, "sigmoid", h0=h, lens=n, want_state=True,
+                                                  want_marks=True)
+        gr = S.sanatan_gated_scan_bwd(x, g, dy, marks, "sigmoid", lens=n, want_dh0=True)
+        return y, last, gr["dx"], gr["dg"], gr["dh0"]
+
+    assert all(torch.equal(a, b) for a, b in zip(both(lens[1:]), both(lens[1:].clone())))

@@ -282,3 +282,17 @@ def test_refusals_of_the_binding():
             W_(*bad)
     with pytest.raises(ValueError):
         S.sanatan_state_cache_read(codes, scales, pages, x[:, :1].expand(1, 2, 128))
+
+
+def test_pages_out_of_a_longer_list():
+    """pages[1:2], one sequence of a batch's list, starts at 8 bytes, not at 16."""
+    x = states(1, 1, 640, 10).to(dev())
+    codes, scales, _ = S.state_cache_empty(3, 640)
+    pages = torch.tensor([0, 2, 1], device=dev())
+    assert pages[1:2].data_ptr() % 16 == 8
+    S.sanatan_state_cache_write(x, pages[1:2], codes, scales)
+    out = torch.zeros_like(x)
+    S.sanatan_state_cache_read(codes, scales, pages[1:2], out)
+    c, s = R.cache_store(f64(x), "int8")
+    assert same(out, R.cache_values(c, s, 640)) and same(scales[2], s[0, 0][None])
+    assert not scales[:2].any()
