@@ -152,17 +152,16 @@ __global__ void __launch_bounds__(kThreads, TMA ? 2 : 1) scan_fwd_kernel(
   cluster.finish();
 }
 
-// One token: four elements a thread (the tensors are dense, so rows do not matter),
-// the last n % 4 by a thread each.
+// One token: four elements a thread (the tensors are dense, so rows do not matter) for
+// the first 4 * quads, the others by a thread each.
 template <typename E, int G>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(float* __restrict__ h,
                                                              const E* __restrict__ x,
                                                              const E* __restrict__ g, int64_t n,
-                                                             E* __restrict__ y) {
+                                                             int64_t quads, E* __restrict__ y) {
   using Q = Quad<E>;
   using QF = Quad<float>;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t quads = n / 4;
   wait_for_previous();
   V4 gv, xv, hv;
   const int64_t last = 4 * quads + (i - quads);
@@ -215,7 +214,9 @@ cudaError_t fwd(const ScanArgs& a, cudaStream_t st) {
 
 template <typename E, int G>
 cudaError_t step(float* h, const void* x, const void* g, int64_t n, void* y, cudaStream_t st) {
-  const int64_t threads = n / 4 + n % 4;
+  // (the state of one sequence of a batch may start at any float)
+  const int64_t quads = reinterpret_cast<uintptr_t>(h) % 16 == 0 ? n / 4 : 0;
+  const int64_t threads = quads + (n - 4 * quads);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads));
   cfg.blockDim = dim3(kThreads);
@@ -224,7 +225,7 @@ cudaError_t step(float* h, const void* x, const void* g, int64_t n, void* y, cud
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, scan_step_kernel<E, G>, h, static_cast<const E*>(x),
-                            static_cast<const E*>(g), n, static_cast<E*>(y));
+                            static_cast<const E*>(g), n, quads, static_cast<E*>(y));
 }
 
 }  // namespace

@@ -147,7 +147,7 @@ __device__ __forceinline__ void store(float* x, int left, const float (&v)[4]) {
 // One part (64 groups, 16 KB of values) of a stretch.  kLanes lanes have a group; lane
 // l its words (four values) l, l + kLanes, ..., so that a warp reads whole lines of
 // values and whole sectors of codes.  All of a thread's loads are under way before the
-// first is used: eight of 16 bytes when writing (VEC, inner a multiple of 4).  Writing
+// first is used: eight of 16 bytes when writing (VEC: stretches at 16 bytes).  Writing
 // takes eight lanes a group (three exchanges for eight values: 168 us where sixteen
 // lanes took 184), reading sixteen and twice the threads (whole lines of codes, four
 // loads a thread: one sequence in 5.0 us instead of 5.9).
@@ -259,8 +259,9 @@ cudaError_t launch(const CacheArgs& a, cudaStream_t st) {
   cudaLaunchAttribute attr = pdl_attribute();
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return a.inner % 4 == 0 ? cudaLaunchKernelEx(&cfg, cache_kernel<F, WRITE, true>, a)
-                          : cudaLaunchKernelEx(&cfg, cache_kernel<F, WRITE, false>, a);
+  const bool vec = a.inner % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+  return vec ? cudaLaunchKernelEx(&cfg, cache_kernel<F, WRITE, true>, a)
+             : cudaLaunchKernelEx(&cfg, cache_kernel<F, WRITE, false>, a);
 }
 
 }  // namespace

@@ -447,6 +447,8 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  *           passes them unchanged.  NULL: all T tokens.
  *   h0      [B, D] f32 or NULL (zero): the state before the first token
  *   h_out   [B, D] f32 or NULL: the state after the last token
+ *           States, also the step's and their gradients, may start at any float
+ *           (a row of a batch's states of odd width).
  *   marks   sanatan_gated_scan_marks_size(B, T, D) bytes or NULL: float32
  *           [B, ceil(T / 64), D], the states before tokens 0, 64, 128, ...,
  *           from which the backward recomputes h.
@@ -518,6 +520,8 @@ SANATAN_API int sanatan_gated_scan_step(float* h, const void* x, const void* g, 
  *     A group whose largest magnitude is below 2^-100 is stored as zeros, one
  *     with a value that is not finite, or is 2^127 or more, reads back as NaN.
  *   exact_cache  [num_pages, layers, exact_inner] f32 or NULL.
+ *   codes start at 16 bytes, the float32 arrays at any float (slowly for a state
+ *   whose inner is a multiple of 4: read and written by the element then).
  * Pages that the call does not name, and state of sequences left out, stay as
  * they were.  The fill of a last group (inner not a multiple of 64) is stored as
  * code 0.  Two calls that write the same page must be ordered by the caller.

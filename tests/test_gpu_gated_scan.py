@@ -566,3 +566,27 @@ def test_lengths_out_of_a_longer_list(D):
         return y, last, gr["dx"], gr["dg"], gr["dh0"]
 
     assert all(torch.equal(a, b) for a, b in zip(both(lens[1:]), both(lens[1:].clone())))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,D", [(90, 771), (300, 64), (1, 5)])
+def test_states_of_one_sequence_out_of_a_batch(T, D, dtype):
+    """h[b:b + 1] of a batch's states (odd widths: at any float): as initial, last and step's
+    state, updated where it is; the others stay as they were."""
+    x, g, dy, h, dh = (t.to(dev()) for t in make(1, T, D, dtype, "log", 28))
+    many = torch.randn(3 * D + 2, device=dev())
+    slot, gslot = many[2:].view(3, D)[1:2], torch.cat([many[:1], dh[0]])[1:].view(1, D)
+    assert slot.data_ptr() % 16 and gslot.data_ptr() % 16
+    slot.copy_(h)
+    kept = many.clone()
+    y, last, marks = S.sanatan_gated_scan_fwd(x, g, h0=h, want_state=True, want_marks=True)
+    y2, _, _ = S.sanatan_gated_scan_fwd(x, g, h0=slot, h_out=slot)
+    assert torch.equal(y, y2) and torch.equal(slot, last)
+    a = S.sanatan_gated_scan_bwd(x, g, dy, marks, dh_last=dh, want_dh0=True)
+    b = S.sanatan_gated_scan_bwd(x, g, dy, marks, dh_last=gslot, want_dh0=True)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    one = S.sanatan_gated_scan_step(last, x[:, 0].contiguous(), g[:, 0].contiguous())
+    two = S.sanatan_gated_scan_step(slot, x[:, 0].contiguous(), g[:, 0].contiguous())
+    assert torch.equal(one, two) and torch.equal(slot, last)
+    kept[2 + D:2 + 2 * D] = many[2 + D:2 + 2 * D]
+    assert torch.equal(kept, many)

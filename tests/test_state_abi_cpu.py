@@ -50,3 +50,17 @@ def test_index_arrays_start_at_any_element(lib):
     for call in (write, read):
         assert call(lib, pages=P((2 << 20) + 8)) == UNSUPPORTED
         assert call(lib, pages=P((2 << 20) + 4)) == INVALID
+
+
+def test_states_start_at_any_element(lib):
+    for name in ("h0", "h_out"):
+        assert fwd(lib, B=0, **{name: P(4)}) == OK
+        assert fwd(lib, B=0, **{name: P(2)}) == INVALID
+    for name in ("dh_out", "dh0"):
+        assert bwd(lib, B=0, **{name: P(4)}) == OK
+        assert bwd(lib, B=0, **{name: P(2)}) == INVALID
+    for call in (write, read):
+        for name in ("state", "scales", "exact", "exact_cache"):
+            args = dict(exact_inner=3, exact=P(5 << 20), exact_cache=P(6 << 20))
+            assert call(lib, **{**args, name: P((7 << 20) + 4)}) == UNSUPPORTED, name
+            assert call(lib, **{**args, name: P((7 << 20) + 2)}) == INVALID, name
