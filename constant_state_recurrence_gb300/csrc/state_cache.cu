@@ -103,19 +103,20 @@ __device__ __forceinline__ void restore(uint32_t word, float scale, float (&v)[4
   }
 }
 
-// The page of sequence b, or -1: none, or a later sequence of the call writes it.  By
-// all threads of the block.
-__device__ __forceinline__ int64_t page_of(const CacheArgs& a, int b, bool writing) {
-  constexpr int kThreads = threads_of(true);
+// The page of sequence b, or -1: none.
+__device__ __forceinline__ int64_t page_of(const CacheArgs& a, int b) {
   const int64_t p = a.pages[b];
-  if (p < 0 || p >= a.num_pages) return -1;
-  if (writing) {
-    bool later = false;
-    for (int i = b + 1 + static_cast<int>(threadIdx.x); i < a.B; i += kThreads)
-      later |= a.pages[i] == p;
-    if (__syncthreads_or(later)) return -1;
-  }
-  return p;
+  return p >= a.num_pages ? -1 : p;
+}
+
+// Whether a later sequence of the call writes page p of sequence b too.  By all threads
+// of a writing block.
+__device__ __forceinline__ bool written_later(const CacheArgs& a, int b, int64_t p) {
+  constexpr int kThreads = threads_of(true);
+  bool later = false;
+  for (int i = b + 1 + static_cast<int>(threadIdx.x); i < a.B; i += kThreads)
+    later |= a.pages[i] == p;
+  return __syncthreads_or(later);
 }
 
 // Four values from x on, of which `left` are there (VEC: all or none).
@@ -171,6 +172,9 @@ __global__ void __launch_bounds__(threads_of(WRITE)) cache_kernel(const CacheArg
   float* x = a.state + row * a.inner + g0 * kGroup;
   wait_for_previous();
 
+  // Before any other load: nothing of a sequence that is left out is read.
+  const int64_t p = page_of(a, b);
+  if (p < 0) return;
   if (WRITE) {
     float v[kBatch][kWords][4];
 #pragma unroll
@@ -180,8 +184,7 @@ __global__ void __launch_bounds__(threads_of(WRITE)) cache_kernel(const CacheArg
         const int k = (first + u * kRows) * kGroup + 4 * (lane + i * kLanes);
         load<VEC>(x + k, values - k, v[u][i]);
       }
-    const int64_t p = page_of(a, b, true);
-    if (p < 0) return;
+    if (written_later(a, b, p)) return;
     const int64_t page = (p * a.layers + l) * groups + g0;
     uint32_t* codes = reinterpret_cast<uint32_t*>(a.codes) + page * 16;
     float* scales = a.scales + page;
@@ -216,8 +219,6 @@ __global__ void __launch_bounds__(threads_of(WRITE)) cache_kernel(const CacheArg
       a.exact_cache[(p * a.layers + l) * a.exact_inner + k] = a.exact[row * a.exact_inner + k];
     return;
   }
-  const int64_t p = page_of(a, b, false);
-  if (p < 0) return;
   const int64_t page = (p * a.layers + l) * groups + g0;
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes) + page * 16;
   const float* scales = a.scales + page;
