@@ -263,7 +263,8 @@ struct CacheArgs {
   float* scales = nullptr;         // [num_pages, layers, ceil(inner / 64)]
   float* exact_cache = nullptr;    // [num_pages, layers, exact_inner] or null
   unsigned blocks = 0;             // thread blocks of one stretch
+  int begin = 0, end = 0;          // sequences of one launch (set by the launcher)
 };
 int64_t state_cache_blocks(int64_t inner);
-cudaError_t state_cache_launch(const CacheArgs& a, bool write, cudaStream_t st);
+cudaError_t state_cache_launch(CacheArgs a, bool write, cudaStream_t st);
 }  // namespace sanatan

@@ -347,3 +347,39 @@ def test_sequences_left_out_are_not_read():
     every = gpu_ms(lambda: S.sanatan_state_cache_write(x, pages, codes, scales, layers=layers))
     left = gpu_ms(lambda: S.sanatan_state_cache_write(x, none, codes, scales, layers=layers))
     assert left < every / 2, (left, every)
+
+
+@pytest.mark.parametrize("layers", [1, 3])
+def test_pages_named_again_much_later_in_a_large_write(layers):
+    """Thousands of sequences in one write, most pages named twice, near and far: the last
+    of the call's sequences is kept, whole."""
+    B, inner, zi = 9001, 70, 3
+    x = states(layers, B, inner, 12).to(dev())
+    z = torch.rand(layers, B, zi, device=dev())
+    gen = torch.Generator().manual_seed(13)
+    pages = torch.randint(-1, 5000, (B,), generator=gen)
+    pages[-1] = pages[0] = 17
+    codes, scales, zc = S.state_cache_empty(5000, inner, zi, layers)
+    S.sanatan_state_cache_write(x, pages.to(dev()), codes, scales, z, zc, layers)
+    last = {p: b for b, p in enumerate(pages.tolist()) if p >= 0}
+    named = torch.tensor(sorted(last))
+    at = torch.tensor([last[p] for p in named.tolist()])
+    c, s = R.cache_store(f64(x)[:, at.numpy()], "int8")
+    assert same(code_values(codes)[named].transpose(0, 1), c)
+    assert same(scales.cpu()[named].transpose(0, 1), s)
+    assert torch.equal(zc[named.to(dev())].transpose(0, 1), z[:, at.to(dev())])
+    free = torch.ones(5000, dtype=torch.bool)
+    free[named] = False
+    assert not scales.cpu()[free].any() and not code_values(codes)[free.to(dev())].any()
+
+
+def test_writes_take_time_in_proportion_to_their_sequences():
+    """Eight times the (small) sequences: not 64 times the time."""
+    def ms(B):
+        x = torch.ones(B, 64, device=dev())
+        codes, scales, _ = S.state_cache_empty(B, 64)
+        pages = torch.arange(B, device=dev())
+        return gpu_ms(lambda: S.sanatan_state_cache_write(x, pages, codes, scales))
+
+    small, large = ms(1 << 15), ms(1 << 18)
+    assert large < 20 * small, (small, large)
