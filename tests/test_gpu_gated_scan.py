@@ -590,3 +590,73 @@ def test_states_of_one_sequence_out_of_a_batch(T, D, dtype):
     assert torch.equal(one, two) and torch.equal(slot, last)
     kept[2 + D:2 + 2 * D] = many[2 + D:2 + 2 * D]
     assert torch.equal(kept, many)
+
+
+def decays(g, gate):
+    """The decays that step, scan and backward use: of a state 1 with nothing added, and of
+    a gradient 1 with nothing added."""
+    g = g.view(1, -1)
+    zero, one = torch.zeros_like(g), torch.ones_like(g)
+    h = one.clone()
+    S.sanatan_gated_scan_step(h, zero, g, gate)
+    g3, zero3 = g[:, None], zero[:, None]
+    y, _, marks = S.sanatan_gated_scan_fwd(zero3, g3, gate, h0=one, want_marks=True)
+    d = S.sanatan_gated_scan_bwd(zero3, g3, zero3, marks, gate, dh_last=one, want_dh0=True)
+    assert torch.equal(h, y[:, 0]) and torch.equal(h, d["dh0"])
+    return f64(h)[0]
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+def test_decays_next_to_one(odd):
+    """Steps E = 2^-24 of the decay itself.  Log gate, |g| < 1/16: the last of five terms
+    rounds by E / 2, the ones within by |g| E / 2 and |g|^2 E / 4 and less (1.07 E / 2 at
+    1/16), and the sixth, left out, is g^5 / 120 <= 0.134 E: 0.67 E, and on average (the
+    roundings come out even; the sixth term averages to 0.022 E, the inner ones to at most
+    0.035 E) less than 0.08 E.  Sigmoid, g > 2.8: e = exp(-g) is within (4 + 2 g) E of its
+    value (power of two 4 E, its argument 2 g E), which moves the decay 1 / (1 + e) by at
+    most 1 - a times that; rounding it once adds E / 2, the reciprocal's error squared
+    nothing to speak of (4 (1 - a) E are more than that)."""
+    n = (1 << 16) + odd
+    gen = torch.Generator().manual_seed(29 + odd)
+    g = -torch.rand(n, generator=gen) / 16
+    off = decays(g.to(dev()), "log") - np.exp(f64(g))
+    assert np.abs(off).max() <= 0.67 * E
+    assert abs(off.mean()) <= 0.08 * E
+    g = 2.8 + 9 * torch.rand(n, generator=gen)
+    keep = 1 / (1 + np.exp(f64(g)))
+    off = decays(g.to(dev()), "sigmoid") - (1 - keep)
+    assert (np.abs(off) <= (0.5 + keep * (8 + 2 * f64(g))) * E).all()
+
+
+@pytest.mark.parametrize("gate", ["log", "sigmoid"])
+@pytest.mark.parametrize("D", [64, 61])
+def test_constant_gates_next_to_one(gate, D):
+    """Gates that do not change from token to token, whose decays' errors do not average out,
+    over 32768 tokens of input 1.  A token adds its decay's error (see above), one product
+    of decays (a tree of products has fewer than a token each: E / 2 of a product above 3/4) and
+    a sixteenth of an addition to the state: together under 3 E / 4; and a scan in pieces
+    40 E of the state on its way."""
+    T = 32768
+    if gate == "log":
+        g = -torch.logspace(-4, -3, D)
+        k = np.full(D, 0.67 * E)
+        a, u = np.exp(f64(g)), np.ones(D)
+    else:
+        g = torch.linspace(7, 10, D)
+        u = 1 / (1 + np.exp(f64(g)))
+        k = (0.5 + u * (8 + 2 * f64(g))) * E
+        a = 1 - u
+    x = torch.ones(1, T, D, device=dev())
+    y, last, _ = S.sanatan_gated_scan_fwd(x, g.to(dev()).expand(1, T, D).contiguous(), gate,
+                                          want_state=True)
+    n = np.arange(1, T + 1)[:, None]
+    ref = u * -np.expm1(n * np.log(a)) / (1 - a)                   # u (1 - a^n) / (1 - a)
+    err = np.zeros(D)
+    room = np.zeros((T, D))
+    ku = (8 + 2 * np.abs(f64(g))) * E * (gate == "sigmoid")
+    for t in range(T):
+        before = ref[t - 1] if t else np.zeros(D)
+        err = a * err + (k + 0.75 * E) * before + ku * u
+        room[t] = err + 40 * E * ref[t]
+    close(y[0], ref, room, F32, "y")
+    close(last[0], ref[-1], room[-1], F32, "last")
