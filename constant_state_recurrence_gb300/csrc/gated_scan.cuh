@@ -41,10 +41,9 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <mutex>
-
 #include "f32x2.cuh"
 #include "pdl.cuh"
+#include "per_device.h"
 #include "sanatan_internal.h"
 #include "sanatan_math.cuh"
 #include "tc_ptx.cuh"
@@ -450,17 +449,23 @@ __device__ __forceinline__ void warp_scan(int tid, const V4& A, const V4& H, V4&
 
 constexpr int exchange_bytes(int cluster, int lanes) { return 2 * cluster * 2 * lanes * 16; }
 
-// cuTensorMapEncodeTiled, looked up once through the runtime.
+// cuTensorMapEncodeTiled, looked up through the runtime until it is found.
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+  static PerDevice<PFN_cuTensorMapEncodeTiled_v12000, 1> known;
+  PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  const cudaError_t e = known.get(0, &fn, [](PFN_cuTensorMapEncodeTiled_v12000* out) {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                                     cudaEnableDefault, &q) == cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
-  }();
-  return fn;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                           cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess) return cudaErrorSymbolNotFound;
+    *out = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    return cudaSuccess;
+  });
+  if (e == cudaSuccess) return fn;
+  cudaGetLastError();  // (the call goes on without tensor maps)
+  return nullptr;
 }
 
 // The map of a [B, T, D] tensor (rows of a multiple of 16 bytes) with boxes of `rows`
@@ -468,20 +473,20 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
 // format's range).
 bool encode(CUtensorMap* map, const void* p, int dtype, int B, int T, int D, int rows, int width) {
   const cuuint64_t e = dtype == SANATAN_F32 ? 4 : 2;
-  if (map_encoder() == nullptr) return false;
+  const PFN_cuTensorMapEncodeTiled_v12000 encoder = map_encoder();
+  if (encoder == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(T),
                               static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[2] = {D * e, static_cast<cuuint64_t>(T) * D * e};
   if (strides[1] >= (1ull << 40)) return false;
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(rows), 1};
   const cuuint32_t step[3] = {1, 1, 1};
-  return map_encoder()(map,
-                       dtype == SANATAN_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                       3, const_cast<void*>(p), dims, strides, box, step,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encoder(map,
+                 dtype == SANATAN_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                 3, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A launch shape: CTAs of a cluster, and the steps that the longest CTA takes (over
@@ -509,7 +514,8 @@ cudaLaunchConfig_t config(int64_t ctas, int cluster, cudaLaunchAttribute* attr, 
 }
 
 // held[n]: clusters of n CTAs of a kernel that the current device holds at once.  The
-// runtime is asked once a device, when the kernel's attributes are set too.
+// runtime is asked once a device (again after a failure), when the kernel's attributes are
+// set too.
 struct Held {
   int held[kMaxCluster + 1] = {};
 };
@@ -524,26 +530,22 @@ cudaError_t ask(Held* out) {
   for (int n = 1; e == cudaSuccess && n <= kMaxCluster; ++n) {
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = config<Args, Ring>(n, n, attr, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&out->held[n], Kernel, &cfg) != cudaSuccess) {
+    e = cudaOccupancyMaxActiveClusters(&out->held[n], Kernel, &cfg);
+    if (e == cudaErrorInvalidClusterSize || e == cudaErrorInvalidConfiguration ||
+        e == cudaErrorLaunchOutOfResources) {  // none of this size
       cudaGetLastError();
       out->held[n] = 0;
+      e = cudaSuccess;
     }
   }
   return e;
 }
 template <auto Kernel, typename Args, typename Ring>
 cudaError_t held_by(Held* out) {
-  constexpr int kDevices = 16;
-  static std::once_flag once[kDevices];
-  static Held known[kDevices];
-  static cudaError_t failed[kDevices];
+  static PerDevice<Held> known;
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= kDevices) return ask<Kernel, Args, Ring>(out);
-  std::call_once(once[dev], [&] { failed[dev] = ask<Kernel, Args, Ring>(&known[dev]); });
-  *out = known[dev];
-  return failed[dev];
+  return e != cudaSuccess ? e : known.get(dev, out, ask<Kernel, Args, Ring>);
 }
 
 // Few sequences: the largest cluster with which all clusters still run at once (a
