@@ -348,7 +348,7 @@ struct Exchange {
 __device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes) {
   asm volatile(
       "{\n\t.reg .b64 st;\n\t"
-      "mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(
+      "mbarrier.arrive.expect_tx.relaxed.cluster.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(
           tc::smem_u32(bar)),
       "r"(bytes)
       : "memory");
@@ -356,10 +356,10 @@ __device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes) {
 
 // The cluster's side of the recurrence, by warp 0, lane = channel pair.  A step:
 // share() sends the CTA's map to every CTA of the cluster (st.async, counted by
-// the receiver's mbarrier; a cluster barrier instead would make every thread wait
-// for its own global stores), arrive() waits for all of them and takes carry over
-// them.  Buffers alternate: who sends step s + 2 has received step s + 1 from
-// every CTA, and they sent that after reading step s.
+// the receiver's mbarrier and acquired at cluster scope; a cluster barrier instead
+// would make every thread wait for its own global stores), arrive() waits for all of
+// them and takes carry over them.  Buffers alternate: who sends step s + 2 has received
+// step s + 1 from every CTA, and they sent that after reading step s.
 template <int LANES, bool BWD>
 struct Cluster {
   Exchange<LANES, BWD>& ex;
@@ -401,7 +401,7 @@ struct Cluster {
   }
   // What comes into this CTA's tile of step s.
   __device__ __forceinline__ uint64_t arrive(int s, uint64_t& carry) {
-    if (!dead && !tc::mbar_wait_bounded(&ex.full[s & 1], (s >> 1) & 1)) {
+    if (!dead && !tc::mbar_wait_cluster_bounded(&ex.full[s & 1], (s >> 1) & 1)) {
       dead = true;
       g_scan_error = 1;
     }

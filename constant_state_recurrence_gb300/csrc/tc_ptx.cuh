@@ -130,6 +130,29 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// As mbar_wait_bounded, for phases that other CTAs of the cluster complete (st.async,
+// remote arrivals): acquires at cluster scope what they wrote, where the plain wait
+// acquires at the CTA's.
+__device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t* bar, uint32_t parity,
+                                                          uint64_t timeout_ns = 2000000000ull) {
+  uint64_t t0 = 0;
+  for (uint32_t tries = 0;; ++tries) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok != 0) return true;
+    if (tries == 0)
+      t0 = globaltimer_ns();
+    else if (globaltimer_ns() - t0 > timeout_ns)
+      return false;
+  }
+}
+
 // ------------------------------------------------------------ registers / L2
 // Warpgroup-wide register re-balancing (all four warps of a warpgroup execute
 // the same instruction).  The increases drawn by some warpgroups must be
