@@ -660,3 +660,51 @@ def test_constant_gates_next_to_one(gate, D):
         room[t] = err + 40 * E * ref[t]
     close(y[0], ref, room, F32, "y")
     close(last[0], ref[-1], room[-1], F32, "last")
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 22000), (BF16, 22001)])
+def test_offsets_beyond_32_bits_backward_and_odd_rows(dtype, D):
+    """More than 2^31 elements, rows of 16 bytes and odd ones: the last sequence's outputs
+    and gradients are where they should be.  a = 1: sums forward and backward in time."""
+    B, T = 3, 32768
+    free = torch.cuda.mem_get_info()[0]
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    x = torch.zeros(B, T, D, dtype=dtype, device=dev())
+    g = torch.zeros_like(x)
+    dy = torch.zeros_like(x)
+    c = torch.arange(D, device=dev()).remainder(251).to(dtype)
+    x[2, -130], x[2, -2] = 1.0, c
+    dy[2, -1], dy[2, 5] = c, 2.0
+    y, last, marks = S.sanatan_gated_scan_fwd(x, g, want_state=True, want_marks=True)
+    assert torch.equal(last[2], c.float() + 1) and not last[:2].any()
+    assert torch.equal(y[2, -1], (c.float() + 1).to(dtype)) and (y[2, -130:-2] == 1).all()
+    assert not y[2, :-130].any() and not y[:2].any()
+    d = S.sanatan_gated_scan_bwd(x, g, dy, marks, want_dh0=True)
+    dx, dg = d["dx"], d["dg"]
+    assert torch.equal(dx[2, 6], c) and torch.equal(dx[2, -1], c)
+    assert torch.equal(dx[2, 5], (c.float() + 2).to(dtype)) and torch.equal(dx[2, 0], dx[2, 5])
+    assert not dx[:2].any() and not dg[:2].any() and not dg[2, :-129].any()
+    assert (dg[2, -129:-1] == c).all()                              # dh a h, h = 1 before
+    assert torch.equal(dg[2, -1], (c.float() * (c.float() + 1)).to(dtype))
+    assert torch.equal(d["dh0"][2], c.float() + 2) and not d["dh0"][:2].any()
+    S.device_status()
+
+
+@pytest.mark.parametrize("D", [64, 66])
+def test_gates_above_zero_grow(D):
+    """The log gate above 0, up to products of all decays next to the largest float32: what
+    the formula gives; zeros stay zeros."""
+    T = 300
+    x, g, dy, h, dh = make(2, T, D, F32, "log", 30)
+    g = torch.where(torch.arange(D) % 2 == 0, g + 0.5, torch.tensor(80.0 / T)).contiguous()
+    d = lambda t: t.to(dev())  # noqa: E731
+    y, last, marks = S.sanatan_gated_scan_fwd(d(x), d(g), h0=d(h), want_state=True,
+                                              want_marks=True)
+    ref, last_ref, _ = R.gated_scan(f64(x), f64(g), "log", f64(h))
+    b = bounds(f64(x), f64(g), "log", f64(h))
+    close(y, ref, b["y"], F32, "y")
+    close(last, last_ref, b["last"], F32, "last")
+    zero = torch.zeros_like(d(x))
+    y, last, _ = S.sanatan_gated_scan_fwd(zero, d(g), want_state=True)
+    assert not y.any() and not last.any()

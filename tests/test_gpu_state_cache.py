@@ -383,3 +383,25 @@ def test_writes_take_time_in_proportion_to_their_sequences():
 
     small, large = ms(1 << 15), ms(1 << 18)
     assert large < 20 * small, (small, large)
+
+
+def test_captured_large_write():
+    """A write of several launches in a graph, replayed on other states and pages."""
+    B, inner = 7000, 66
+    x = states(1, B, inner, 14).to(dev())
+    pages = torch.arange(B, device=dev()) % 3000
+    pool = S.state_cache_empty(3000, inner)[:2]
+    S.sanatan_state_cache_write(x, pages, *pool)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        S.sanatan_state_cache_write(x, pages, *pool)
+    x.mul_(-3)
+    pages.copy_(pages.flip(0).clone())
+    graph.replay()
+    torch.cuda.synchronize()
+    want = S.state_cache_empty(3000, inner)[:2]
+    S.sanatan_state_cache_write(x, pages, *want)
+    assert torch.equal(pool[0], want[0]) and torch.equal(pool[1], want[1])
+    c, s = R.cache_store(f64(x[0, -1000:]), "int8")      # nobody names these again
+    assert same(code_values(pool[0])[pages[-1000:]][:, 0], c)
