@@ -21,13 +21,14 @@
 //
 // Bound: bytes (three tensors forward, five backward), and beside them the latency of
 // a step: map, exchange, tokens.  Hence two CTAs an SM, and few steps rather than many
-// warps.  Forward, training shape (B 8 T 4096 D 768, bf16, log gate), GB300: 28.4 us;
+// warps.  Forward, training shape (B 8 T 4096 D 768, bf16, log gate), GB300: 28 us;
 // half the run and three or four CTAs an SM 34 and 37 us, a third stage 29.4; as
 // first built, a cluster barrier instead of st.async with a counting mbarrier made
 // 44 us into 60 (the barrier's release waits for every thread's global stores), cp.async
 // instead of TMA 27 into 32.  Device times of the measured copy rate: this forward
-// 5.3 TB/s (0.78), its backward 48 us, 5.2 TB/s (0.77); B 1 T 32768 D 768, sigmoid,
-// forward 36 us, 4.2 TB/s (0.62: one sequence's clusters do not fill the SMs evenly).
+// 5.4 TB/s (0.80), its backward 48 us, 5.2 TB/s (0.77), with the sigmoid 29 and 55 us;
+// B 1 T 32768 D 768, sigmoid, forward 37 us, 4.1 TB/s (0.60: one sequence's clusters do
+// not fill the SMs evenly), backward 76 us, 3.3 TB/s (0.49: twice the steps).
 // The same work without exchanges (24 sequences of 1408 tokens) takes 26.4 and 43.4 us.
 //
 // The backward needs h_{t-1}: the forward leaves the state before every 64th

@@ -156,7 +156,7 @@ __device__ __forceinline__ void store(float* x, int left, const float (&v)[4]) {
 // Bound: bytes.  64 sequences of 144 states (0.9 GB), int8, GB300: written in 168 us,
 // 7.0 TB/s, read in 169 us, 7.0 TB/s (a plain copy: 6.8).  Many small states are bound by
 // their blocks instead: 9,216 of 768 values (12 groups of the block's 64, 36 MB, 5.3 us at
-// the copy rate) are written in 40 us and read in 20.
+// the copy rate) are written in 34 us and read in 16.
 template <int F, bool WRITE, bool VEC>
 __global__ void __launch_bounds__(threads_of(WRITE)) cache_kernel(const CacheArgs a) {
   constexpr int kThreads = threads_of(WRITE);
@@ -281,8 +281,9 @@ int64_t state_cache_blocks(int64_t inner) {
 // Every block of a write looks through the pages of the launch's later sequences, so a
 // write of many goes in launches of about kAtOnce sequences (a page that two of them
 // write is the later one's, as within one): the work grows with the sequences, not their
-// square.  States of 768 values, int8, GB300: 9,216 in 40 us and 65,536 in 253 us (in one
-// launch 43 and 733; in launches of 2,048: 44 and 273, of 8,192: 43 and 269).
+// square.  States of 768 values, int8, GB300, from a flushed L2: 9,216 in 40 us and 65,536
+// in 253 us (in one launch 43 and 733; in launches of 2,048: 44 and 273, of 8,192: 43 and
+// 269).
 cudaError_t state_cache_launch(CacheArgs a, bool write, cudaStream_t st) {
   const int64_t all = a.B, parts = (all + kAtOnce / 2) / kAtOnce;
   const int64_t launches = write && parts > 1 ? parts : 1;

@@ -454,8 +454,10 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  *           from which the backward recomputes h.
  * With the log gate g <= 0 is meant; g = -inf (a = 0) starts a new text.  Gates
  * above 0 grow, and give what the formula gives while the products of the
- * decays stay finite.  Values that are not finite reach only later tokens (and,
- * backward, earlier ones) of their own sequence and channel.
+ * decays of any stretch of tokens stay finite (beyond, NaN may come also where
+ * the states themselves are finite); products below float32's range count as 0.
+ * Values that are not finite reach only later tokens (and, backward, earlier
+ * ones) of their own sequence and channel.
  * All sums are taken in a fixed order: the same call gives the same bits.
  * B = 0 or D = 0 does nothing; T = 0 copies h0 (or zeros) to h_out.
  *
