@@ -14,7 +14,7 @@ constexpr int kMaxPower = 8;   // largest p of sanatan_power_fwd
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
 bool ok_nullable(const void* p) { return p == nullptr || aligned16(p); }
-// Null, or where an element of `size` bytes may start: what kernels touch element by element.
+// Where an element of `size` bytes may start: for what kernels touch element by element.
 bool at_element(const void* p, size_t size) {
   return reinterpret_cast<uintptr_t>(p) % size == 0;
 }
@@ -84,10 +84,9 @@ int state_cache(float* state, float* exact, int layers, int B, int64_t inner, in
   if (static_cast<int64_t>(layers) * B == 0 || (inner == 0 && exact_inner == 0) || num_pages == 0)
     return SANATAN_OK;
   if (pages == nullptr || !at_element(pages, 8)) return SANATAN_ERR_INVALID;
-  if (inner > 0 && (!ok_floats(state) || !ok_ptr(codes) || !ok_floats(scales)))
+  if (inner > 0 && (!ok_floats(state) || !ok_ptr(codes) || !ok_ptr(scales)))
     return SANATAN_ERR_INVALID;
-  if (exact_inner > 0 && (!ok_floats(exact) || !ok_floats(exact_cache)))
-    return SANATAN_ERR_INVALID;
+  if (exact_inner > 0 && (!ok_floats(exact) || !ok_ptr(exact_cache))) return SANATAN_ERR_INVALID;
   // Thread blocks must fit a grid, and the largest offset 63 bits.
   const int64_t most = (1LL << 31) - 1;
   if (inner > (1LL << 40) || exact_inner > (1LL << 40) || num_pages > most)
@@ -631,7 +630,7 @@ int sanatan_gated_scan_fwd(const void* x, const void* g, int dtype, int gate, co
                            int B, int T, int D, const float* h0, void* y, float* h_out,
                            float* marks, void* stream) {
   if (int s = check_scan(dtype, gate, B, T, D)) return s;
-  if (!at_element(lens, 8) || !at_element(h0, 4) || !at_element(h_out, 4) || !ok_nullable(marks))
+  if (!ok_nullable(lens) || !ok_nullable(h0) || !ok_nullable(h_out) || !ok_nullable(marks))
     return SANATAN_ERR_INVALID;
   if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
   if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || !ok_ptr(y))) return SANATAN_ERR_INVALID;
@@ -670,8 +669,7 @@ int sanatan_gated_scan_bwd(const void* x, const void* g, const void* dy, int dty
                            const int64_t* lens, int B, int T, int D, const float* marks,
                            const float* dh_out, void* dx, void* dg, float* dh0, void* stream) {
   if (int s = check_scan(dtype, gate, B, T, D)) return s;
-  if (!at_element(lens, 8) || !at_element(dh_out, 4) || !at_element(dh0, 4))
-    return SANATAN_ERR_INVALID;
+  if (!ok_nullable(lens) || !ok_nullable(dh_out) || !ok_nullable(dh0)) return SANATAN_ERR_INVALID;
   if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
   if (T > 0 && (!ok_ptr(x) || !ok_ptr(g) || dy == nullptr ||
                 !at_element(dy, dtype == SANATAN_F32 ? 4 : 2) || !ok_ptr(marks) || !ok_ptr(dx) ||

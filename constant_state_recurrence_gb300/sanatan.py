@@ -770,6 +770,12 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _at16(t):
+    """t, or a copy of it where it does not start at 16 bytes: a part of a longer
+    list, one sequence's state of a batch's, a gradient cut out of a larger one."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.detach().clone()
+
+
 def _call(name, dev, *args):
     """Call a library function with the tensors' device current, on its stream
     (asked for raw: a Stream object costs as much as the launch)."""
@@ -801,6 +807,8 @@ def sanatan_gated_scan_fwd(x, g, gate="log", h0=None, lens=None, want_state=Fals
     or bf16): gate "log" has a = exp(g), u = x, gate "sigmoid" a = 1 / (1 +
     exp(-g)), u = (1 - a) x.  h0 [B, D] f32 is the state before the first
     token; tokens from lens[b] (int64 [B]) on are left out and give zeros.
+    lens, h0 and h_out may be parts of larger tensors (copied where the library
+    needs them at 16 bytes).
 
     Returns (y [B,T,D] in x's dtype, the last state [B,D] f32 or None, marks
     [B, ceil(T/64), D] f32 (states for the backward) or None)."""
@@ -814,8 +822,12 @@ def sanatan_gated_scan_fwd(x, g, gate="log", h0=None, lens=None, want_state=Fals
         h_out = torch.empty(B, D, dtype=torch.float32, device=dev)
     marks = torch.empty(B, -(-T // SCAN_MARK), D, dtype=torch.float32, device=dev) \
         if want_marks else None
+    lens, h0 = _at16(lens), _at16(h0)
+    last = _at16(h_out)
     _call("sanatan_gated_scan_fwd", dev, x.data_ptr(), g.data_ptr(), dt, gt, _at(lens), B, T, D,
-          _at(h0), y.data_ptr(), _at(h_out), _at(marks))
+          _at(h0), y.data_ptr(), _at(last), _at(marks))
+    if last is not h_out:
+        h_out.detach().copy_(last)
     return y, h_out, marks
 
 
@@ -829,6 +841,7 @@ def sanatan_gated_scan_bwd(x, g, dy, marks, gate="log", lens=None, dh_last=None,
         _fit(dh_last, "dh_last", torch.float32, (B, D), dev)
     dx, dg = torch.empty_like(x), torch.empty_like(g)
     dh0 = torch.empty(B, D, dtype=torch.float32, device=dev) if want_dh0 else None
+    lens, dh_last = _at16(lens), _at16(dh_last)
     _call("sanatan_gated_scan_bwd", dev, x.data_ptr(), g.data_ptr(), dy.data_ptr(), dt, gt,
           _at(lens), B, T, D, marks.data_ptr(), _at(dh_last), dx.data_ptr(), dg.data_ptr(),
           _at(dh0))

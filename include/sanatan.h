@@ -440,15 +440,12 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  * (The notes compare the method with gated linear attention, Table 1; the pages
  * give no formula for a gate, these are the plain ones.)
  *   x, g    [B, T, D]  dtype;   y [B, T, D] dtype (the float32 state rounded once)
- *   lens    [B] int64 or NULL, at 8 bytes (lens + 1 of a longer list will do): tokens
- *           of each sequence (values outside [0, T] are taken as the nearest of
- *           the two).  Tokens from lens[b] on
+ *   lens    [B] int64 or NULL: tokens of each sequence (values outside [0, T]
+ *           are taken as the nearest of the two).  Tokens from lens[b] on
  *           have no effect; their y, dx and dg are written as zeros, and the state
  *           passes them unchanged.  NULL: all T tokens.
  *   h0      [B, D] f32 or NULL (zero): the state before the first token
  *   h_out   [B, D] f32 or NULL: the state after the last token
- *           States, also the step's and their gradients, may start at any float
- *           (a row of a batch's states of odd width).
  *   marks   sanatan_gated_scan_marks_size(B, T, D) bytes or NULL: float32
  *           [B, ceil(T / 64), D], the states before tokens 0, 64, 128, ...,
  *           from which the backward recomputes h.
@@ -463,14 +460,15 @@ SANATAN_API int sanatan_decode_step(float* S, float* z, const float* q, const fl
  *
  * sanatan_gated_scan_bwd -- gradients of sum(y * dy) + sum(h_out * dh_out):
  *   marks as the forward wrote them for the same x, g, h0 and lens (h0 is their
- *   first row); dy [B, T, D] dtype; dh_out [B, D] f32 or NULL (zero): both may start at
- *   any element (the gradients of joined outputs come as slices of a larger one);
+ *   first row); dy [B, T, D] dtype, which may start at any element (the gradient of
+ *   a joined output is a slice of a larger one); dh_out [B, D] f32 or NULL (zero);
  *   dx, dg [B, T, D] dtype outputs; dh0 [B, D] f32 output or NULL.
  *     dh_t = dy_t + a_{t+1} dh_{t+1};  dh0 = a_0 dh_0;
  *     log: dx = dh, dg = dh a h_{t-1};
  *     sigmoid: dx = dh (1 - a), dg = dh (h_{t-1} - x) a (1 - a).
  * sanatan_gated_scan_step -- one token of N sequences: h [N, D] f32 is updated
- *   in place, x, g, y [N, D] dtype.
+ *   in place and may start at any float (a row of a batch's states); x, g, y [N, D]
+ *   dtype.
  * Errors: SANATAN_ERR_INVALID for an unknown dtype or gate, a negative size, a
  * null (where not allowed) or misaligned pointer; SANATAN_ERR_UNSUPPORTED for
  * B * D (N * D) of 2^31 or more, or T or D above 2^30.  Outputs share no bytes with
@@ -522,8 +520,9 @@ SANATAN_API int sanatan_gated_scan_step(float* h, const void* x, const void* g, 
  *     A group whose largest magnitude is below 2^-100 is stored as zeros, one
  *     with a value that is not finite, or is 2^127 or more, reads back as NaN.
  *   exact_cache  [num_pages, layers, exact_inner] f32 or NULL.
- *   codes start at 16 bytes, the float32 arrays at any float (slowly for a state
- *   whose inner is a multiple of 4: read and written by the element then).
+ *   state and exact may start at any float (a row of a batch's; a state whose
+ *   stretches do not start at 16 bytes is read and written by the element), the
+ *   pool's arrays start at 16 bytes.
  * Pages that the call does not name, and state of sequences left out, stay as
  * they were.  The fill of a last group (inner not a multiple of 64) is stored as
  * code 0.  Two calls that write the same page must be ordered by the caller.

@@ -301,25 +301,20 @@ def test_pages_out_of_a_longer_list():
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("inner,zi", [(771, 5), (640, 7), (3, 1), (24576, 384)])
 def test_states_at_any_float(fmt, inner, zi):
-    """One sequence's state and z out of a batch's, and a pool that is part of a larger one."""
+    """One sequence's state and z out of a batch's."""
     x, z = states(1, 1, inner, 11), torch.rand(zi)
     at = lambda n: torch.full((n + 1,), 3.0, device=dev())  # noqa: E731
     xs, zs, xo, zo = at(inner), at(zi), at(inner), at(zi)
     xs[1:] = x.flatten().to(dev())
     zs[1:] = z.to(dev())
-    groups = -(-inner // 64)
-    codes, _, _ = S.state_cache_empty(2, inner, dtype=DT[fmt])
-    scales, zc = at(2 * groups), at(2 * zi)
+    codes, scales, zc = S.state_cache_empty(2, inner, zi, dtype=DT[fmt])
     page = torch.ones(1, dtype=torch.int64, device=dev())
-    pool = (codes, scales[1:].view(2, 1, groups))
-    S.sanatan_state_cache_write(xs[1:].view(1, inner), page, *pool, zs[1:].view(1, zi),
-                                zc[1:].view(2, 1, zi))
-    S.sanatan_state_cache_read(*pool, page, xo[1:].view(1, inner), zc[1:].view(2, 1, zi),
-                               zo[1:].view(1, zi))
+    S.sanatan_state_cache_write(xs[1:].view(1, inner), page, codes, scales, zs[1:].view(1, zi), zc)
+    S.sanatan_state_cache_read(codes, scales, page, xo[1:].view(1, inner), zc, zo[1:].view(1, zi))
     c, s = R.cache_store(f64(x), fmt)
-    assert same(code_values(codes)[1, 0], c[0, 0]) and same(scales[1 + groups:], s[0, 0])
+    assert same(code_values(codes)[1, 0], c[0, 0]) and same(scales[1, 0], s[0, 0])
     assert same(xo[1:], R.cache_values(c, s, inner)[0, 0]) and torch.equal(zo, zs)
-    assert xo[0] == 3 and (scales[:1 + groups] == 3).all() and (zc[:1 + zi] == 3).all()
+    assert xo[0] == 3 and not scales[0].any() and not zc[0].any()
     assert not code_values(codes)[0].any()
 
 
