@@ -1,6 +1,8 @@
 // C ABI of libsanatan.so: host-side validation and dispatch (see sanatan.h).
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include "sanatan_internal.h"
 
@@ -72,6 +74,83 @@ struct Range {
 bool overlap(const void* a, size_t n, const void* b, size_t m) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a != nullptr && b != nullptr && n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
+// Whether an output shares bytes with an input or another output.  may[k] = {output, input}
+// are pairs that may be one and the same tensor.
+struct Pair {
+  int out, in;
+};
+bool clash(std::initializer_list<Range> out, std::initializer_list<Range> in,
+           std::initializer_list<Pair> may = {}) {
+  int o = 0;
+  for (const Range* x = out.begin(); x != out.end(); ++x, ++o) {
+    int i = 0;
+    for (const Range* y = in.begin(); y != in.end(); ++y, ++i) {
+      bool same = false;
+      for (const Pair& m : may) same |= m.out == o && m.in == i && x->p == y->p;
+      if (!same && overlap(x->p, x->n, y->p, y->n)) return true;
+    }
+    for (const Range* y = out.begin(); y != x; ++y)
+      if (overlap(x->p, x->n, y->p, y->n)) return true;
+  }
+  return false;
+}
+
+size_t size_of(int dtype) { return dtype == SANATAN_F32 ? 4 : 2; }
+
+// Pointers that may start at any element: null only where `nullable`.
+bool at_elements(std::initializer_list<const void*> all, size_t size, bool nullable = false) {
+  for (const void* p : all)
+    if ((p == nullptr && !nullable) || !at_element(p, size)) return false;
+  return true;
+}
+
+// Bytes of `rows` rows of `width` values, ld between two.
+size_t span(int64_t rows, int64_t ld, int64_t width, size_t size) {
+  return rows <= 0 ? 0 : (static_cast<size_t>(rows - 1) * ld + width) * size;
+}
+
+// Sizes of the layers over [B, T, D] (width: values of the widest row; N: states).
+int check_layer(int dtype, int B, int T, int D, int64_t widest, int N) {
+  if (!ok_dtype(dtype) || B < 0 || T < 0 || D < 0) return SANATAN_ERR_INVALID;
+  if (static_cast<int64_t>(B) * D > (1LL << 31) - 1) return SANATAN_ERR_UNSUPPORTED;
+  if (T > (1 << 30) || D > (1 << 30)) return SANATAN_ERR_UNSUPPORTED;
+  const double tokens = static_cast<double>(B) * (T + 16.0);
+  // Offsets fit 60 bits; a thread block holds at least 128 of a launch's items.
+  if (tokens * widest > 1e18 || tokens * D * N > 1e18) return SANATAN_ERR_UNSUPPORTED;
+  if (tokens / 16 * D / 128 > 2e9 || tokens * N / 128 > 2e9) return SANATAN_ERR_UNSUPPORTED;
+  return SANATAN_OK;
+}
+
+int check_norm(int dtype, int64_t rows, int D) {
+  if (!ok_dtype(dtype) || rows < 0 || D < 0) return SANATAN_ERR_INVALID;
+  return rows > (1LL << 31) - 1 || D > (1 << 30) ? SANATAN_ERR_UNSUPPORTED : SANATAN_OK;
+}
+
+int check_conv(int dtype, int act, int B, int T, int D, int K, int64_t ldx) {
+  if (act != SANATAN_ACT_NONE && act != SANATAN_ACT_SILU) return SANATAN_ERR_INVALID;
+  if (K < 1 || ldx < D) return SANATAN_ERR_INVALID;
+  if (int s = check_layer(dtype, B, T, D, ldx, 1)) return s;
+  return K > kConvTaps ? SANATAN_ERR_UNSUPPORTED : SANATAN_OK;
+}
+
+// The selective scan's inputs, shared by its calls (T = 1: the step, lens and h0 null).
+int check_selective(const SelectiveArgs& a) {
+  if (a.N < 1 || a.ldb < a.N || a.ldc < a.N || (a.z != nullptr && a.ldz < a.D))
+    return SANATAN_ERR_INVALID;
+  const int64_t widest = std::max(std::max(a.ldb, a.ldc), a.z != nullptr ? a.ldz : 0);
+  if (int s = check_layer(a.dtype, a.B, a.T, a.D, std::max<int64_t>(widest, a.D),
+                          std::min(a.N, kSelectiveStates)))
+    return s;
+  if (a.N > kSelectiveStates) return SANATAN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(a.B) * a.D == 0) return SANATAN_OK;
+  const size_t e = size_of(a.dtype);
+  if (!at_elements({a.A}, 4) || !at_elements({a.skip, a.dt_bias, a.h0, a.h_out, a.marks}, 4, true) ||
+      !at_elements({a.lens}, 8, true) || !at_elements({a.z}, e, true))
+    return SANATAN_ERR_INVALID;
+  if (a.T > 0 && !at_elements({a.u, a.dt, a.Bm, a.Cm}, e)) return SANATAN_ERR_INVALID;
+  return SANATAN_OK;
 }
 
 // Argument checks and launch of the state cache's two directions.
@@ -739,6 +818,364 @@ int sanatan_state_cache_read(const void* codes, const float* scales, const float
   return state_cache(state, exact, layers, B, inner, exact_inner, pages, num_pages, fmt,
                      const_cast<void*>(codes), const_cast<float*>(scales),
                      const_cast<float*>(exact_cache), false, stream);
+}
+
+int sanatan_layer_norm_fwd(const void* x, const void* residual, const float* weight,
+                           const float* bias, int dtype, int64_t rows, int D, float eps, void* y,
+                           void* sum, float* stats, void* stream) {
+  if (int s = check_norm(dtype, rows, D)) return s;
+  if (rows == 0 || D == 0) return SANATAN_OK;
+  const size_t e = size_of(dtype), all = static_cast<size_t>(rows) * D * e;
+  const size_t row = static_cast<size_t>(D) * 4;
+  if (!at_elements({x, y}, e) || !at_elements({residual, sum}, e, true) ||
+      !at_elements({weight, bias, stats}, 4, true))
+    return SANATAN_ERR_INVALID;
+  if (sum != nullptr && residual == nullptr) return SANATAN_ERR_INVALID;
+  if (clash({{y, all}, {sum, all}, {stats, static_cast<size_t>(rows) * 8}},
+            {{x, all}, {residual, all}, {weight, row}, {bias, row}}, {{1, 1}}))
+    return SANATAN_ERR_INVALID;
+  if (int s = check_arch()) return s;
+  NormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.bias = bias;
+  a.dtype = dtype;
+  a.rows = rows;
+  a.D = D;
+  a.eps = eps;
+  a.y = y;
+  a.sum = sum;
+  a.stats = stats;
+  return from_cuda(layer_norm_fwd_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sanatan_layer_norm_bwd_workspace_size(int64_t rows, int D) {
+  return layer_norm_bwd_workspace_bytes(rows, D);
+}
+
+int sanatan_layer_norm_bwd(const void* s, const float* weight, const void* dy, const void* ds,
+                           const float* stats, int dtype, int64_t rows, int D, void* dx,
+                           float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (int st = check_norm(dtype, rows, D)) return st;
+  if (D == 0) return SANATAN_OK;
+  const size_t e = size_of(dtype), all = static_cast<size_t>(rows) * D * e;
+  const size_t row = static_cast<size_t>(D) * 4;
+  if (!at_elements({weight, dweight, dbias, workspace}, 4, true)) return SANATAN_ERR_INVALID;
+  if (rows > 0 && (!at_elements({s, dy, dx}, e) || !at_elements({ds}, e, true) ||
+                   !at_elements({stats}, 4)))
+    return SANATAN_ERR_INVALID;
+  const bool sums = rows > 0 && (dweight != nullptr || dbias != nullptr);
+  const size_t need = sums ? layer_norm_bwd_workspace_bytes(rows, D) : 0;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SANATAN_ERR_INVALID;
+  if (clash({{dx, all}, {dweight, row}, {dbias, row}, {workspace, need}},
+            {{s, all}, {weight, row}, {dy, all}, {ds, all}, {stats, static_cast<size_t>(rows) * 8}},
+            {}))
+    return SANATAN_ERR_INVALID;
+  if (int st = check_arch()) return st;
+  NormBwdArgs a;
+  a.s = s;
+  a.weight = weight;
+  a.dy = dy;
+  a.ds = ds;
+  a.stats = stats;
+  a.dtype = dtype;
+  a.rows = rows;
+  a.D = D;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.parts = static_cast<float*>(workspace);
+  return from_cuda(layer_norm_bwd_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+int sanatan_causal_conv_fwd(const void* x, int64_t ldx, const float* w, const float* bias,
+                            int dtype, int act, const int64_t* lens, int B, int T, int D, int K,
+                            const float* s0, void* y, float* s_out, void* stream) {
+  if (int s = check_conv(dtype, act, B, T, D, K, ldx)) return s;
+  if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
+  const size_t e = size_of(dtype), state = static_cast<size_t>(B) * (K - 1) * D * 4;
+  const int64_t tokens = static_cast<int64_t>(B) * T;
+  if (!at_elements({w}, 4) || !at_elements({bias, s0, s_out}, 4, true) ||
+      !at_elements({lens}, 8, true))
+    return SANATAN_ERR_INVALID;
+  if (T > 0 && !at_elements({x, y}, e)) return SANATAN_ERR_INVALID;
+  if (clash({{y, span(tokens, D, D, e)}, {s_out, state}},
+            {{x, span(tokens, ldx, D, e)},
+             {w, static_cast<size_t>(D) * K * 4},
+             {bias, static_cast<size_t>(D) * 4},
+             {lens, static_cast<size_t>(B) * 8},
+             {s0, state}}))
+    return SANATAN_ERR_INVALID;
+  if (int s = check_arch()) return s;
+  ConvArgs a;
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.bias = bias;
+  a.dtype = dtype;
+  a.act = act;
+  a.lens = lens;
+  a.B = B;
+  a.T = T;
+  a.D = D;
+  a.K = K;
+  a.s0 = s0;
+  a.y = y;
+  a.s_out = K > 1 ? s_out : nullptr;
+  return from_cuda(causal_conv_fwd_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sanatan_causal_conv_bwd_workspace_size(int B, int T, int D, int K) {
+  return causal_conv_bwd_workspace_bytes(B, T, D, K);
+}
+
+int sanatan_causal_conv_bwd(const void* x, int64_t ldx, const float* w, const float* bias,
+                            const void* dy, int dtype, int act, const int64_t* lens, int B, int T,
+                            int D, int K, const float* s0, const float* ds_out, void* dx,
+                            float* dw, float* dbias, float* ds0, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (int s = check_conv(dtype, act, B, T, D, K, ldx)) return s;
+  if (D == 0) return SANATAN_OK;
+  const size_t e = size_of(dtype), state = static_cast<size_t>(B) * (K - 1) * D * 4;
+  const int64_t tokens = static_cast<int64_t>(B) * T;
+  if (!at_elements({w}, 4) || !at_elements({bias, s0, ds_out, dw, dbias, ds0, workspace}, 4, true) ||
+      !at_elements({lens}, 8, true))
+    return SANATAN_ERR_INVALID;
+  if (tokens > 0 && !at_elements({x, dy, dx}, e)) return SANATAN_ERR_INVALID;
+  const bool sums = dw != nullptr || dbias != nullptr;
+  const size_t need = sums ? causal_conv_bwd_workspace_bytes(B, T, D, K) : 0;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SANATAN_ERR_INVALID;
+  const size_t wide = static_cast<size_t>(D) * K * 4, row = static_cast<size_t>(D) * 4;
+  if (clash({{dx, span(tokens, D, D, e)}, {dw, wide}, {dbias, row}, {ds0, state},
+             {workspace, need}},
+            {{x, span(tokens, ldx, D, e)}, {w, wide}, {bias, row}, {dy, span(tokens, D, D, e)},
+             {lens, static_cast<size_t>(B) * 8}, {s0, state}, {ds_out, state}}))
+    return SANATAN_ERR_INVALID;
+  if (int s = check_arch()) return s;
+  ConvBwdArgs a;
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.bias = bias;
+  a.dy = dy;
+  a.dtype = dtype;
+  a.act = act;
+  a.lens = lens;
+  a.B = B;
+  a.T = T;
+  a.D = D;
+  a.K = K;
+  a.s0 = s0;
+  a.ds_out = ds_out;
+  a.dx = dx;
+  a.dw = dw;
+  a.dbias = dbias;
+  a.ds0 = ds0;
+  a.parts = static_cast<float*>(workspace);
+  return from_cuda(causal_conv_bwd_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+int sanatan_causal_conv_step(float* state, const void* x, int64_t ldx, const float* w,
+                             const float* bias, int dtype, int act, int N, int D, int K, void* y,
+                             void* stream) {
+  if (int s = check_conv(dtype, act, N, 1, D, K, ldx)) return s;
+  if (static_cast<int64_t>(N) * D == 0) return SANATAN_OK;
+  const size_t e = size_of(dtype);
+  if (!at_elements({x, y}, e) || !at_elements({w}, 4) || !at_elements({state}, 4, K == 1) ||
+      !at_elements({bias}, 4, true))
+    return SANATAN_ERR_INVALID;
+  if (clash({{y, span(N, D, D, e)}, {state, static_cast<size_t>(N) * (K - 1) * D * 4}},
+            {{x, span(N, ldx, D, e)}, {w, static_cast<size_t>(D) * K * 4},
+             {bias, static_cast<size_t>(D) * 4}}))
+    return SANATAN_ERR_INVALID;
+  if (int s = check_arch()) return s;
+  ConvArgs a;
+  a.x = x;
+  a.ldx = ldx;
+  a.w = w;
+  a.bias = bias;
+  a.dtype = dtype;
+  a.act = act;
+  a.B = N;
+  a.T = 1;
+  a.D = D;
+  a.K = K;
+  a.y = y;
+  a.s_out = state;
+  return from_cuda(causal_conv_step_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sanatan_selective_scan_marks_size(int B, int T, int D, int N) {
+  if (B < 0 || T < 0 || D < 0 || N < 0) return 0;
+  return static_cast<size_t>(B) *
+         ((static_cast<size_t>(T) + kSelectiveMark - 1) / kSelectiveMark) * D * N * sizeof(float);
+}
+
+size_t sanatan_selective_scan_fwd_workspace_size(int B, int T, int D, int N) {
+  return N > kSelectiveStates ? 0 : selective_scan_fwd_workspace_bytes(B, T, D, N);
+}
+
+int sanatan_selective_scan_fwd(const void* u, const void* dt, const void* z, int64_t ldz,
+                               const void* Bm, int64_t ldb, const void* Cm, int64_t ldc,
+                               const float* A, const float* skip, const float* dt_bias, int dtype,
+                               int softplus, const int64_t* lens, int B, int T, int D, int N,
+                               const float* h0, void* y, float* h_out, float* marks,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  SelectiveArgs a;
+  a.u = u;
+  a.dt = dt;
+  a.z = z;
+  a.Bm = Bm;
+  a.Cm = Cm;
+  a.ldz = ldz;
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.A = A;
+  a.skip = skip;
+  a.dt_bias = dt_bias;
+  a.dtype = dtype;
+  a.softplus = softplus != 0;
+  a.lens = lens;
+  a.B = B;
+  a.T = T;
+  a.D = D;
+  a.N = N;
+  a.h0 = h0;
+  a.y = y;
+  a.h_out = h_out;
+  a.marks = marks;
+  if (int s = check_selective(a)) return s;
+  if (static_cast<int64_t>(B) * D == 0) return SANATAN_OK;
+  const size_t e = size_of(dtype);
+  const int64_t tokens = static_cast<int64_t>(B) * T;
+  if (T > 0 && !at_elements({y}, e)) return SANATAN_ERR_INVALID;
+  if (T == 0 && h_out == nullptr) return SANATAN_OK;
+  const size_t need = selective_scan_fwd_workspace_bytes(B, T, D, N);
+  if (need > 0 && (workspace == nullptr || !at_element(workspace, 4) || workspace_bytes < need))
+    return SANATAN_ERR_INVALID;
+  const size_t state = static_cast<size_t>(B) * D * N * 4, row = static_cast<size_t>(D) * 4;
+  const size_t dense = span(tokens, D, D, e);
+  if (clash({{y, dense}, {h_out, state}, {marks, sanatan_selective_scan_marks_size(B, T, D, N)},
+             {workspace, need}},
+            {{h0, state}, {u, dense}, {dt, dense}, {z, span(tokens, ldz, D, e)},
+             {Bm, span(tokens, ldb, N, e)}, {Cm, span(tokens, ldc, N, e)},
+             {A, static_cast<size_t>(D) * N * 4}, {skip, row}, {dt_bias, row},
+             {lens, static_cast<size_t>(B) * 8}},
+            {{1, 0}}))
+    return SANATAN_ERR_INVALID;
+  if (int s = check_arch()) return s;
+  return from_cuda(selective_scan_fwd_launch(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sanatan_selective_scan_bwd_workspace_size(int B, int T, int D, int N) {
+  return N > kSelectiveStates ? 0 : selective_scan_bwd_workspace_bytes(B, T, D, N);
+}
+
+int sanatan_selective_scan_bwd(const void* u, const void* dt, const void* z, int64_t ldz,
+                               const void* Bm, int64_t ldb, const void* Cm, int64_t ldc,
+                               const float* A, const float* skip, const float* dt_bias, int dtype,
+                               int softplus, const int64_t* lens, int B, int T, int D, int N,
+                               const void* dy, const float* marks, const float* dh_out, void* du,
+                               void* ddt, void* dz, float* dA, void* dB, void* dC, float* dskip,
+                               float* ddt_bias, float* dh0, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  SelectiveBwdArgs args;
+  SelectiveArgs& a = args.f;
+  a.u = u;
+  a.dt = dt;
+  a.z = z;
+  a.Bm = Bm;
+  a.Cm = Cm;
+  a.ldz = ldz;
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.A = A;
+  a.skip = skip;
+  a.dt_bias = dt_bias;
+  a.dtype = dtype;
+  a.softplus = softplus != 0;
+  a.lens = lens;
+  a.B = B;
+  a.T = T;
+  a.D = D;
+  a.N = N;
+  if (int s = check_selective(a)) return s;
+  if (D == 0) return SANATAN_OK;
+  const size_t e = size_of(dtype);
+  const int64_t tokens = static_cast<int64_t>(B) * T;
+  if (!at_elements({dA}, 4) || !at_elements({dskip, ddt_bias, dh0, dh_out}, 4, true))
+    return SANATAN_ERR_INVALID;
+  if (tokens > 0 && (!at_elements({dy, du, ddt, dB, dC}, e) || !at_elements({dz}, e, z == nullptr) ||
+                !at_elements({marks}, 4)))
+    return SANATAN_ERR_INVALID;
+  if (z == nullptr && dz != nullptr) return SANATAN_ERR_INVALID;
+  const size_t need = selective_scan_bwd_workspace_bytes(B, T, D, N);
+  if (need > 0 && (workspace == nullptr || !at_element(workspace, 4) || workspace_bytes < need))
+    return SANATAN_ERR_INVALID;
+  const size_t state = static_cast<size_t>(B) * D * N * 4, row = static_cast<size_t>(D) * 4;
+  const size_t dense = span(tokens, D, D, e), pair = span(tokens, N, N, e);
+  const size_t matrix = static_cast<size_t>(D) * N * 4;
+  if (clash({{dh0, state}, {du, dense}, {ddt, dense}, {dz, dense}, {dA, matrix}, {dB, pair},
+             {dC, pair}, {dskip, row}, {ddt_bias, row}, {workspace, need}},
+            {{dh_out, state}, {u, dense}, {dt, dense}, {z, span(tokens, ldz, D, e)},
+             {Bm, span(tokens, ldb, N, e)}, {Cm, span(tokens, ldc, N, e)}, {A, matrix},
+             {skip, row}, {dt_bias, row}, {lens, static_cast<size_t>(B) * 8}, {dy, dense},
+             {marks, sanatan_selective_scan_marks_size(B, T, D, N)}},
+            {{0, 0}}))
+    return SANATAN_ERR_INVALID;
+  if (int s = check_arch()) return s;
+  args.dy = dy;
+  args.marks = marks;
+  args.dh_out = dh_out;
+  args.du = du;
+  args.ddt = ddt;
+  args.dz = dz;
+  args.dA = dA;
+  args.dB = dB;
+  args.dC = dC;
+  args.dskip = dskip;
+  args.ddt_bias = ddt_bias;
+  args.dh0 = dh0;
+  return from_cuda(selective_scan_bwd_launch(args, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int sanatan_selective_scan_step(float* h, const void* u, const void* dt, const void* z,
+                                int64_t ldz, const void* Bm, int64_t ldb, const void* Cm,
+                                int64_t ldc, const float* A, const float* skip,
+                                const float* dt_bias, int dtype, int softplus, int nseq, int D,
+                                int N, void* y, void* stream) {
+  SelectiveArgs a;
+  a.u = u;
+  a.dt = dt;
+  a.z = z;
+  a.Bm = Bm;
+  a.Cm = Cm;
+  a.ldz = ldz;
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.A = A;
+  a.skip = skip;
+  a.dt_bias = dt_bias;
+  a.dtype = dtype;
+  a.softplus = softplus != 0;
+  a.B = nseq;
+  a.T = 1;
+  a.D = D;
+  a.N = N;
+  a.y = y;
+  a.h_out = h;
+  if (int s = check_selective(a)) return s;
+  if (static_cast<int64_t>(nseq) * D == 0) return SANATAN_OK;
+  const size_t e = size_of(dtype), row = static_cast<size_t>(D) * 4, dense = span(nseq, D, D, e);
+  if (!at_elements({h}, 4) || !at_elements({y}, e)) return SANATAN_ERR_INVALID;
+  if (clash({{y, dense}, {h, static_cast<size_t>(nseq) * D * N * 4}},
+            {{u, dense}, {dt, dense}, {z, span(nseq, ldz, D, e)}, {Bm, span(nseq, ldb, N, e)},
+             {Cm, span(nseq, ldc, N, e)}, {A, row * N}, {skip, row}, {dt_bias, row}}))
+    return SANATAN_ERR_INVALID;
+  if (int s = check_arch()) return s;
+  return from_cuda(selective_scan_step_launch(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -267,4 +267,132 @@ struct CacheArgs {
 };
 int64_t state_cache_blocks(int64_t inner);
 cudaError_t state_cache_launch(CacheArgs a, bool write, cudaStream_t st);
+
+// Layer norm of rows of D values (layer_norm.cu).
+constexpr int kNormParts = 304;    // partial sums of dw and db: blocks of the backward at most
+struct NormArgs {
+  const void* x = nullptr;
+  const void* residual = nullptr;  // or null
+  const float* weight = nullptr;   // [D] or null (1)
+  const float* bias = nullptr;     // [D] or null (0)
+  int dtype = 0, D = 0;
+  int64_t rows = 0;
+  float eps = 0.f;
+  void* y = nullptr;
+  void* sum = nullptr;             // x + residual or null
+  float* stats = nullptr;          // [rows, 2] mean, 1 / sqrt(var + eps), or null
+};
+struct NormBwdArgs {
+  const void* s = nullptr;         // what was normalised
+  const float* weight = nullptr;
+  const void* dy = nullptr;
+  const void* ds = nullptr;        // or null
+  const float* stats = nullptr;
+  int dtype = 0, D = 0;
+  int64_t rows = 0;
+  void* dx = nullptr;
+  float* dweight = nullptr;        // [D] or null
+  float* dbias = nullptr;          // [D] or null
+  float* parts = nullptr;          // layer_norm_bwd_workspace_bytes
+};
+size_t layer_norm_bwd_workspace_bytes(int64_t rows, int D);
+cudaError_t layer_norm_fwd_launch(const NormArgs& a, cudaStream_t st);
+cudaError_t layer_norm_bwd_launch(const NormBwdArgs& a, cudaStream_t st);
+
+// Short causal convolution over [B, T, D] (causal_conv.cu).
+constexpr int kConvTaps = 8;    // K at most
+constexpr int kConvParts = 256; // partial sums of dw and dbias at most
+struct ConvArgs {
+  const void* x = nullptr;
+  int64_t ldx = 0;                 // values between two tokens of x
+  const float* w = nullptr;        // [D, K]
+  const float* bias = nullptr;     // [D] or null
+  int dtype = 0, act = 0;
+  const int64_t* lens = nullptr;   // [B] or null
+  int B = 0, T = 0, D = 0, K = 0;
+  const float* s0 = nullptr;       // [B, K - 1, D] or null
+  void* y = nullptr;
+  float* s_out = nullptr;          // [B, K - 1, D] or null (the step's state)
+  int runs = 0;                    // of a sequence (set by the launcher)
+};
+struct ConvBwdArgs {
+  const void* x = nullptr;
+  int64_t ldx = 0;
+  const float* w = nullptr;
+  const float* bias = nullptr;
+  const void* dy = nullptr;
+  int dtype = 0, act = 0;
+  const int64_t* lens = nullptr;
+  int B = 0, T = 0, D = 0, K = 0;
+  const float* s0 = nullptr;
+  const float* ds_out = nullptr;   // [B, K - 1, D] or null
+  void* dx = nullptr;
+  float* dw = nullptr;             // [D, K] or null
+  float* dbias = nullptr;          // [D] or null
+  float* ds0 = nullptr;            // [B, K - 1, D] or null
+  float* parts = nullptr;          // causal_conv_bwd_workspace_bytes
+  int runs = 0;
+};
+size_t causal_conv_bwd_workspace_bytes(int B, int T, int D, int K);
+cudaError_t causal_conv_fwd_launch(const ConvArgs& a, cudaStream_t st);
+cudaError_t causal_conv_bwd_launch(const ConvBwdArgs& a, cudaStream_t st);
+cudaError_t causal_conv_step_launch(const ConvArgs& a, cudaStream_t st);
+
+// Selective state space scan over [B, T, D] with N states a channel (selective_scan_fwd.cu,
+// selective_scan_bwd.cu).
+constexpr int kSelectiveMark = 16;      // tokens between two marks (saved states)
+constexpr int kSelectiveStates = 128;   // N at most
+constexpr int kSelectiveFwdBlocks = 4;  // blocks of an SM that the splits aim at
+constexpr int kSelectiveBwdBlocks = 3;
+struct SelectiveArgs {
+  const void* u = nullptr;
+  const void* dt = nullptr;
+  const void* z = nullptr;          // or null
+  const void* Bm = nullptr;
+  const void* Cm = nullptr;
+  int64_t ldz = 0, ldb = 0, ldc = 0;  // values between two tokens
+  const float* A = nullptr;         // [D, N]
+  const float* skip = nullptr;      // [D] or null
+  const float* dt_bias = nullptr;   // [D] or null
+  int dtype = 0, softplus = 0;
+  const int64_t* lens = nullptr;    // [B] or null
+  int B = 0, T = 0, D = 0, N = 0;
+  const float* h0 = nullptr;        // [B, D, N] or null
+  void* y = nullptr;
+  float* h_out = nullptr;           // [B, D, N] or null (the step's state)
+  float* marks = nullptr;           // [B, ceil(T / 16), D, N] or null
+  // set by the launchers
+  bool vec = false;                 // states are read and written four at a time
+  int blocks = 0, segments = 1, tiles_per_segment = 0;  // of channels; of tokens
+  float* carry = nullptr;           // [B, segments, D, N]
+  float* sums = nullptr;            // [B, segments, D]
+};
+int selective_lanes(int N);
+int selective_blocks(int D, int N);
+int selective_segments(int B, int T, int D, int N, int per_sm, int* tiles_per_segment);
+size_t selective_scan_fwd_workspace_bytes(int B, int T, int D, int N);
+cudaError_t selective_scan_fwd_launch(SelectiveArgs a, void* workspace, cudaStream_t st);
+cudaError_t selective_scan_step_launch(SelectiveArgs a, cudaStream_t st);
+
+struct SelectiveBwdArgs {
+  SelectiveArgs f;                  // inputs, sizes and plan (y, h0, h_out, f.marks: unused)
+  const void* dy = nullptr;
+  const float* marks = nullptr;
+  const float* dh_out = nullptr;    // [B, D, N] or null
+  void* du = nullptr;
+  void* ddt = nullptr;
+  void* dz = nullptr;               // where there is a z
+  float* dA = nullptr;
+  void* dB = nullptr;
+  void* dC = nullptr;
+  float* dskip = nullptr;           // [D] or null
+  float* ddt_bias = nullptr;        // [D] or null
+  float* dh0 = nullptr;             // [B, D, N] or null
+  // parts in the workspace (set by the launcher)
+  float* pairs = nullptr;           // [blocks of channels, B, T, 2, N]: dB, dC
+  float* params = nullptr;          // [B, segments, D, N]: dA
+  float* channels = nullptr;        // [B, segments, 2, D]: dskip, ddt_bias
+};
+size_t selective_scan_bwd_workspace_bytes(int B, int T, int D, int N);
+cudaError_t selective_scan_bwd_launch(SelectiveBwdArgs a, void* workspace, cudaStream_t st);
 }  // namespace sanatan

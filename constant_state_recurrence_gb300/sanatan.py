@@ -93,6 +93,33 @@ _SIGS = {
                                            _c_i64, _c_int, _c_p, _c_p, _c_p, _c_p]),
     "sanatan_state_cache_read": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_int, _c_p, _c_int, _c_int,
                                           _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+    "sanatan_layer_norm_fwd": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_int, _c_i64, _c_int, _c_f,
+                                        _c_p, _c_p, _c_p, _c_p]),
+    "sanatan_layer_norm_bwd_workspace_size": (_c_sz, [_c_i64, _c_int]),
+    "sanatan_layer_norm_bwd": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_i64, _c_int,
+                                        _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "sanatan_causal_conv_fwd": (_c_int, [_c_p, _c_i64, _c_p, _c_p, _c_int, _c_int, _c_p, _c_int,
+                                         _c_int, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p]),
+    "sanatan_causal_conv_bwd_workspace_size": (_c_sz, [_c_int] * 4),
+    "sanatan_causal_conv_bwd": (_c_int, [_c_p, _c_i64, _c_p, _c_p, _c_p, _c_int, _c_int, _c_p,
+                                         _c_int, _c_int, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p,
+                                         _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "sanatan_causal_conv_step": (_c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_int, _c_int, _c_int,
+                                          _c_int, _c_int, _c_p, _c_p]),
+    "sanatan_selective_scan_marks_size": (_c_sz, [_c_int] * 4),
+    "sanatan_selective_scan_fwd_workspace_size": (_c_sz, [_c_int] * 4),
+    "sanatan_selective_scan_fwd": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64,
+                                            _c_p, _c_p, _c_p, _c_int, _c_int, _c_p, _c_int,
+                                            _c_int, _c_int, _c_int, _c_p, _c_p, _c_p, _c_p, _c_p,
+                                            _c_sz, _c_p]),
+    "sanatan_selective_scan_bwd_workspace_size": (_c_sz, [_c_int] * 4),
+    "sanatan_selective_scan_bwd": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64,
+                                            _c_p, _c_p, _c_p, _c_int, _c_int, _c_p, _c_int,
+                                            _c_int, _c_int, _c_int] + [_c_p] * 13
+                                   + [_c_sz, _c_p]),
+    "sanatan_selective_scan_step": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_p,
+                                             _c_i64, _c_p, _c_p, _c_p, _c_int, _c_int, _c_int,
+                                             _c_int, _c_int, _c_p, _c_p]),
 }
 
 _lib = None
@@ -956,6 +983,384 @@ def sanatan_state_cache_read(codes, scales, pages, state, z_cache=None, z=None, 
     _call("sanatan_state_cache_read", state.device, codes.data_ptr(), scales.data_ptr(),
           _at(z_cache), P, fmt, pages.data_ptr(), layers, B, inner, zi, state.data_ptr(), _at(z))
     return state
+
+
+ACTIVATIONS = {None: 0, "silu": 1}
+CONV_TAPS = 8           # taps of the short convolution at most
+SELECTIVE_MARK = 16     # tokens between two saved states of the selective scan
+SELECTIVE_STATES = 128  # states of a channel at most
+
+
+def _rows(t, name, dtype, shape, dev):
+    """Values between two rows of t, whose rows are those of a dense tensor or of a
+    wider one (a half of a projection): t[..., k] one behind the other, rows ld apart."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == dev \
+            and t.is_contiguous():
+        return shape[-1]
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} "
+                         f"{tuple(shape)} on {dev}")
+    if t.is_contiguous():
+        return shape[-1]
+    ld = None
+    if shape[-1] == 1 or t.stride(-1) == 1:
+        ld, rows = shape[-1], 1         # (of a tensor of one row)
+        for i in range(len(shape) - 2, -1, -1):
+            if shape[i] > 1:
+                if rows == 1:
+                    ld = t.stride(i)
+                elif t.stride(i) != rows * ld:
+                    ld = -1
+                    break
+                rows *= shape[i]
+    if ld is None or ld < shape[-1]:
+        raise ValueError(f"{name} has strides {t.stride()}: its rows must be dense and evenly "
+                         "spaced")
+    return ld
+
+
+def _opt(t, name, dtype, shape, dev):
+    """The address of an optional dense tensor."""
+    if t is None:
+        return None
+    return _fit(t, name, dtype, shape, dev).data_ptr()
+
+
+def _scratch(size, workspace, dev):
+    """(the caller's workspace or one of this call, its address, its bytes)"""
+    if workspace is not None:
+        _need(workspace, "workspace")
+        if workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if size == 0:
+        return None, None, 0
+    workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    return workspace, workspace.data_ptr(), size
+
+
+def _input(x, name, dims=None):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype not in _FLOATS:
+        raise ValueError(f"{name} has dtype {x.dtype}, expected one of {_FLOATS}")
+    if x.dim() != dims if dims else x.dim() < 1:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {dims or 'some'} dimensions")
+    return x.shape, x.device, x.dtype
+
+
+def layer_norm_bwd_workspace_size(rows, D):
+    return int(lib().sanatan_layer_norm_bwd_workspace_size(rows, D))
+
+
+def sanatan_layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, want_stats=False,
+                           out=None, sum_out=None):
+    """Layer norm over the last dimension of x [..., D] (f32 or bf16), of s = x +
+    residual where there is a residual (rounded to x's type, as it is stored);
+    weight, bias [D] f32.  sum_out may be the residual (the stream in place).
+
+    Returns (y, s or None without a residual, stats [rows, 2] f32 for the backward
+    or None)."""
+    shape, dev, dt = _input(x, "x")
+    _fit(x, "x", dt, shape, dev)
+    D = shape[-1]
+    rows = x.numel() // D if D else 0
+    y = torch.empty_like(x) if out is None else _fit(out, "out", dt, shape, dev)
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out without a residual")
+        s = None
+    else:
+        _fit(residual, "residual", dt, shape, dev)
+        s = torch.empty_like(x) if sum_out is None else _fit(sum_out, "sum_out", dt, shape, dev)
+    stats = torch.empty(rows, 2, dtype=torch.float32, device=dev) if want_stats else None
+    _call("sanatan_layer_norm_fwd", dev, x.data_ptr(), _at(residual),
+          _opt(weight, "weight", torch.float32, (D,), dev),
+          _opt(bias, "bias", torch.float32, (D,), dev), _DT[dt], rows, D, float(eps),
+          y.data_ptr(), _at(s), _at(stats))
+    return y, s, stats
+
+
+def sanatan_layer_norm_bwd(s, weight, dy, stats, ds=None, want_dweight=True, want_dbias=True,
+                           workspace=None):
+    """Gradients of sum(y * dy) + sum(s * ds) for sanatan_layer_norm_fwd: dict(dx,
+    dweight, dbias); s is what was normalised (the sum, or x without a residual),
+    dx the gradient of x and of the residual alike."""
+    shape, dev, dt = _input(s, "s")
+    _fit(s, "s", dt, shape, dev)
+    D = shape[-1]
+    rows = s.numel() // D if D else 0
+    _fit(dy, "dy", dt, shape, dev)
+    _fit(stats, "stats", torch.float32, (rows, 2), dev)
+    dx = torch.empty_like(s)
+    dw = torch.empty(D, dtype=torch.float32, device=dev) if want_dweight else None
+    db = torch.empty(D, dtype=torch.float32, device=dev) if want_dbias else None
+    size = layer_norm_bwd_workspace_size(rows, D) if want_dweight or want_dbias else 0
+    _hold, ws, ws_bytes = _scratch(size, workspace, dev)
+    _call("sanatan_layer_norm_bwd", dev, s.data_ptr(),
+          _opt(weight, "weight", torch.float32, (D,), dev), dy.data_ptr(),
+          _opt(ds, "ds", dt, shape, dev), stats.data_ptr(), _DT[dt], rows, D, dx.data_ptr(),
+          _at(dw), _at(db), ws, ws_bytes)
+    return dict(dx=dx, dweight=dw, dbias=db)
+
+
+class LayerNorm(torch.autograd.Function):
+    """autograd wrapper: y = LayerNorm.apply(x, weight, bias), or (y, s) =
+    LayerNorm.apply(x, weight, bias, residual, eps) with s = x + residual."""
+
+    @staticmethod
+    def forward(ctx, x, weight=None, bias=None, residual=None, eps=1e-5):
+        y, s, stats = sanatan_layer_norm_fwd(x, weight, bias, residual, eps,
+                                             want_stats=any(ctx.needs_input_grad))
+        ctx.save_for_backward(x if s is None else s, weight, stats)
+        ctx.set_materialize_grads(False)
+        return y if s is None else (y, s)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, ds=None):
+        s, weight, stats = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dy is None and ds is None:
+            return None, None, None, None, None
+        dy = torch.zeros_like(s) if dy is None else dy.contiguous()
+        d = sanatan_layer_norm_bwd(s, weight, dy, stats, None if ds is None else ds.contiguous(),
+                                   want_dweight=need[1], want_dbias=need[2])
+        return (d["dx"] if need[0] else None, d["dweight"], d["dbias"],
+                d["dx"] if need[3] else None, None)
+
+
+def _act(activation):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}, not {activation!r}")
+    return ACTIVATIONS[activation]
+
+
+def _conv_args(x, w, bias, activation, dims):
+    """(shape, device, dtype, ld of x, K, w's and bias's addresses, activation)"""
+    shape, dev, dt = _input(x, "x", dims)
+    _need(w, "w", (torch.float32,))
+    if w.dim() != 2 or not 1 <= w.shape[1] <= CONV_TAPS:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected [D, 1 .. {CONV_TAPS}]")
+    K = w.shape[1]
+    ld = _rows(x, "x", dt, shape, dev)
+    wp = _fit(w, "w", torch.float32, (shape[-1], K), dev).data_ptr()
+    return shape, dev, dt, ld, K, wp, _opt(bias, "bias", torch.float32, (shape[-1],), dev), \
+        _act(activation)
+
+
+def causal_conv_bwd_workspace_size(B, T, D, K):
+    return int(lib().sanatan_causal_conv_bwd_workspace_size(B, T, D, K))
+
+
+def sanatan_causal_conv_fwd(x, w, bias=None, activation="silu", s0=None, lens=None,
+                            want_state=False, out=None, s_out=None):
+    """Short causal convolution of x [B, T, D] (f32 or bf16; may be a half of a wider
+    projection) with w [D, K] f32: c_t = bias + sum_k w_k x_{t-K+1+k}, y = c (activation
+    None) or c / (1 + exp(-c)) ("silu").  s0 [B, K-1, D] f32 are the inputs before the
+    first token (None: zeros); tokens from lens[b] (int64 [B]) on are left out.
+
+    Returns (y [B, T, D], the last K-1 inputs [B, K-1, D] f32 or None)."""
+    (B, T, D), dev, dt, ld, K, wp, bp, act = _conv_args(x, w, bias, activation, 3)
+    y = torch.empty((B, T, D), dtype=dt, device=dev) if out is None else \
+        _fit(out, "out", dt, (B, T, D), dev)
+    sp = _opt(s0, "s0", torch.float32, (B, K - 1, D), dev)
+    if s_out is not None:
+        _fit(s_out, "s_out", torch.float32, (B, K - 1, D), dev)
+    elif want_state:
+        s_out = torch.empty(B, K - 1, D, dtype=torch.float32, device=dev)
+    _call("sanatan_causal_conv_fwd", dev, x.data_ptr(), ld, wp, bp, _DT[dt], act,
+          _opt(lens, "lens", torch.int64, (B,), dev), B, T, D, K, sp, y.data_ptr(), _at(s_out))
+    return y, s_out
+
+
+def sanatan_causal_conv_bwd(x, w, dy, bias=None, activation="silu", s0=None, lens=None,
+                            ds_last=None, want_dw=True, want_dbias=True, want_ds0=False,
+                            workspace=None):
+    """Gradients of sum(y * dy) + sum(s_last * ds_last) for sanatan_causal_conv_fwd:
+    dict(dx, dw, dbias, ds0)."""
+    (B, T, D), dev, dt, ld, K, wp, bp, act = _conv_args(x, w, bias, activation, 3)
+    _fit(dy, "dy", dt, (B, T, D), dev)
+    dx = torch.empty((B, T, D), dtype=dt, device=dev)
+    dw = torch.empty(D, K, dtype=torch.float32, device=dev) if want_dw else None
+    db = torch.empty(D, dtype=torch.float32, device=dev) if want_dbias else None
+    ds0 = torch.empty(B, K - 1, D, dtype=torch.float32, device=dev) if want_ds0 else None
+    size = causal_conv_bwd_workspace_size(B, T, D, K) if want_dw or want_dbias else 0
+    _hold, ws, ws_bytes = _scratch(size, workspace, dev)
+    _call("sanatan_causal_conv_bwd", dev, x.data_ptr(), ld, wp, bp, dy.data_ptr(), _DT[dt], act,
+          _opt(lens, "lens", torch.int64, (B,), dev), B, T, D, K,
+          _opt(s0, "s0", torch.float32, (B, K - 1, D), dev),
+          _opt(ds_last, "ds_last", torch.float32, (B, K - 1, D), dev), dx.data_ptr(), _at(dw),
+          _at(db), _at(ds0), ws, ws_bytes)
+    return dict(dx=dx, dw=dw, dbias=db, ds0=ds0)
+
+
+def sanatan_causal_conv_step(state, x, w, bias=None, activation="silu", out=None):
+    """One token of the short convolution for N sequences: state [N, K-1, D] f32 (the
+    inputs before, oldest first) is updated in place, x [N, D].  Returns y [N, D]."""
+    (N, D), dev, dt, ld, K, wp, bp, act = _conv_args(x, w, bias, activation, 2)
+    _fit(state, "state", torch.float32, (N, K - 1, D), dev)
+    y = torch.empty((N, D), dtype=dt, device=dev) if out is None else \
+        _fit(out, "out", dt, (N, D), dev)
+    _call("sanatan_causal_conv_step", dev, state.data_ptr(), x.data_ptr(), ld, wp, bp, _DT[dt],
+          act, N, D, K, y.data_ptr())
+    return y
+
+
+class CausalConv(torch.autograd.Function):
+    """autograd wrapper: (y, s_last) = CausalConv.apply(x, w, bias, activation, s0,
+    lens); forward = sanatan_causal_conv_fwd, backward = sanatan_causal_conv_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias=None, activation="silu", s0=None, lens=None):
+        y, s = sanatan_causal_conv_fwd(x, w, bias, activation, s0=s0, lens=lens, want_state=True)
+        ctx.save_for_backward(x, w, bias, s0, lens)
+        ctx.activation = activation
+        ctx.set_materialize_grads(False)
+        return y, s
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, ds_last):
+        x, w, bias, s0, lens = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dy is None and ds_last is None:
+            return None, None, None, None, None, None
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None \
+            else dy.contiguous()
+        d = sanatan_causal_conv_bwd(x, w, dy, bias, ctx.activation, s0=s0, lens=lens,
+                                    ds_last=None if ds_last is None else ds_last.contiguous(),
+                                    want_dw=need[1], want_dbias=need[2], want_ds0=need[4])
+        return d["dx"], d["dw"], d["dbias"], None, d["ds0"], None
+
+
+def selective_scan_fwd_workspace_size(B, T, D, N):
+    return int(lib().sanatan_selective_scan_fwd_workspace_size(B, T, D, N))
+
+
+def selective_scan_bwd_workspace_size(B, T, D, N):
+    return int(lib().sanatan_selective_scan_bwd_workspace_size(B, T, D, N))
+
+
+def _selective_args(u, dt, A, B, C, D, z, dt_bias, softplus, dims):
+    """(u's shape, device, dtype, N, the arguments that the three calls share)"""
+    shape, dev, ty = _input(u, "u", dims)
+    _need(A, "A", (torch.float32,))
+    if A.dim() != 2 or not 1 <= A.shape[1] <= SELECTIVE_STATES:
+        raise ValueError(f"A has shape {tuple(A.shape)}, expected [D, 1 .. {SELECTIVE_STATES}]")
+    N, width = A.shape[1], shape[-1]
+    pair = (*shape[:-1], N)
+    _fit(u, "u", ty, shape, dev)
+    _fit(dt, "dt", ty, shape, dev)
+    ldz = 0 if z is None else _rows(z, "z", ty, shape, dev)
+    ldb, ldc = _rows(B, "B", ty, pair, dev), _rows(C, "C", ty, pair, dev)
+    return shape, dev, ty, N, (
+        u.data_ptr(), dt.data_ptr(), _at(z), ldz, B.data_ptr(), ldb, C.data_ptr(), ldc,
+        _fit(A, "A", torch.float32, (width, N), dev).data_ptr(),
+        _opt(D, "D", torch.float32, (width,), dev),
+        _opt(dt_bias, "dt_bias", torch.float32, (width,), dev), _DT[ty], int(bool(softplus)))
+
+
+def sanatan_selective_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True,
+                               h0=None, lens=None, want_state=False, want_marks=False, out=None,
+                               h_out=None, workspace=None):
+    """Selective scan of u, dt [B, T, D] (f32 or bf16) with A [D, N] f32 and B, C
+    [B, T, N]: delta = log(1 + exp(dt + dt_bias)) (softplus False: dt + dt_bias), h_t =
+    exp(delta A) h_{t-1} + delta u B_t, y_t = sum_n C_t h_t + D u, with z [B, T, D]
+    times z / (1 + exp(-z)).  B, C and z may be parts of wider projections; D (the
+    skip) and dt_bias are [D] f32 or None.  h0 [B, D, N] f32 is the state before the
+    first token; tokens from lens[b] (int64 [B]) on are left out and give zeros.
+
+    Returns (y [B, T, D], the last state [B, D, N] f32 or None, marks [B, ceil(T/16),
+    D, N] f32 (states for the backward) or None)."""
+    shape, dev, ty, N, args = _selective_args(u, dt, A, B, C, D, z, dt_bias, softplus, 3)
+    b, T, width = shape
+    y = torch.empty_like(u) if out is None else _fit(out, "out", ty, shape, dev)
+    hp = _opt(h0, "h0", torch.float32, (b, width, N), dev)
+    if h_out is not None:
+        _fit(h_out, "h_out", torch.float32, (b, width, N), dev)
+    elif want_state:
+        h_out = torch.empty(b, width, N, dtype=torch.float32, device=dev)
+    marks = torch.empty(b, -(-T // SELECTIVE_MARK), width, N, dtype=torch.float32, device=dev) \
+        if want_marks else None
+    _hold, ws, ws_bytes = _scratch(
+        lib().sanatan_selective_scan_fwd_workspace_size(b, T, width, N), workspace, dev)
+    _call("sanatan_selective_scan_fwd", dev, *args, _opt(lens, "lens", torch.int64, (b,), dev), b,
+          T, width, N, hp, y.data_ptr(), _at(h_out), _at(marks), ws, ws_bytes)
+    return y, h_out, marks
+
+
+def sanatan_selective_scan_bwd(u, dt, A, B, C, dy, marks, D=None, z=None, dt_bias=None,
+                               softplus=True, lens=None, dh_last=None, want_dh0=False,
+                               workspace=None):
+    """Gradients of sum(y * dy) + sum(h_last * dh_last) for sanatan_selective_scan_fwd:
+    dict(du, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0); marks are the forward's."""
+    shape, dev, ty, N, args = _selective_args(u, dt, A, B, C, D, z, dt_bias, softplus, 3)
+    b, T, width = shape
+    f32 = dict(dtype=torch.float32, device=dev)
+    _fit(dy, "dy", ty, shape, dev)
+    _fit(marks, "marks", torch.float32, (b, -(-T // SELECTIVE_MARK), width, N), dev)
+    du, ddt = torch.empty_like(u), torch.empty_like(u)
+    dz = None if z is None else torch.empty_like(u)
+    dA, dB, dC = torch.empty(width, N, **f32), *(
+        torch.empty(b, T, N, dtype=ty, device=dev) for _ in range(2))
+    dD = None if D is None else torch.empty(width, **f32)
+    dbias = None if dt_bias is None else torch.empty(width, **f32)
+    dh0 = torch.empty(b, width, N, **f32) if want_dh0 else None
+    _hold, ws, ws_bytes = _scratch(
+        lib().sanatan_selective_scan_bwd_workspace_size(b, T, width, N), workspace, dev)
+    _call("sanatan_selective_scan_bwd", dev, *args, _opt(lens, "lens", torch.int64, (b,), dev), b,
+          T, width, N, dy.data_ptr(), marks.data_ptr(),
+          _opt(dh_last, "dh_last", torch.float32, (b, width, N), dev), du.data_ptr(),
+          ddt.data_ptr(), _at(dz), dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _at(dD),
+          _at(dbias), _at(dh0), ws, ws_bytes)
+    return dict(du=du, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=dD, dz=dz, ddt_bias=dbias, dh0=dh0)
+
+
+def sanatan_selective_scan_step(h, u, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True,
+                                out=None):
+    """One token of the selective scan for N sequences: h [N, D, states] f32 is updated
+    in place; u, dt, z [N, D], B, C [N, states] (f32 or bf16).  Returns y [N, D]."""
+    shape, dev, ty, N, args = _selective_args(u, dt, A, B, C, D, z, dt_bias, softplus, 2)
+    b, width = shape
+    _fit(h, "h", torch.float32, (b, width, N), dev)
+    y = torch.empty_like(u) if out is None else _fit(out, "out", ty, shape, dev)
+    _call("sanatan_selective_scan_step", dev, h.data_ptr(), *args, b, width, N, y.data_ptr())
+    return y
+
+
+class SelectiveScan(torch.autograd.Function):
+    """autograd wrapper: (y, h_last) = SelectiveScan.apply(u, dt, A, B, C, D, z, dt_bias,
+    softplus, h0, lens); forward = sanatan_selective_scan_fwd, backward =
+    sanatan_selective_scan_bwd."""
+
+    @staticmethod
+    def forward(ctx, u, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, h0=None,
+                lens=None):
+        y, h, marks = sanatan_selective_scan_fwd(u, dt, A, B, C, D, z, dt_bias, softplus, h0=h0,
+                                                 lens=lens, want_state=True,
+                                                 want_marks=any(ctx.needs_input_grad))
+        ctx.save_for_backward(u, dt, A, B, C, D, z, dt_bias, lens, marks)
+        ctx.softplus = softplus
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh_last):
+        u, dt, A, B, C, D, z, dt_bias, lens, marks = ctx.saved_tensors
+        if dy is None and dh_last is None:
+            return (None,) * 11
+        dy = torch.zeros_like(u) if dy is None else dy.contiguous()
+        d = sanatan_selective_scan_bwd(u, dt, A, B, C, dy, marks, D, z, dt_bias, ctx.softplus,
+                                       lens=lens, want_dh0=ctx.needs_input_grad[9],
+                                       dh_last=None if dh_last is None else dh_last.contiguous())
+        return (d["du"], d["ddt"], d["dA"], d["dB"], d["dC"], d["dD"], d["dz"], d["ddt_bias"],
+                None, d["dh0"], None)
 
 
 class SanatanAttention(torch.autograd.Function):

@@ -71,6 +71,9 @@ enum sanatan_gate { SANATAN_GATE_LOG = 0, SANATAN_GATE_SIGMOID = 1 };
 /* Code formats of the state cache (sanatan_state_cache_write). */
 enum sanatan_cache_format { SANATAN_CACHE_INT8 = 0, SANATAN_CACHE_E4M3 = 1 };
 
+/* Activations behind the short causal convolution (sanatan_causal_conv_fwd). */
+enum sanatan_activation { SANATAN_ACT_NONE = 0, SANATAN_ACT_SILU = 1 };
+
 /* Human-readable text of a status code (static storage, never NULL). */
 SANATAN_API const char* sanatan_status_string(int status);
 
@@ -541,6 +544,133 @@ SANATAN_API int sanatan_state_cache_read(const void* codes, const float* scales,
                                          const int64_t* pages, int layers, int B, int64_t inner,
                                          int64_t exact_inner, float* state, float* exact,
                                          void* stream);
+
+/*
+ * Layers of a selective state space, next to the attention and the gated recurrence:
+ * the norm in front of a mixer, the short convolution and the selective scan, a third
+ * constant-state mixer whose state [D, N] forgets and takes in as the token says.  (The
+ * notes compare the method with state space layers; the pages give no formulas for
+ * them, these are the plain ones.)  Shared by the calls of this group:
+ *   - Tensors may start at any element of their type (parts of larger ones); where all
+ *     start at 16 bytes and rows are multiples of that, loads are wide.
+ *   - ld...: values between two tokens of an input that is part of a wider one (a half of
+ *     a projection): token t of sequence b starts at (b * T + t) * ld.  At least the
+ *     row's own values.  Every other tensor is dense.
+ *   - Outputs are written whole.  They share no bytes with inputs, each other or the
+ *     workspace (SANATAN_ERR_INVALID), but for the pairs named below.
+ *   - All sums are float32, in a fixed order: the same call gives the same bits.
+ *   - lens [B] int64 or NULL as for the gated recurrence: tokens from lens[b] on have no
+ *     effect and are not read; their outputs and gradients are zeros, the state passes
+ *     them unchanged.
+ *   - SANATAN_ERR_INVALID for an unknown dtype or activation, a negative size, a null (where
+ *     not allowed) or misaligned pointer, a workspace smaller than its size;
+ *     SANATAN_ERR_UNSUPPORTED for sizes whose thread blocks or offsets leave the grid: B * D
+ *     or rows of 2^31 or more, T or D above 2^30, and beyond 2^60 values.
+ *
+ * sanatan_layer_norm_fwd -- rows of D values:
+ *     s = x + residual, rounded to dtype (no residual: s = x),
+ *     y = (s - mean) / sqrt(var + eps) * weight + bias,  var = sum((s - mean)^2) / D.
+ *   x, residual (or NULL), y [rows, D] dtype;  weight, bias [D] f32 or NULL (1 and 0)
+ *   sum     [rows, D] dtype or NULL: s.  May be residual (the stream updated in place).
+ *   stats   [rows, 2] f32 or NULL: mean and 1 / sqrt(var + eps), for the backward.
+ * sanatan_layer_norm_bwd -- gradients of sum(y * dy) + sum(s * ds):
+ *   s [rows, D] what was normalised (sum, or x without a residual), stats as the forward
+ *   wrote them; dy, ds (or NULL) [rows, D] dtype; dx [rows, D] dtype: the gradient of x
+ *   and of the residual alike; dweight, dbias [D] f32 or NULL.
+ *   workspace: sanatan_layer_norm_bwd_workspace_size(rows, D) bytes (may be NULL where
+ *   neither dweight nor dbias is asked for).
+ */
+SANATAN_API int sanatan_layer_norm_fwd(const void* x, const void* residual, const float* weight,
+                                       const float* bias, int dtype, int64_t rows, int D,
+                                       float eps, void* y, void* sum, float* stats, void* stream);
+SANATAN_API size_t sanatan_layer_norm_bwd_workspace_size(int64_t rows, int D);
+SANATAN_API int sanatan_layer_norm_bwd(const void* s, const float* weight, const void* dy,
+                                       const void* ds, const float* stats, int dtype,
+                                       int64_t rows, int D, void* dx, float* dweight,
+                                       float* dbias, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/*
+ * sanatan_causal_conv_fwd -- per channel of [B, T, D], K taps:
+ *     c_t = bias + sum_{k < K} w[d, k] x_{t-K+1+k},   y = c or (SANATAN_ACT_SILU) c / (1 + exp(-c)).
+ *   x       [B, T, D] dtype, ldx;   y [B, T, D] dtype
+ *   w       [D, K] f32, K in 1 .. 8 (SANATAN_ERR_UNSUPPORTED above);  bias [D] f32 or NULL
+ *   s0      [B, K - 1, D] f32 or NULL (zeros): the inputs before the first token, oldest
+ *           first;  s_out [B, K - 1, D] f32 or NULL: those before the next token.
+ *   The state is float32 whatever the dtype, so that the state cache keeps it.
+ * sanatan_causal_conv_bwd -- gradients of sum(y * dy) + sum(s_out * ds_out): dx [B, T, D]
+ *   dtype; dw [D, K], dbias [D] f32 or NULL; ds0 [B, K - 1, D] f32 or NULL.
+ *   workspace: sanatan_causal_conv_bwd_workspace_size(...) bytes (may be NULL where
+ *   neither dw nor dbias is asked for).
+ * sanatan_causal_conv_step -- one token of N sequences: state [N, K - 1, D] f32 is updated
+ *   in place; x [N, D] (ldx between two sequences), y [N, D] dtype.
+ */
+SANATAN_API int sanatan_causal_conv_fwd(const void* x, int64_t ldx, const float* w,
+                                        const float* bias, int dtype, int act,
+                                        const int64_t* lens, int B, int T, int D, int K,
+                                        const float* s0, void* y, float* s_out, void* stream);
+SANATAN_API size_t sanatan_causal_conv_bwd_workspace_size(int B, int T, int D, int K);
+SANATAN_API int sanatan_causal_conv_bwd(const void* x, int64_t ldx, const float* w,
+                                        const float* bias, const void* dy, int dtype, int act,
+                                        const int64_t* lens, int B, int T, int D, int K,
+                                        const float* s0, const float* ds_out, void* dx, float* dw,
+                                        float* dbias, float* ds0, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+SANATAN_API int sanatan_causal_conv_step(float* state, const void* x, int64_t ldx, const float* w,
+                                         const float* bias, int dtype, int act, int N, int D,
+                                         int K, void* y, void* stream);
+
+/*
+ * sanatan_selective_scan_fwd -- per channel d of [B, T, D] with N states h [B, D, N] f32:
+ *     delta = dt + dt_bias, or (softplus != 0) log(1 + exp(dt + dt_bias)),
+ *     h_t[n] = exp(delta A[d, n]) h_{t-1}[n] + delta u B_t[n],
+ *     y_t = (sum_n C_t[n] h_t[n] + skip[d] u) * g,  g = 1 or (with z) z / (1 + exp(-z)).
+ *   u, dt, y [B, T, D] dtype;  z [B, T, D] dtype, ldz, or NULL
+ *   Bm, Cm   [B, T, N] dtype, ldb, ldc;  N in 1 .. 128 (SANATAN_ERR_UNSUPPORTED above)
+ *   A        [D, N] f32 (negative: the state decays);  skip, dt_bias [D] f32 or NULL (0)
+ *   h0       [B, D, N] f32 or NULL (zero);  h_out [B, D, N] f32 or NULL, may be h0
+ *   marks    sanatan_selective_scan_marks_size(...) bytes or NULL: f32 [B, ceil(T / 16), D,
+ *            N], the states before tokens 0, 16, 32, ... of every sequence (those behind
+ *            its last token are not written)
+ *   workspace: sanatan_selective_scan_fwd_workspace_size(...) bytes (NULL if 0).
+ *   Decays delta A below -126 ln 2 count as 0.  T = 0 copies h0 (or zeros) to h_out.
+ * sanatan_selective_scan_bwd -- gradients of sum(y * dy) + sum(h_out * dh_out), with the
+ *   marks that the forward wrote for the same inputs (h0 is among them): du, ddt [B, T, D]
+ *   dtype, dz [B, T, D] dtype (NULL exactly where z is), dA [D, N] f32, dB, dC [B, T, N]
+ *   dtype, dskip, ddt_bias [D] f32 or NULL, dh0 [B, D, N] f32 or NULL, may be dh_out
+ *   ([B, D, N] f32 or NULL).
+ *   workspace: sanatan_selective_scan_bwd_workspace_size(...) bytes: dB's and dC's parts,
+ *   8 N bytes for each token and block of channels (32 channels at N = 16).
+ * sanatan_selective_scan_step -- one token of nseq sequences: h [nseq, D, N] f32 is updated
+ *   in place; u, dt, z, y [nseq, D], Bm, Cm [nseq, N] dtype (ld: between two sequences).
+ */
+SANATAN_API size_t sanatan_selective_scan_marks_size(int B, int T, int D, int N);
+SANATAN_API size_t sanatan_selective_scan_fwd_workspace_size(int B, int T, int D, int N);
+SANATAN_API int sanatan_selective_scan_fwd(const void* u, const void* dt, const void* z,
+                                           int64_t ldz, const void* Bm, int64_t ldb,
+                                           const void* Cm, int64_t ldc, const float* A,
+                                           const float* skip, const float* dt_bias, int dtype,
+                                           int softplus, const int64_t* lens, int B, int T, int D,
+                                           int N, const float* h0, void* y, float* h_out,
+                                           float* marks, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+SANATAN_API size_t sanatan_selective_scan_bwd_workspace_size(int B, int T, int D, int N);
+SANATAN_API int sanatan_selective_scan_bwd(const void* u, const void* dt, const void* z,
+                                           int64_t ldz, const void* Bm, int64_t ldb,
+                                           const void* Cm, int64_t ldc, const float* A,
+                                           const float* skip, const float* dt_bias, int dtype,
+                                           int softplus, const int64_t* lens, int B, int T, int D,
+                                           int N, const void* dy, const float* marks,
+                                           const float* dh_out, void* du, void* ddt, void* dz,
+                                           float* dA, void* dB, void* dC, float* dskip,
+                                           float* ddt_bias, float* dh0, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+SANATAN_API int sanatan_selective_scan_step(float* h, const void* u, const void* dt,
+                                            const void* z, int64_t ldz, const void* Bm,
+                                            int64_t ldb, const void* Cm, int64_t ldc,
+                                            const float* A, const float* skip,
+                                            const float* dt_bias, int dtype, int softplus,
+                                            int nseq, int D, int N, void* y, void* stream);
 
 #ifdef __cplusplus
 }
