@@ -342,8 +342,6 @@ cudaError_t causal_conv_step_launch(const ConvArgs& a, cudaStream_t st);
 // selective_scan_bwd.cu).
 constexpr int kSelectiveMark = 16;      // tokens between two marks (saved states)
 constexpr int kSelectiveStates = 128;   // N at most
-constexpr int kSelectiveFwdBlocks = 4;  // blocks of an SM that the splits aim at
-constexpr int kSelectiveBwdBlocks = 3;
 struct SelectiveArgs {
   const void* u = nullptr;
   const void* dt = nullptr;
@@ -369,7 +367,7 @@ struct SelectiveArgs {
 };
 int selective_lanes(int N);
 int selective_blocks(int D, int N);
-int selective_segments(int B, int T, int D, int N, int per_sm, int* tiles_per_segment);
+int selective_segments(int B, int T, int D, int N, int* tiles_per_segment);
 size_t selective_scan_fwd_workspace_bytes(int B, int T, int D, int N);
 cudaError_t selective_scan_fwd_launch(SelectiveArgs a, void* workspace, cudaStream_t st);
 cudaError_t selective_scan_step_launch(SelectiveArgs a, cudaStream_t st);

@@ -11,7 +11,8 @@
 // and the single-token step.  States and all sums are float32.
 //
 // A block of four warps takes 128 / L channels of a stretch of tokens, L lanes a channel, four
-// states a lane (L = N / 4, up to a power of two).  In tiles of sixteen tokens the threads
+// states a lane (L = N / 4, up to a power of two); neighbouring lanes have neighbouring
+// channels, so that loads of B and C from shared memory, the same for both, are half as long.  In tiles of sixteen tokens the threads
 // form delta, delta u and v once for each token and channel and leave them in shared memory
 // with B and C; then each lane walks its four states through the tile.  Sums over the
 // states meet by shuffles, four tokens at a time, so that a lane ends with one
@@ -35,6 +36,7 @@
 #include "pdl.cuh"
 #include "sanatan_internal.h"
 #include "sanatan_math.cuh"
+#include "vec_io.cuh"
 
 namespace sanatan {
 namespace {
@@ -53,11 +55,14 @@ struct Geo {
   static constexpr int CW = 32 / L;          // channels of a warp
   static constexpr int CB = CW * kWarps;     // of a block
   static constexpr int NP = kStates * L;     // states, with those that fill up
-  static constexpr int kCells = kTile * CB;  // (token, channel) pairs of a tile
-  static constexpr int kItems = (kCells + kThreads - 1) / kThreads;  // of a thread
-  static constexpr int kPairs = kTile * 2 * NP;   // values of B and C of a tile
-  static constexpr int kPairItems = kPairs / kThreads;
-  static constexpr int kPitch = CB + 8;  // (four tokens of eight channels: 32 banks)
+  // A warp's cells, (token, channel) pairs of a tile, W neighbouring channels at a time.
+  static constexpr int W = CW < 4 ? CW : 4;
+  static constexpr int kCells = kTile * CW / W;            // of a warp
+  static constexpr int kItems = (kCells + 31) / 32;        // of a lane
+  static constexpr int kRowPitch = CW + 1;                 // of float4: no bank conflicts
+  // B and C of a tile, four states at a time.
+  static constexpr int kQuads = kTile * 2 * L;
+  static constexpr int kQuadItems = (kQuads + kThreads - 1) / kThreads;
 };
 
 __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
@@ -76,26 +81,75 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// 2^x of a pair.  The hardware's power of two is 0.3 steps of 2^-24 low next to 1, and a
-// memory of n tokens multiplies the mean error of its decays by n; the first four terms of
-// the series are within 0.15 steps for |x| < 1/32 (x ln 2 < 0.0217; the next is its fourth
-// power / 24) and have no bias beside the rounding.  Beyond, memories are below 50 tokens.
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
-  const uint64_t c1 = pk2(kLn2, kLn2), one = pk2(1.0f, 1.0f);
-  const uint64_t c2 = pk2(0.24022650695910072f, 0.24022650695910072f);    // ln(2)^2 / 2
-  const uint64_t c3 = pk2(0.055504108664821580f, 0.055504108664821580f);  // ln(2)^3 / 6
-  const uint64_t p = ffma2(ffma2(ffma2(c3, x, c2), x, c1), x, one);
-  float x0, x1, p0, p1;
-  upk2(x, x0, x1);
-  upk2(p, p0, p1);
-  return pk2(fabsf(x0) < 0.03125f ? p0 : ex2(x0), fabsf(x1) < 0.03125f ? p1 : ex2(x1));
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// 2^x of a pair by the hardware, which is 0.1 to 0.8 steps of 2^-24 low on average (measured,
+// by binades of x).  A memory of n tokens multiplies that by n: see Decays.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
+  float a, b;
+  upk2(x, a, b);
+  return pk2(ex2(a), ex2(b));
+}
 
-// log(1 + exp(x)); for large x that is x.
-__device__ __forceinline__ float softplus(float x) {
-  return fmaxf(x, 0.0f) + log1pf(__expf(-fabsf(x)));
+// 2^x without that bias where x is small: the first four terms of the series are within 0.15
+// steps for |x| < 1/32 (x ln 2 < 0.0217; the next is its fourth power / 24).
+__device__ __forceinline__ float exp2_near(float x) {
+  const float p = fmaf(fmaf(fmaf(0.055504108664821580f, x, 0.24022650695910072f), x, kLn2), x,
+                       1.0f);  // (ln(2)^3 / 6, ln(2)^2 / 2, ln(2))
+  return fabsf(x) < 0.03125f ? p : ex2(x);
+}
+
+// What the decays of a tile multiply a lane's states by: their product as they were rounded,
+// and the sum of delta, which gives what it should be, 2^(A sum delta).  Their ratio puts
+// the state right once a tile, so that the bias of sixteen decays (3e-7) is all that is ever
+// in a state, whatever its memory.  (The series for every decay instead: 973 us for the forward
+// of B 8 T 4096 D 1536 N 16 bf16, 750 so.)
+struct Decays {
+  uint64_t q0, q1, sum;
+  __device__ __forceinline__ Decays() : q0(pk2(1.0f, 1.0f)), q1(q0), sum(pk2(0.0f, 0.0f)) {}
+  __device__ __forceinline__ void add(uint64_t a0, uint64_t a1, uint64_t delta) {
+    q0 = fmul2(q0, a0), q1 = fmul2(q1, a1), sum = fadd2(sum, delta);
+  }
+  // (x of 8 and more: the memory is two tokens, and q may have no digits left)
+  __device__ __forceinline__ static float ratio(float x, float q) {
+    return fabsf(x) < 8.0f ? exp2_near(x) * rcp(q) : 1.0f;
+  }
+  __device__ __forceinline__ void put_right(uint64_t A0, uint64_t A1, uint64_t& h0,
+                                            uint64_t& h1) const {
+    float x[kStates], q[kStates];
+    upk2(fmul2(sum, A0), x[0], x[1]);
+    upk2(fmul2(sum, A1), x[2], x[3]);
+    upk2(q0, q[0], q[1]);
+    upk2(q1, q[2], q[3]);
+    h0 = fmul2(h0, pk2(ratio(x[0], q[0]), ratio(x[1], q[1])));
+    h1 = fmul2(h1, pk2(ratio(x[2], q[2]), ratio(x[3], q[3])));
+  }
+};
+
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(x * -kLog2e)); }
+
+// log(1 + exp(x)) = max(x, 0) + log(1 + e) of a pair, e = exp(-|x|) <= 1, with log(1 + e) = 2
+// atanh(r), r = e / (2 + e) <= 1/3: the series r + r^3 / 3 + r^5 / 5 ... to r^13 is within
+// 2^-26 of its value, for all e alike, so that the small steps of delta have all their digits.
+__device__ __forceinline__ uint64_t softplus_pair(uint64_t x) {
+  float x0, x1, e0, e1;
+  upk2(x, x0, x1);
+  e0 = ex2(fabsf(x0) * -kLog2e), e1 = ex2(fabsf(x1) * -kLog2e);
+  const uint64_t r = pk2(e0 * rcp(2.0f + e0), e1 * rcp(2.0f + e1));
+  const uint64_t q = fmul2(r, r);
+  auto both = [](float c) { return pk2(c, c); };
+  uint64_t p = ffma2(q, both(1.0f / 13), both(1.0f / 11));
+  p = ffma2(p, q, both(1.0f / 9));
+  p = ffma2(p, q, both(1.0f / 7));
+  p = ffma2(p, q, both(1.0f / 5));
+  p = ffma2(p, q, both(1.0f / 3));
+  p = ffma2(p, q, both(1.0f));
+  // (a NaN goes through r; fmaxf alone would drop it)
+  return ffma2(fmul2(r, both(2.0f)), p, pk2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
 }
 
 __device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
@@ -194,28 +248,234 @@ struct StatePlace {
   }
 };
 
-// B and C of a tile, loaded into registers, then put into shared memory [token][B | C][NP].
-template <typename E, int L>
-struct PairTile {
+__device__ __forceinline__ void copy_async(void* to, const void* from, bool real, int bytes) {
+  const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  const int n = real ? bytes : 0;  // (the rest is filled with zeros)
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n)
+                 : "memory");
+  else if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(n)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// A tile of the tensors of a block, as they are in memory, on its way to shared memory while
+// tiles before are worked on: NT tensors of [B, T, D] (its channels), then B and C.  Where
+// rows are words, by asynchronous copies, the same few places of every tile for a thread;
+// else through registers (begin() loads, end() stores).  Tokens behind the sequence and
+// channels behind the last are zeros, and not read.
+template <typename E, int L, bool ALIGNED, int NT>
+struct Stage {
   using G = Geo<L>;
-  float r[G::kPairItems];
-  __device__ __forceinline__ void load(const SelectiveArgs& a, int b, int t0, int n) {
+  static constexpr int kSize = sizeof(E);
+  static constexpr int kRow = G::CB * kSize;                 // bytes
+  static constexpr int kChunk = kRow < 16 ? kRow : 16;
+  static constexpr int kPitch = kRow + 16;                   // (rows in different banks)
+  static constexpr int kCell = kTile * kPitch;
+  static constexpr int kPairPitch = G::NP * kSize;
+  static constexpr int kPair = kTile * kPairPitch;
+  static constexpr int kBytes = NT * kCell + 2 * kPair;      // of a buffer
+  static constexpr int kPer = kRow / kChunk, kCellChunks = kTile * kPer;
+  static constexpr int kPairPer = (kPairPitch + 15) / 16, kPairChunks = kTile * kPairPer;
+  static constexpr int kChunks = NT * kCellChunks + 2 * kPairChunks;
+  static constexpr int kSlots = ALIGNED ? (kChunks + kThreads - 1) / kThreads : 1;
+  static constexpr int kOne = kTile * G::CB / kThreads > 0 ? kTile * G::CB / kThreads : 1;
+  static constexpr int kPairOne = kTile * G::NP / kThreads > 0 ? kTile * G::NP / kThreads : 1;
+  static constexpr int kNever = 1 << 30;
+
+  // ALIGNED: where a slot's next copy comes from and goes to, its token of the tile
+  const char* from[kSlots];
+  int64_t step[kSlots];
+  int to[kSlots], token[kSlots], bytes[kSlots];
+  // else: what is on its way
+  E r[ALIGNED ? 1 : NT * kOne + 2 * kPairOne];
+  const E* x[NT + 2];
+  int64_t ld[NT + 2], row0;
+  int n, d0, D, N;
+
+  // A null tensor is left out.  Tiles go from k on, up (dir 1) or down (-1).
+  __device__ __forceinline__ void init(const void* const (&tensors)[NT + 2],
+                                       const int64_t (&lds)[NT + 2], const SelectiveArgs& a,
+                                       int64_t row0_, int n_, int d0_, int k, int dir) {
+    n = n_, d0 = d0_, D = a.D, N = a.N, row0 = row0_;
 #pragma unroll
-    for (int i = 0; i < G::kPairItems; ++i) {
-      const int k = threadIdx.x + i * kThreads, s = k % G::NP, which = k / G::NP % 2;
-      const int t = t0 + k / (2 * G::NP);
-      const int64_t row = static_cast<int64_t>(b) * a.T + t;
-      r[i] = 0.0f;
-      if (t < n && s < a.N)
-        r[i] = which == 0 ? load_as_float(static_cast<const E*>(a.Bm) + row * a.ldb + s)
-                          : load_as_float(static_cast<const E*>(a.Cm) + row * a.ldc + s);
+    for (int q = 0; q < NT + 2; ++q) x[q] = static_cast<const E*>(tensors[q]), ld[q] = lds[q];
+    if constexpr (ALIGNED) place(a, k, dir);
+  }
+  __device__ __forceinline__ void place(const SelectiveArgs& a, int k, int dir) {
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      int c = threadIdx.x + i * kThreads;
+      from[i] = reinterpret_cast<const char*>(x[0]);
+      step[i] = 0, to[i] = 0, token[i] = kNever, bytes[i] = 0;
+      int base = 0;
+#pragma unroll
+      for (int q = 0; q < NT + 2; ++q) {
+        const bool cell = q < NT;
+        const int chunks = cell ? kCellChunks : kPairChunks, per = cell ? kPer : kPairPer;
+        const int chunk = cell ? kChunk : 16;
+        if (c >= 0 && c < chunks) {
+          const int t = c / per, at = c % per * chunk, v = at / kSize;
+          to[i] = base + t * (cell ? kPitch : kPairPitch) + at;
+          bytes[i] = chunk;
+          if (x[q] != nullptr && (cell ? d0 + v < D : v < N)) {
+            from[i] = reinterpret_cast<const char*>(
+                x[q] + (row0 + static_cast<int64_t>(k) * kTile + t) * ld[q] + (cell ? d0 + v : v));
+            step[i] = ld[q] * (dir * kTile * kSize);
+            token[i] = t;
+          }
+        }
+        c -= chunks;
+        base += cell ? kCell : kPair;
+      }
     }
   }
-  __device__ __forceinline__ void put(float* pairs) const {
+  __device__ __forceinline__ void begin(char* buffer, int k) {
+    const int left = n - k * kTile;
+    if constexpr (ALIGNED) {
 #pragma unroll
-    for (int i = 0; i < G::kPairItems; ++i) pairs[threadIdx.x + i * kThreads] = r[i];
+      for (int i = 0; i < kSlots; ++i) {
+        if (kChunk == 16) {
+          if (i + 1 < kSlots || kChunks % kThreads == 0 || bytes[i] != 0)
+            copy_async(buffer + to[i], from[i], token[i] < left, 16);
+        } else if (bytes[i] == 16) {
+          copy_async(buffer + to[i], from[i], token[i] < left, 16);
+        } else if (bytes[i] != 0) {
+          copy_async(buffer + to[i], from[i], token[i] < left, kChunk);
+        }
+        from[i] += step[i];
+      }
+      copy_commit();
+    } else {
+      load(row0 + static_cast<int64_t>(k) * kTile, left);
+    }
   }
+  __device__ __forceinline__ void load(int64_t row, int left) {
+#pragma unroll
+    for (int q = 0; q < NT + 2; ++q) {
+      if (x[q] == nullptr) continue;
+#pragma unroll
+      for (int i = 0; i < (q < NT ? kOne : kPairOne); ++i) {
+        const int c = threadIdx.x + i * kThreads;
+        const int t = q < NT ? c / G::CB : c / G::NP, v = q < NT ? d0 + c % G::CB : c % G::NP;
+        const bool real = t < kTile && t < left && v < (q < NT ? D : N);
+        // (one load whether real or not: a branch would wait for it)
+        E e = *(real ? x[q] + (row + t) * ld[q] + v : x[q]);
+        if (!real) e = store_from_float<E>(0.0f);
+        r[(q < NT ? q * kOne : NT * kOne + (q - NT) * kPairOne) + i] = e;
+      }
+    }
+  }
+  __device__ __forceinline__ void end(char* buffer) const {
+    if constexpr (!ALIGNED) store(buffer);
+  }
+  __device__ __forceinline__ void store(char* buffer) const {
+#pragma unroll
+    for (int q = 0; q < NT + 2; ++q) {
+      if (x[q] == nullptr) continue;
+      char* base = buffer + (q < NT ? q * kCell : NT * kCell + (q - NT) * kPair);
+#pragma unroll
+      for (int i = 0; i < (q < NT ? kOne : kPairOne); ++i) {
+        const int c = threadIdx.x + i * kThreads;
+        const int t = q < NT ? c / G::CB : c / G::NP, v = q < NT ? c % G::CB : c % G::NP;
+        if (t < kTile)
+          *reinterpret_cast<E*>(base + t * (q < NT ? kPitch : kPairPitch) + v * kSize) =
+              r[(q < NT ? q * kOne : NT * kOne + (q - NT) * kPairOne) + i];
+      }
+    }
+  }
+  // W channels of a token of tensor q from c, as floats.
+  __device__ __forceinline__ static void get(const char* buffer, int q, int t, int c,
+                                             float (&f)[G::W]) {
+    Vec<E, G::W> v;
+    v.load(reinterpret_cast<const E*>(buffer + q * kCell + t * kPitch + c * kSize));
+    v.get(f);
+  }
+  // B and C from there to floats, [token][B | C][ORDERS][WIDE], zeros behind N.
+  template <int ORDERS, int WIDE>
+  __device__ __forceinline__ static void pairs_to_float(const char* buffer, int N,
+                                                        float (*pairs)[2][ORDERS][WIDE]);
 };
+
+// The order of a lane's states in its registers: register j holds state j ^ order.  In the
+// backward's main kernel neighbouring channels hold theirs in different orders, so that where
+// two lanes halve their values each keeps the first and sends the last, without selecting.
+__device__ __forceinline__ void reorder(float (&f)[kStates], int order) {
+  if (order & 2) {
+    const float a = f[0], b = f[1];
+    f[0] = f[2], f[1] = f[3], f[2] = a, f[3] = b;
+  }
+  if (order & 1) {
+    const float a = f[0], b = f[2];
+    f[0] = f[1], f[2] = f[3], f[1] = a, f[3] = b;
+  }
+}
+
+template <typename E, int L, bool ALIGNED, int NT>
+template <int ORDERS, int WIDE>
+__device__ __forceinline__ void Stage<E, L, ALIGNED, NT>::pairs_to_float(
+    const char* buffer, int N, float (*pairs)[2][ORDERS][WIDE]) {
+#pragma unroll
+  for (int i = 0; i < G::kQuadItems; ++i) {
+    const int k = threadIdx.x + i * kThreads, q = k % L, which = k / L % 2, t = k / (2 * L);
+    if (G::kQuads % kThreads != 0 && k >= G::kQuads) break;
+    Vec<E, 4> v;
+    float f[4];
+    v.load(reinterpret_cast<const E*>(buffer + NT * kCell + which * kPair + t * kPairPitch) +
+           4 * q);
+    v.get(f);
+    if (4 * q + 4 > N)  // (what fills up was never written)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = 4 * q + j < N ? f[j] : 0.0f;
+#pragma unroll
+    for (int o = 0; o < ORDERS; ++o) {
+      const int x = (o & 1) * 2 + (o >> 1);
+      *reinterpret_cast<float4*>(&pairs[t][which][o][4 * q]) =
+          make_float4(f[0 ^ x], f[1 ^ x], f[2 ^ x], f[3 ^ x]);
+    }
+  }
+}
+
+// delta of W cells of a token from dt (zero where the token is not there: a = 1 and no
+// input, the state passes).
+template <int W>
+__device__ __forceinline__ void steps(float (&delta)[W], const float (&bias)[W], bool soft,
+                                      bool real) {
+#pragma unroll
+  for (int j = 0; j < W; ++j) delta[j] += bias[j];
+  if (soft) {
+#pragma unroll
+    for (int j = 0; j < W; j += 2) {
+      float other = 0.0f;
+      upk2(softplus_pair(pk2(delta[j], delta[j + 1 < W ? j + 1 : j])), delta[j],
+           j + 1 < W ? delta[j + 1] : other);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) delta[j] = real ? delta[j] : 0.0f;
+}
+
+// W neighbours of a row from d, those that exist.
+template <typename E, int W, bool ALIGNED>
+__device__ __forceinline__ void store_cells(E* row, int d, int D, const float (&f)[W]) {
+  if (ALIGNED) {
+    Vec<E, W> v;
+    v.put(f);
+    if (d < D) v.store(row + d);
+  } else {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (d + j < D) row[d + j] = store_from_float<E>(f[j]);
+  }
+}
 
 // The carries of S segments, in place: H[b][s][D][N] becomes the state before segment s
 // (reverse: the gradient behind it); sums [b][s][D] of delta.
@@ -260,6 +520,19 @@ cudaError_t launch_carry(const SelectiveArgs& a, const float* first, bool revers
   const int64_t all = static_cast<int64_t>(a.B) * a.D * a.N;
   return launch(selective_carry_kernel, (all - 1) / 256 + 1, 256, 0, st, a.carry,
                 static_cast<const float*>(a.sums), a.A, first, a.segments, a.D, a.N, all, reverse);
+}
+
+// Whether every row of every tensor is 16-byte words.
+template <typename E>
+bool words(const SelectiveArgs& a, std::initializer_list<const void*> dense) {
+  const int64_t V = 16 / sizeof(E);
+  if (a.D % V != 0 || a.N % V != 0 || a.ldb % V != 0 || a.ldc % V != 0) return false;
+  if (a.z != nullptr && a.ldz % V != 0) return false;
+  for (const void* p : {a.u, a.dt, a.z, a.Bm, a.Cm})
+    if (!at_bytes(p, 16)) return false;
+  for (const void* p : dense)
+    if (!at_bytes(p, 16)) return false;
+  return true;
 }
 
 inline bool state_words(int N, std::initializer_list<const void*> states) {

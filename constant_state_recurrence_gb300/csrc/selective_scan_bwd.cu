@@ -1,301 +1,448 @@
 // The selective scan's backward (formulas and method: selective_scan.cuh).
 //
-// A tile's states and decays (sixteen tokens x four states a lane) stay in registers between
-// the walk forward from the mark and the walk back, so that a decay is formed once.
+// A tile is walked forward from its mark, its decays kept in registers and the state before
+// every token in shared memory, then back.
 #include "selective_scan.cuh"
 
 namespace sanatan {
 namespace {
 
-// Shared memory of a block, beside the sums of dB and dC [warp][token][B | C][NP].
-template <int L>
-struct Shared {
+template <typename E, int L, bool ALIGNED>
+struct BwdStateShared {
   using G = Geo<L>;
-  float4 cells[kTile][G::CB];  // delta, delta, delta u, delta u
-  float2 v[kTile][G::CB];      // v, v
-  float pairs[kTile][2][G::NP];
-  float sums[3][kTile][G::kPitch];  // of dh B, of w A, and y
-  float by_warp[kWarps][kTile][2][G::NP];
+  using Tiles = Stage<E, L, ALIGNED, 3>;      // dt, z, dy
+  float4 cells[kWarps][kTile][G::kRowPitch];  // delta, delta, v, v
+  float pairs[2][kTile][2][1][G::NP];
+  char raw[3][Tiles::kBytes];
 };
 
 // The walk back alone, from no gradient behind the segment: what its own tokens add to the
 // gradient before it, and its sum of delta.
-template <typename E, int L>
+template <typename E, int L, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) selective_bwd_state_kernel(SelectiveBwdArgs args) {
   using G = Geo<L>;
+  constexpr int W = G::W;
+  using Sm = BwdStateShared<E, L, ALIGNED>;
+  using Tiles = typename Sm::Tiles;
   const SelectiveArgs& a = args.f;
-  __shared__ float4 cells[kTile][G::CB];  // delta, delta, v, v
-  __shared__ __align__(16) float pairs[kTile][2][G::NP];
+  extern __shared__ float4 smem4[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem4);
   const Place<L> at(a);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, l = lane % L;
-  const int mine = warp * G::CW + lane / L;
-  const int d0 = at.cb * G::CB, d = d0 + mine;
-  const int cell_ch = tid % G::CB, cell_d = d0 + cell_ch;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, l = lane / G::CW;
+  const int mine = lane % G::CW;
+  const int d0 = at.cb * G::CB, w0 = d0 + warp * G::CW, d = w0 + mine;
+  constexpr int kPer = G::CW / W, kStep = 32 / kPer;
+  const int cell_c = lane % kPer * W, cell_t = lane / kPer, cell_d = w0 + cell_c;
   const StatePlace st(d, l, a.D, a.N, a.vec);
   wait_for_previous();
   const int n = length_of(a.lens, at.b, a.T);
-  const int64_t slab = static_cast<int64_t>(a.D) * a.N;
+  const int64_t slab = static_cast<int64_t>(a.D) * a.N, row0 = static_cast<int64_t>(at.b) * a.T;
+  const bool gated = a.z != nullptr;
+  const int live = min(at.k1, (n + kTile - 1) / kTile), last = live - 1;
+  Tiles tiles;
+  tiles.init({a.dt, a.z, args.dy, nullptr, a.Cm}, {a.D, a.ldz, a.D, 0, a.ldc}, a, row0, n, d0,
+             last, -1);
+  if (last >= at.k0) tiles.begin(sm.raw[0], last), tiles.end(sm.raw[0]);
+  if (last > at.k0) tiles.begin(sm.raw[1], last - 1), tiles.end(sm.raw[1]);
   float f[kStates];
   st.load(a.A, f);
   const uint64_t A0 = pk2(f[0] * kLog2e, f[1] * kLog2e), A1 = pk2(f[2] * kLog2e, f[3] * kLog2e);
   uint64_t g0 = pk2(0.0f, 0.0f), g1 = g0;
-  const bool there = cell_d < a.D;
-  const float bias = there && a.dt_bias != nullptr ? a.dt_bias[cell_d] : 0.0f;
-  const E* DT = static_cast<const E*>(a.dt);
-  const E* Z = static_cast<const E*>(a.z);
-  const E* DY = static_cast<const E*>(args.dy);
-  const int64_t row0 = static_cast<int64_t>(at.b) * a.T;
-  float sum = 0.0f;
-  float rdt[G::kItems], rz[G::kItems], rdy[G::kItems];
-  PairTile<E, L> pt;
-  auto load = [&](int k) {
+  float bias[W], sum[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    bias[j] = cell_d + j < a.D && a.dt_bias != nullptr ? a.dt_bias[cell_d + j] : 0.0f;
+    sum[j] = 0.0f;
+  }
+  if (last >= at.k0) {
+    copy_wait<0>();
+    __syncthreads();
+    Tiles::pairs_to_float(sm.raw[0], a.N, sm.pairs[last & 1]);
+  }
+  int now = 0;  // the buffer of tile k
+  for (int k = last; k >= at.k0; --k) {
+    const int next = now == 2 ? 0 : now + 1, after = next == 2 ? 0 : next + 1;
+    copy_wait<0>();
+    __syncthreads();
+    if (k - 2 >= at.k0) tiles.begin(sm.raw[after], k - 2);
+    if (k > at.k0) Tiles::pairs_to_float(sm.raw[next], a.N, sm.pairs[(k - 1) & 1]);
 #pragma unroll
     for (int i = 0; i < G::kItems; ++i) {
-      const int cell = tid + i * kThreads, t = k * kTile + cell / G::CB;
-      rdt[i] = rz[i] = rdy[i] = 0.0f;
-      if (cell < G::kCells && t < n && there) {
-        rdt[i] = load_as_float(DT + (row0 + t) * a.D + cell_d);
-        rdy[i] = load_as_float(DY + (row0 + t) * a.D + cell_d);
-        if (Z != nullptr) rz[i] = load_as_float(Z + (row0 + t) * a.ldz + cell_d);
+      const int t = cell_t + i * kStep;
+      if (G::kCells % 32 != 0 && t >= kTile) break;
+      float delta[W], v[W], z[W];
+      Tiles::get(sm.raw[now], 0, t, warp * G::CW + cell_c, delta);
+      Tiles::get(sm.raw[now], 2, t, warp * G::CW + cell_c, v);
+      if (gated) Tiles::get(sm.raw[now], 1, t, warp * G::CW + cell_c, z);
+      steps<W>(delta, bias, a.softplus, k * kTile + t < n);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        sum[j] += delta[j];
+        if (gated) v[j] *= z[j] * sigmoid(z[j]);
+        sm.cells[warp][t][cell_c + j] = make_float4(delta[j], delta[j], v[j], v[j]);
       }
     }
-    pt.load(a, at.b, k * kTile, n);
-  };
-  const int live = min(at.k1, (n + kTile - 1) / kTile);
-  if (at.k0 < live) load(live - 1);
-  for (int k = live - 1; k >= at.k0; --k) {
-#pragma unroll
-    for (int i = 0; i < G::kItems; ++i) {
-      const int cell = tid + i * kThreads, t = k * kTile + cell / G::CB;
-      float delta = rdt[i] + bias, v = rdy[i];
-      if (a.softplus) delta = softplus(delta);
-      if (t >= n || !there || cell >= G::kCells) delta = 0.0f;
-      if (Z != nullptr) v *= rz[i] * sigmoid(rz[i]);
-      sum += delta;
-      if (cell < G::kCells) cells[cell / G::CB][cell_ch] = make_float4(delta, delta, v, v);
-    }
-    pt.put(&pairs[0][0][0]);
-    __syncthreads();
-    if (k > at.k0) load(k - 1);
+    __syncwarp();
+    Decays decays;
 #pragma unroll
     for (int t = kTile - 1; t >= 0; --t) {
-      const ulonglong2 c = reinterpret_cast<const ulonglong2&>(cells[t][mine]);
-      const ulonglong2 Cv = reinterpret_cast<const ulonglong2&>(pairs[t][1][kStates * l]);
-      g0 = fmul2(exp2_pair(fmul2(c.x, A0)), ffma2(c.y, Cv.x, g0));
-      g1 = fmul2(exp2_pair(fmul2(c.x, A1)), ffma2(c.y, Cv.y, g1));
+      const ulonglong2 c = reinterpret_cast<const ulonglong2&>(sm.cells[warp][t][mine]);
+      const ulonglong2 Cv =
+          reinterpret_cast<const ulonglong2&>(sm.pairs[k & 1][t][1][0][kStates * l]);
+      const uint64_t a0 = exp2_pair(fmul2(c.x, A0)), a1 = exp2_pair(fmul2(c.x, A1));
+      g0 = fmul2(a0, ffma2(c.y, Cv.x, g0));
+      g1 = fmul2(a1, ffma2(c.y, Cv.y, g1));
+      decays.add(a0, a1, c.x);
     }
-    __syncthreads();
+    decays.put_right(A0, A1, g0, g1);
+    __syncwarp();
+    if (k - 2 >= at.k0) tiles.end(sm.raw[after]);
+    now = next;
   }
-  st.store(a.carry + (static_cast<int64_t>(at.b) * a.segments + at.seg) * slab, g0, g1);
-  float* all = &pairs[0][0][0];
-  all[tid] = sum;  // (the tile's readers are done)
-  __syncthreads();
-  if (tid < G::CB && there) {
-    for (int i = tid + G::CB; i < kThreads; i += G::CB) sum += all[i];
-    a.sums[(static_cast<int64_t>(at.b) * a.segments + at.seg) * a.D + cell_d] = sum;
+  const int64_t part = static_cast<int64_t>(at.b) * a.segments + at.seg;
+  st.store(a.carry + part * slab, g0, g1);
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+#pragma unroll
+    for (int bit = kPer; bit < 32; bit *= 2) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], bit);
+    if (cell_t == 0 && cell_d + j < a.D) a.sums[part * a.D + cell_d + j] = sum[j];
   }
 }
 
-template <typename E, int L>
-__global__ void __launch_bounds__(kThreads, L == 4 || L == 8 ? kSelectiveBwdBlocks : 1)
+// The lane bits over which the sums over channels are halved: first by two states of four,
+// then by one of two, so that these say a lane's order; then (where there is a third) into
+// dB and dC.  Neighbouring lanes have the same order where they can.
+template <int L>
+struct Bits {
+  static constexpr int CW = Geo<L>::CW;
+  static constexpr int A = CW >= 4 ? 2 : 1, B = CW >= 8 ? 4 : 1;  // (dB and dC: 1)
+  static constexpr int kOrders = CW < 4 ? CW : 4;
+  __device__ __forceinline__ static int order(int lane) {  // 0 .. kOrders - 1
+    return (CW >= 2 && (lane & A) ? 1 : 0) + (CW >= 4 && (lane & B) ? 2 : 0);
+  }
+};
+
+template <typename E, int L, bool ALIGNED>
+struct BwdShared {
+  using G = Geo<L>;
+  using Tiles = Stage<E, L, ALIGNED, 4>;      // u, dt, z, dy
+  // The state before every token, of each lane; behind it, where the walk back is done, the
+  // warp's sums of dB and dC, [B | C][NP] from the token's place on.
+  float4 states[kWarps][kTile][L == 32 ? 64 : 32];  // (a row holds 2 NP sums, too)
+  float4 cells[kWarps][kTile][G::kRowPitch];  // delta, delta u, v, v
+  float pairs[kTile][2][Bits<L>::kOrders][G::NP + 8];  // (orders in different banks)
+  float sums[kWarps][3][kTile][G::CW];        // of dh B, of w A, and y
+  char raw[Tiles::kBytes];
+};
+
+__device__ __forceinline__ uint64_t shfl2(uint64_t v, int bit) {
+  float a, b;
+  upk2(v, a, b);
+  return pk2(__shfl_xor_sync(0xffffffffu, a, bit), __shfl_xor_sync(0xffffffffu, b, bit));
+}
+
+// The sum over a warp's channels of its lanes' dB and dC (b0: registers 0 and 1, b1: 2 and
+// 3).  Returns how a lane's values are to be written: out [0], or [0] (dB) and [1] (dC), or
+// [0, 1] and [2, 3], or all eight.
+template <int L>
+__device__ __forceinline__ void sum_channels(uint64_t b0, uint64_t b1, uint64_t c0, uint64_t c1,
+                                             int lane, float (&out)[8]) {
+  constexpr int CW = Geo<L>::CW;
+  if constexpr (CW >= 2) {
+    b0 = fadd2(b0, shfl2(b1, Bits<L>::A));
+    c0 = fadd2(c0, shfl2(c1, Bits<L>::A));
+    float p, q, r, s;
+    upk2(b0, p, q);
+    upk2(c0, r, s);
+    if constexpr (CW >= 4) {
+      p += __shfl_xor_sync(0xffffffffu, q, Bits<L>::B);
+      r += __shfl_xor_sync(0xffffffffu, s, Bits<L>::B);
+      if constexpr (CW >= 8) {
+        const bool up = lane & 1;
+        p = (up ? r : p) + __shfl_xor_sync(0xffffffffu, up ? p : r, 1);
+#pragma unroll
+        for (int bit = 8; bit < CW; bit *= 2) p += __shfl_xor_sync(0xffffffffu, p, bit);
+      }
+    }
+    out[0] = p, out[1] = CW >= 4 ? r : q, out[2] = r, out[3] = s;
+  } else {
+    upk2(b0, out[0], out[1]);
+    upk2(b1, out[2], out[3]);
+    upk2(c0, out[4], out[5]);
+    upk2(c1, out[6], out[7]);
+  }
+}
+// They go to [B | C][NP] of the token; x: the lane's order.
+template <int L>
+__device__ __forceinline__ void put_channels(const float (&v)[8], int lane, int x, float* to) {
+  constexpr int CW = Geo<L>::CW, NP = Geo<L>::NP;
+  float* at = to + kStates * (lane / CW);
+  if constexpr (CW >= 8) {
+    if (lane % CW < 8) at[(lane & 1) * NP + x] = v[0];
+  } else if constexpr (CW == 4) {
+    at[x] = v[0];
+    at[NP + x] = v[1];
+  } else if constexpr (CW == 2) {
+    at[0 ^ x] = v[0], at[1 ^ x] = v[1];
+    at[NP + (0 ^ x)] = v[2], at[NP + (1 ^ x)] = v[3];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) at[j] = v[j], at[NP + j] = v[4 + j];
+  }
+}
+
+template <typename E, int L, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
     selective_bwd_kernel(SelectiveBwdArgs args) {
   using G = Geo<L>;
+  constexpr int W = G::W;
+  using Sm = BwdShared<E, L, ALIGNED>;
+  using Tiles = typename Sm::Tiles;
   const SelectiveArgs& a = args.f;
   extern __shared__ float4 smem4[];
-  Shared<L>& sm = *reinterpret_cast<Shared<L>*>(smem4);
+  Sm& sm = *reinterpret_cast<Sm*>(smem4);
   const Place<L> at(a);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, l = lane % L;
-  const int mine = warp * G::CW + lane / L;
-  const int d0 = at.cb * G::CB, d = d0 + mine;
-  const int cell_ch = tid % G::CB, cell_d = d0 + cell_ch;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, l = lane / G::CW;
+  const int mine = lane % G::CW;
+  const int d0 = at.cb * G::CB, w0 = d0 + warp * G::CW, d = w0 + mine;
+  constexpr int kPer = G::CW / W, kStep = 32 / kPer;
+  const int cell_c = lane % kPer * W, cell_t = lane / kPer, cell_d = w0 + cell_c;
+  const int order = Bits<L>::order(lane), x = (order & 1) * 2 + (order >> 1);
   const StatePlace st(d, l, a.D, a.N, a.vec);
   wait_for_previous();
   const int n = length_of(a.lens, at.b, a.T);
-  const int64_t slab = static_cast<int64_t>(a.D) * a.N;
+  const int64_t slab = static_cast<int64_t>(a.D) * a.N, row0 = static_cast<int64_t>(at.b) * a.T;
   const int64_t part = static_cast<int64_t>(at.b) * a.segments + at.seg;
+  const bool gated = a.z != nullptr;
+  E* DU = static_cast<E*>(args.du);
+  E* DDT = static_cast<E*>(args.ddt);
+  E* DZ = static_cast<E*>(args.dz);
+  const int live = min(at.k1, (n + kTile - 1) / kTile);
+  Tiles tiles;
+  tiles.init({a.u, a.dt, a.z, args.dy, a.Bm, a.Cm}, {a.D, a.D, a.ldz, a.D, a.ldb, a.ldc}, a, row0,
+             n, d0, live - 1, -1);
+  float rmark[kStates];
+  auto begin = [&](int k) {
+    st.load(args.marks + (static_cast<int64_t>(at.b) * at.tiles + k) * slab, rmark);
+    tiles.begin(sm.raw, k);
+  };
+  if (at.k0 < live) begin(live - 1), tiles.end(sm.raw);
   uint64_t A0, A1, g0, g1, dA0 = pk2(0.0f, 0.0f), dA1 = dA0;
   {
     float f[kStates];
     st.load(a.A, f);
+    reorder(f, x);
     A0 = pk2(f[0] * kLog2e, f[1] * kLog2e), A1 = pk2(f[2] * kLog2e, f[3] * kLog2e);
     const float* from = a.segments > 1 ? a.carry + part * slab
                         : (args.dh_out != nullptr ? args.dh_out + at.b * slab : nullptr);
     f[0] = f[1] = f[2] = f[3] = 0.0f;
     if (from != nullptr) st.load(from, f);
+    reorder(f, x);
     g0 = pk2(f[0], f[1]), g1 = pk2(f[2], f[3]);
   }
-  const bool there = cell_d < a.D;
-  const float bias = there && a.dt_bias != nullptr ? a.dt_bias[cell_d] : 0.0f;
-  const float skip = there && a.skip != nullptr ? a.skip[cell_d] : 0.0f;
-  const E* U = static_cast<const E*>(a.u);
-  const E* DT = static_cast<const E*>(a.dt);
-  const E* Z = static_cast<const E*>(a.z);
-  const E* DY = static_cast<const E*>(args.dy);
-  E* DU = static_cast<E*>(args.du);
-  E* DDT = static_cast<E*>(args.ddt);
-  E* DZ = static_cast<E*>(args.dz);
-  const int64_t row0 = static_cast<int64_t>(at.b) * a.T;
-  float dskip = 0.0f, dbias = 0.0f;
-  const int live = min(at.k1, (n + kTile - 1) / kTile);
-
-  for (int k = max(at.k0, live); k < at.k1; ++k)  // tiles without a token
-    for (int i = 0; i < G::kItems; ++i) {
-      const int cell = tid + i * kThreads, t = k * kTile + cell / G::CB;
-      if (cell < G::kCells && t < a.T && there) {
-        const int64_t o = (row0 + t) * a.D + cell_d;
-        DU[o] = DDT[o] = store_from_float<E>(0.0f);
-        if (DZ != nullptr) DZ[o] = store_from_float<E>(0.0f);
-      }
-    }
-
-  float ru[G::kItems], rdt[G::kItems], rz[G::kItems], rdy[G::kItems], rmark[kStates];
-  PairTile<E, L> pt;
-  auto load = [&](int k) {
-    st.load(args.marks + (static_cast<int64_t>(at.b) * at.tiles + k) * slab, rmark);
+  float bias[W], skip[W], dskip[W], dbias[W];
 #pragma unroll
-    for (int i = 0; i < G::kItems; ++i) {
-      const int cell = tid + i * kThreads, t = k * kTile + cell / G::CB;
-      ru[i] = rdt[i] = rz[i] = rdy[i] = 0.0f;
-      if (cell < G::kCells && t < n && there) {
-        ru[i] = load_as_float(U + (row0 + t) * a.D + cell_d);
-        rdt[i] = load_as_float(DT + (row0 + t) * a.D + cell_d);
-        rdy[i] = load_as_float(DY + (row0 + t) * a.D + cell_d);
-        if (Z != nullptr) rz[i] = load_as_float(Z + (row0 + t) * a.ldz + cell_d);
+  for (int j = 0; j < W; ++j) {
+    const bool there = cell_d + j < a.D;
+    bias[j] = there && a.dt_bias != nullptr ? a.dt_bias[cell_d + j] : 0.0f;
+    skip[j] = there && a.skip != nullptr ? a.skip[cell_d + j] : 0.0f;
+    dskip[j] = dbias[j] = 0.0f;
+  }
+  {
+    const float zero[W] = {};
+    for (int t = max(at.k0, live) * kTile + cell_t; t < min(at.k1 * kTile, a.T); t += kStep) {
+      store_cells<E, W, ALIGNED>(DU + (row0 + t) * a.D, cell_d, a.D, zero);  // without a token
+      store_cells<E, W, ALIGNED>(DDT + (row0 + t) * a.D, cell_d, a.D, zero);
+      if (gated) store_cells<E, W, ALIGNED>(DZ + (row0 + t) * a.D, cell_d, a.D, zero);
+    }
+  }
+  // dB and dC of the block's channels and tile k: [block of channels][b][t][B | C][N]
+  auto put_pairs = [&](int k) {
+    float* out = args.pairs + (static_cast<int64_t>(at.cb) * a.B * a.T + row0) * 2 * a.N;
+#pragma unroll
+    for (int i = 0; i < G::kQuadItems; ++i) {
+      const int q = tid + i * kThreads, s = q % L * 4, which = q / L % 2, tl = q / (2 * L);
+      const int t = k * kTile + tl;
+      if ((G::kQuads % kThreads != 0 && q >= G::kQuads) || t >= n || s >= a.N) continue;
+      float sum[4] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = reinterpret_cast<const float4*>(sm.states[w][tl])[(which * G::NP + s) / 4];
+        sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+      }
+      float* o = out + (static_cast<int64_t>(t) * 2 + which) * a.N + s;
+      if (a.N % 4 == 0 && a.vec) {
+        *reinterpret_cast<float4*>(o) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (s + j < a.N) o[j] = sum[j];
       }
     }
-    pt.load(a, at.b, k * kTile, n);
   };
-  if (at.k0 < live) load(live - 1);
   for (int k = live - 1; k >= at.k0; --k) {
-    float u[G::kItems], raw[G::kItems], z[G::kItems], dy[G::kItems];
+    copy_wait<0>();
+    __syncthreads();
+    if (k + 1 < live) put_pairs(k + 1);
+    float u[G::kItems][W], raw[G::kItems][W], z[G::kItems][W], dy[G::kItems][W];
 #pragma unroll
     for (int i = 0; i < G::kItems; ++i) {
-      const int cell = tid + i * kThreads, t = k * kTile + cell / G::CB;
-      u[i] = ru[i], z[i] = rz[i], dy[i] = rdy[i], raw[i] = rdt[i] + bias;
-      float delta = a.softplus ? softplus(raw[i]) : raw[i], v = dy[i];
-      if (t >= n || !there) delta = 0.0f;
-      if (Z != nullptr) v *= z[i] * sigmoid(z[i]);
-      if (cell < G::kCells) {
-        sm.cells[cell / G::CB][cell_ch] = make_float4(delta, delta, delta * u[i], delta * u[i]);
-        sm.v[cell / G::CB][cell_ch] = make_float2(v, v);
+      const int t = cell_t + i * kStep;
+      if (G::kCells % 32 != 0 && t >= kTile) break;
+      const int c = warp * G::CW + cell_c;
+      float delta[W];
+      Tiles::get(sm.raw, 0, t, c, u[i]);
+      Tiles::get(sm.raw, 1, t, c, raw[i]);
+      if (gated) Tiles::get(sm.raw, 2, t, c, z[i]);
+      Tiles::get(sm.raw, 3, t, c, dy[i]);
+#pragma unroll
+      for (int j = 0; j < W; ++j) delta[j] = raw[i][j];
+      steps<W>(delta, bias, a.softplus, k * kTile + t < n);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const float du = delta[j] * u[i][j];
+        const float v = gated ? dy[i][j] * z[i][j] * sigmoid(z[i][j]) : dy[i][j];
+        sm.cells[warp][t][cell_c + j] = make_float4(delta[j], du, v, v);
       }
     }
-    pt.put(&sm.pairs[0][0][0]);
-    uint64_t h[kTile + 1][2], decay[kTile][2];
-    h[0][0] = pk2(rmark[0], rmark[1]), h[0][1] = pk2(rmark[2], rmark[3]);
+    Tiles::pairs_to_float(sm.raw, a.N, sm.pairs);
+    reorder(rmark, x);
+    uint64_t h0 = pk2(rmark[0], rmark[1]), h1 = pk2(rmark[2], rmark[3]);
     __syncthreads();
-    if (k > at.k0) load(k - 1);
+    if (k > at.k0) begin(k - 1);
+    uint64_t decay[kTile][2];
+    Decays decays;
 #pragma unroll
     for (int g = 0; g < kTile; g += 4) {
       float y[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = g + i;
-        const ulonglong2 c = reinterpret_cast<const ulonglong2&>(sm.cells[t][mine]);
-        const ulonglong2 Bv = reinterpret_cast<const ulonglong2&>(sm.pairs[t][0][kStates * l]);
+        const float2 half = reinterpret_cast<const float2&>(sm.cells[warp][t][mine]);
+        const ulonglong2 c = make_ulonglong2(pk2(half.x, half.x), pk2(half.y, half.y));
+        const ulonglong2 Bv =
+            reinterpret_cast<const ulonglong2&>(sm.pairs[t][0][order][kStates * l]);
+        reinterpret_cast<ulonglong2&>(sm.states[warp][t][lane]) = make_ulonglong2(h0, h1);
         decay[t][0] = exp2_pair(fmul2(c.x, A0)), decay[t][1] = exp2_pair(fmul2(c.x, A1));
-        h[t + 1][0] = ffma2(decay[t][0], h[t][0], fmul2(c.y, Bv.x));
-        h[t + 1][1] = ffma2(decay[t][1], h[t][1], fmul2(c.y, Bv.y));
-        if (Z != nullptr) {
-          const ulonglong2 Cv = reinterpret_cast<const ulonglong2&>(sm.pairs[t][1][kStates * l]);
-          y[i] = sum2(ffma2(h[t + 1][1], Cv.y, fmul2(h[t + 1][0], Cv.x)));
+        h0 = ffma2(decay[t][0], h0, fmul2(c.y, Bv.x));
+        h1 = ffma2(decay[t][1], h1, fmul2(c.y, Bv.y));
+        decays.add(decay[t][0], decay[t][1], c.x);
+        if (gated) {
+          const ulonglong2 Cv =
+              reinterpret_cast<const ulonglong2&>(sm.pairs[t][1][order][kStates * l]);
+          y[i] = sum2(ffma2(h1, Cv.y, fmul2(h0, Cv.x)));
         }
       }
-      if (Z != nullptr) {
-        using M = Meet<4, 1, L / 2>;
+      if (gated) {
+        using M = Meet<4, G::CW, 16>;
         M::sum(y, lane);
         if (M::first(lane))
 #pragma unroll
-          for (int i = 0; i < M::kLeft; ++i) sm.sums[2][g + M::index(lane) + i][mine] = y[i];
+          for (int i = 0; i < M::kLeft; ++i) sm.sums[warp][2][g + M::index(lane) + i][mine] = y[i];
       }
     }
 #pragma unroll
     for (int g = kTile - 4; g >= 0; g -= 4) {
-      float s[8];  // of dh B, then of w A, of four tokens
+      float s[8], p[4][8];  // s: of dh B, then of w A, of four tokens
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
         const int t = g + i;
-        const ulonglong2 c = reinterpret_cast<const ulonglong2&>(sm.cells[t][mine]);
-        const uint64_t v = reinterpret_cast<const uint64_t&>(sm.v[t][mine]);
-        const ulonglong2 Bv = reinterpret_cast<const ulonglong2&>(sm.pairs[t][0][kStates * l]);
-        const ulonglong2 Cv = reinterpret_cast<const ulonglong2&>(sm.pairs[t][1][kStates * l]);
+        const float4 cell = sm.cells[warp][t][mine];
+        const ulonglong2 c = make_ulonglong2(pk2(cell.x, cell.x), pk2(cell.y, cell.y));
+        const uint64_t v = pk2(cell.z, cell.w);
+        const ulonglong2 Bv =
+            reinterpret_cast<const ulonglong2&>(sm.pairs[t][0][order][kStates * l]);
+        const ulonglong2 Cv =
+            reinterpret_cast<const ulonglong2&>(sm.pairs[t][1][order][kStates * l]);
+        const ulonglong2 before = reinterpret_cast<const ulonglong2&>(sm.states[warp][t][lane]);
         const uint64_t dh0 = ffma2(v, Cv.x, g0), dh1 = ffma2(v, Cv.y, g1);
         g0 = fmul2(decay[t][0], dh0), g1 = fmul2(decay[t][1], dh1);
-        const uint64_t w0 = fmul2(g0, h[t][0]), w1 = fmul2(g1, h[t][1]);
+        const uint64_t w0 = fmul2(g0, before.x), w1 = fmul2(g1, before.y);
         dA0 = ffma2(w0, c.x, dA0), dA1 = ffma2(w1, c.x, dA1);
         s[i] = sum2(ffma2(dh1, Bv.y, fmul2(dh0, Bv.x)));
         s[4 + i] = sum2(ffma2(w1, A1, fmul2(w0, A0)));
-        float p[8];  // the lane's dB, then dC, of its channel
-        upk2(fmul2(c.y, dh0), p[0], p[1]);
-        upk2(fmul2(c.y, dh1), p[2], p[3]);
-        upk2(fmul2(v, h[t + 1][0]), p[4], p[5]);
-        upk2(fmul2(v, h[t + 1][1]), p[6], p[7]);
-        using M = Meet<8, L, 16>;
-        M::sum(p, lane);
-        if (M::first(lane))
-#pragma unroll
-          for (int q = 0; q < M::kLeft; ++q) {
-            const int k8 = M::index(lane) + q;
-            sm.by_warp[warp][t][k8 / 4][kStates * l + k8 % 4] = p[q];
-          }
+        sum_channels<L>(fmul2(c.y, dh0), fmul2(c.y, dh1), fmul2(v, h0), fmul2(v, h1), lane, p[i]);
+        h0 = before.x, h1 = before.y;
       }
-      using M = Meet<8, 1, L / 2>;
+      using M = Meet<8, G::CW, 16>;
       M::sum(s, lane);
       if (M::first(lane))
 #pragma unroll
         for (int q = 0; q < M::kLeft; ++q) {
           const int k8 = M::index(lane) + q;
-          sm.sums[k8 / 4][g + k8 % 4][mine] = s[q];
+          sm.sums[warp][k8 / 4][g + k8 % 4][mine] = s[q];
         }
+      __syncwarp();  // (the group's states have been read)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        put_channels<L>(p[i], lane, x, reinterpret_cast<float*>(sm.states[warp][g + i]));
     }
-    __syncthreads();
+    decays.put_right(A0, A1, g0, g1);
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < G::kItems; ++i) {
-      const int cell = tid + i * kThreads, tl = cell / G::CB, t = k * kTile + tl;
-      if (cell >= G::kCells || t >= a.T || !there) continue;
-      const float delta = sm.cells[tl][cell_ch].x, v = sm.v[tl][cell_ch].x;
-      const float sB = sm.sums[0][tl][cell_ch], sA = sm.sums[1][tl][cell_ch] * kLn2;
-      const float du = fmaf(delta, sB, skip * v);
-      float ddt = fmaf(u[i], sB, sA);
-      if (a.softplus) ddt *= sigmoid(raw[i]);
-      const int64_t o = (row0 + t) * a.D + cell_d;
+      const int tl = cell_t + i * kStep, t = k * kTile + tl;
+      if (G::kCells % 32 != 0 && tl >= kTile) break;
+      float sB[W], sA[W], du[W], ddt[W], dz[W];
+      Vec<float, W> r;
+      r.load(&sm.sums[warp][0][tl][cell_c]);
+      r.get(sB);
+      r.load(&sm.sums[warp][1][tl][cell_c]);
+      r.get(sA);
+      if (gated) {
+        r.load(&sm.sums[warp][2][tl][cell_c]);
+        r.get(dz);
+      }
       const bool real = t < n;
-      DU[o] = store_from_float<E>(real ? du : 0.0f);
-      DDT[o] = store_from_float<E>(real ? ddt : 0.0f);
-      if (Z != nullptr) {
-        const float y0 = fmaf(skip, u[i], sm.sums[2][tl][cell_ch]), sg = sigmoid(z[i]);
-        const float dz = dy[i] * y0 * fmaf(z[i] * sg, 1.0f - sg, sg);
-        DZ[o] = store_from_float<E>(real ? dz : 0.0f);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const float4 cell = sm.cells[warp][tl][cell_c + j];
+        const float delta = cell.x, v = cell.z;
+        du[j] = fmaf(delta, sB[j], skip[j] * v);
+        ddt[j] = fmaf(u[i][j], sB[j], sA[j] * kLn2);
+        if (a.softplus) ddt[j] *= sigmoid(raw[i][j] + bias[j]);
+        if (gated) {
+          const float y0 = fmaf(skip[j], u[i][j], dz[j]), sg = sigmoid(z[i][j]);
+          dz[j] = dy[i][j] * y0 * fmaf(z[i][j] * sg, 1.0f - sg, sg);
+        }
+        if (!real) du[j] = ddt[j] = dz[j] = 0.0f;
+        dskip[j] = fmaf(v, u[i][j], dskip[j]);  // (zeros where there is no token)
+        dbias[j] += ddt[j];
       }
-      if (real) {
-        dskip = fmaf(v, u[i], dskip);
-        dbias += ddt;
+      if (t < a.T) {
+        store_cells<E, W, ALIGNED>(DU + (row0 + t) * a.D, cell_d, a.D, du);
+        store_cells<E, W, ALIGNED>(DDT + (row0 + t) * a.D, cell_d, a.D, ddt);
+        if (gated) store_cells<E, W, ALIGNED>(DZ + (row0 + t) * a.D, cell_d, a.D, dz);
       }
     }
-    // dB and dC of the block's channels: [block of channels][b][t][B | C][N]
-    float* out = args.pairs + (static_cast<int64_t>(at.cb) * a.B * a.T + row0) * 2 * a.N;
-#pragma unroll
-    for (int i = 0; i < G::kPairItems; ++i) {
-      const int q = tid + i * kThreads, s = q % G::NP, which = q / G::NP % 2;
-      const int tl = q / (2 * G::NP), t = k * kTile + tl;
-      if (s >= a.N || t >= n) continue;
-      float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += sm.by_warp[w][tl][which][s];
-      out[(static_cast<int64_t>(t) * 2 + which) * a.N + s] = sum;
-    }
-    __syncthreads();  // (the next tile's cells take this one's place)
+    if (k > at.k0) tiles.end(sm.raw);
   }
-  if (args.dh0 != nullptr && at.seg == 0) st.store(args.dh0 + at.b * slab, g0, g1);
-  st.store(args.params + part * slab, dA0, dA1);
-  float* all = &sm.sums[0][0][0];
-  all[tid] = dskip;
-  all[kThreads + tid] = dbias;
-  __syncthreads();
-  if (tid < G::CB && there) {
-    for (int i = tid + G::CB; i < kThreads; i += G::CB) dskip += all[i], dbias += all[kThreads + i];
-    args.channels[part * 2 * a.D + cell_d] = dskip;
-    args.channels[(part * 2 + 1) * a.D + cell_d] = dbias;
+  if (at.k0 < live) {
+    __syncthreads();
+    put_pairs(at.k0);
+  }
+  float f[kStates];
+  if (args.dh0 != nullptr && at.seg == 0) {
+    upk2(g0, f[0], f[1]);
+    upk2(g1, f[2], f[3]);
+    reorder(f, x);
+    st.store(args.dh0 + at.b * slab, pk2(f[0], f[1]), pk2(f[2], f[3]));
+  }
+  upk2(dA0, f[0], f[1]);
+  upk2(dA1, f[2], f[3]);
+  reorder(f, x);
+  st.store(args.params + part * slab, pk2(f[0], f[1]), pk2(f[2], f[3]));
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+#pragma unroll
+    for (int bit = kPer; bit < 32; bit *= 2) {
+      dskip[j] += __shfl_xor_sync(0xffffffffu, dskip[j], bit);
+      dbias[j] += __shfl_xor_sync(0xffffffffu, dbias[j], bit);
+    }
+    if (cell_t == 0 && cell_d + j < a.D) {
+      args.channels[part * 2 * a.D + cell_d + j] = dskip[j];
+      args.channels[(part * 2 + 1) * a.D + cell_d + j] = dbias[j];
+    }
   }
 }
 
@@ -338,17 +485,19 @@ __global__ void __launch_bounds__(256) selective_params_kernel(SelectiveBwdArgs 
     (d < a.D ? args.dskip : args.ddt_bias - a.D)[d] = sum;
 }
 
-template <typename E, int L>
-cudaError_t bwd(const SelectiveBwdArgs& args, cudaStream_t st) {
+template <typename E, int L, bool ALIGNED>
+cudaError_t bwd_of(const SelectiveBwdArgs& args, cudaStream_t st) {
   const SelectiveArgs& a = args.f;
   const int64_t blocks = static_cast<int64_t>(a.B) * a.blocks * a.segments;
   cudaError_t e;
   if (a.segments > 1) {
-    e = launch(selective_bwd_state_kernel<E, L>, blocks, kThreads, 0, st, args);
+    e = launch(selective_bwd_state_kernel<E, L, ALIGNED>, blocks, kThreads,
+               sizeof(BwdStateShared<E, L, ALIGNED>), st, args);
     if (e == cudaSuccess) e = launch_carry(a, args.dh_out, true, st);
     if (e != cudaSuccess) return e;
   }
-  e = launch(selective_bwd_kernel<E, L>, blocks, kThreads, sizeof(Shared<L>), st, args);
+  e = launch(selective_bwd_kernel<E, L, ALIGNED>, blocks, kThreads,
+             sizeof(BwdShared<E, L, ALIGNED>), st, args);
   const int64_t pairs = static_cast<int64_t>(a.B) * a.T * 2 * a.N;
   if (e == cudaSuccess && pairs > 0)
     e = launch(selective_pairs_kernel<E>, (pairs - 1) / 256 + 1, 256, 0, st, args);
@@ -356,6 +505,11 @@ cudaError_t bwd(const SelectiveBwdArgs& args, cudaStream_t st) {
   if (e == cudaSuccess)
     e = launch(selective_params_kernel, (params - 1) / 256 + 1, 256, 0, st, args);
   return e;
+}
+template <typename E, int L>
+cudaError_t bwd(const SelectiveBwdArgs& args, cudaStream_t st) {
+  return words<E>(args.f, {args.dy, args.du, args.ddt, args.dz}) ? bwd_of<E, L, true>(args, st)
+                                                                : bwd_of<E, L, false>(args, st);
 }
 
 struct Sizes {
@@ -374,8 +528,7 @@ Sizes sizes(int B, int T, int D, int N, int segments) {
 size_t selective_scan_bwd_workspace_bytes(int B, int T, int D, int N) {
   if (B <= 0 || T < 0 || D <= 0 || N <= 0) return 0;
   int tiles;
-  const Sizes s =
-      sizes(B, T, D, N, selective_segments(B, T, D, N, kSelectiveBwdBlocks, &tiles));
+  const Sizes s = sizes(B, T, D, N, selective_segments(B, T, D, N, &tiles));
   return sizeof(float) * (s.pairs + s.params + s.channels + s.carry + s.sums);
 }
 
@@ -390,7 +543,7 @@ cudaError_t selective_scan_bwd_launch(SelectiveBwdArgs args, void* workspace, cu
     return e;
   }
   a.blocks = selective_blocks(a.D, a.N);
-  a.segments = selective_segments(a.B, a.T, a.D, a.N, kSelectiveBwdBlocks, &a.tiles_per_segment);
+  a.segments = selective_segments(a.B, a.T, a.D, a.N, &a.tiles_per_segment);
   const Sizes s = sizes(a.B, a.T, a.D, a.N, a.segments);
   args.pairs = static_cast<float*>(workspace);
   args.params = args.pairs + s.pairs;

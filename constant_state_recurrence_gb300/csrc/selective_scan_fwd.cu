@@ -4,22 +4,48 @@
 namespace sanatan {
 namespace {
 
+template <typename E, int L, bool ALIGNED, bool STATE>
+struct FwdShared {
+  using G = Geo<L>;
+  using Tiles = Stage<E, L, ALIGNED, STATE ? 2 : 3>;  // u, dt, z
+  float4 cells[kWarps][kTile][G::kRowPitch];          // delta, delta, delta u, delta u
+  float pairs[2][kTile][2][1][G::NP];
+  float ys[kWarps][kTile][G::CW];
+  char raw[3][Tiles::kBytes];
+};
+
 // STATE: only the segment's result from a zero state, and its sum of delta.
-template <typename E, int L, bool STATE>
+template <typename E, int L, bool ALIGNED, bool STATE>
 __global__ void __launch_bounds__(kThreads) selective_fwd_kernel(SelectiveArgs a) {
   using G = Geo<L>;
-  __shared__ float4 cells[kTile][G::CB];  // delta, delta, delta u, delta u
-  __shared__ __align__(16) float pairs[kTile][2][G::NP];
-  __shared__ float ys[kTile][G::kPitch];
-  Place<L> at(a);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, l = lane % L;
-  const int mine = warp * G::CW + lane / L;  // the lane's channel of the block
-  const int d0 = at.cb * G::CB, d = d0 + mine;
-  const int cell_ch = tid % G::CB, cell_d = d0 + cell_ch;  // the thread's in every cell of its
+  constexpr int W = G::W;
+  using Sm = FwdShared<E, L, ALIGNED, STATE>;
+  using Tiles = typename Sm::Tiles;
+  extern __shared__ float4 smem4[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem4);
+  const Place<L> at(a);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, l = lane / G::CW;
+  const int mine = lane % G::CW;
+  const int d0 = at.cb * G::CB, w0 = d0 + warp * G::CW, d = w0 + mine;
+  // The lane's cells: W channels from cell_c of the warp's, tokens cell_t, cell_t + ...
+  constexpr int kPer = G::CW / W, kStep = 32 / kPer;
+  const int cell_c = lane % kPer * W, cell_t = lane / kPer, cell_d = w0 + cell_c;
   const StatePlace st(d, l, a.D, a.N, a.vec);
   wait_for_previous();
   const int n = length_of(a.lens, at.b, a.T);
-  const int64_t slab = static_cast<int64_t>(a.D) * a.N;
+  const int64_t slab = static_cast<int64_t>(a.D) * a.N, row0 = static_cast<int64_t>(at.b) * a.T;
+  E* Y = static_cast<E*>(a.y);
+  const bool gated = !STATE && a.z != nullptr;
+  const int live = min(at.k1, (n + kTile - 1) / kTile);  // tiles from here on hold no token
+  Tiles tiles;
+  if constexpr (STATE)
+    tiles.init({a.u, a.dt, a.Bm, nullptr}, {a.D, a.D, a.ldb, 0}, a, row0, n, d0, at.k0, 1);
+  else
+    tiles.init({a.u, a.dt, a.z, a.Bm, a.Cm}, {a.D, a.D, a.ldz, a.ldb, a.ldc}, a, row0, n, d0,
+               at.k0, 1);
+  // Tile k is worked on while B and C of tile k + 1 become floats and tile k + 2 is under way.
+  if (at.k0 < live) tiles.begin(sm.raw[0], at.k0), tiles.end(sm.raw[0]);
+  if (at.k0 + 1 < live) tiles.begin(sm.raw[1], at.k0 + 1), tiles.end(sm.raw[1]);
   uint64_t A0, A1, h0, h1;
   {
     float f[kStates];
@@ -33,102 +59,109 @@ __global__ void __launch_bounds__(kThreads) selective_fwd_kernel(SelectiveArgs a
     if (from != nullptr) st.load(from, f);
     h0 = pk2(f[0], f[1]), h1 = pk2(f[2], f[3]);
   }
-  const bool there = cell_d < a.D;
-  const float bias = there && a.dt_bias != nullptr ? a.dt_bias[cell_d] : 0.0f;
-  const float skip = !STATE && there && a.skip != nullptr ? a.skip[cell_d] : 0.0f;
-  const E* U = static_cast<const E*>(a.u);
-  const E* DT = static_cast<const E*>(a.dt);
-  const E* Z = static_cast<const E*>(a.z);
-  E* Y = static_cast<E*>(a.y);
-  const int64_t row0 = static_cast<int64_t>(at.b) * a.T;
-  float sum = 0.0f;
-
-  float ru[G::kItems], rdt[G::kItems], rz[G::kItems];
-  PairTile<E, L> pt;
-  auto load = [&](int k) {
+  float bias[W], skip[W], sum[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    const bool there = cell_d + j < a.D;
+    bias[j] = there && a.dt_bias != nullptr ? a.dt_bias[cell_d + j] : 0.0f;
+    skip[j] = there && a.skip != nullptr ? a.skip[cell_d + j] : 0.0f;
+    sum[j] = 0.0f;
+  }
+  if (at.k0 < live) {
+    copy_wait<0>();
+    __syncthreads();
+    Tiles::pairs_to_float(sm.raw[0], a.N, sm.pairs[at.k0 & 1]);
+  }
+  int now = 0;  // the buffer of tile k
+  for (int k = at.k0; k < live; ++k) {
+    const int next = now == 2 ? 0 : now + 1, after = next == 2 ? 0 : next + 1;
+    copy_wait<0>();
+    __syncthreads();
+    if (k + 2 < live) tiles.begin(sm.raw[after], k + 2);
+    if (k + 1 < live) Tiles::pairs_to_float(sm.raw[next], a.N, sm.pairs[(k + 1) & 1]);
+    float u[G::kItems][W], z[G::kItems][W];
 #pragma unroll
     for (int i = 0; i < G::kItems; ++i) {
-      const int cell = tid + i * kThreads, t = k * kTile + cell / G::CB;
-      ru[i] = rdt[i] = rz[i] = 0.0f;
-      if (cell < G::kCells && t < n && there) {
-        ru[i] = load_as_float(U + (row0 + t) * a.D + cell_d);
-        rdt[i] = load_as_float(DT + (row0 + t) * a.D + cell_d);
-        if (!STATE && Z != nullptr) rz[i] = load_as_float(Z + (row0 + t) * a.ldz + cell_d);
+      const int t = cell_t + i * kStep;
+      if (G::kCells % 32 != 0 && t >= kTile) break;
+      float delta[W];
+      Tiles::get(sm.raw[now], 0, t, warp * G::CW + cell_c, u[i]);
+      Tiles::get(sm.raw[now], 1, t, warp * G::CW + cell_c, delta);
+      if (gated) Tiles::get(sm.raw[now], 2, t, warp * G::CW + cell_c, z[i]);
+      steps<W>(delta, bias, a.softplus, k * kTile + t < n);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        if (STATE) sum[j] += delta[j];
+        const float du = delta[j] * u[i][j];
+        sm.cells[warp][t][cell_c + j] = make_float4(delta[j], delta[j], du, du);
       }
     }
-    pt.load(a, at.b, k * kTile, n);
-  };
-  const int live = min(at.k1, (n + kTile - 1) / kTile);  // tiles from here on hold no token
-  if (at.k0 < live) load(at.k0);
-  for (int k = at.k0; k < live; ++k) {
-    float u[G::kItems], z[G::kItems];
-#pragma unroll
-    for (int i = 0; i < G::kItems; ++i) {
-      const int cell = tid + i * kThreads, t = k * kTile + cell / G::CB;
-      u[i] = ru[i], z[i] = rz[i];
-      float delta = rdt[i] + bias;
-      if (a.softplus) delta = softplus(delta);
-      if (t >= n || !there) delta = 0.0f;  // (a = 1 and no input: the state passes)
-      if (STATE) sum += cell < G::kCells ? delta : 0.0f;
-      if (cell < G::kCells)
-        cells[cell / G::CB][cell_ch] = make_float4(delta, delta, delta * u[i], delta * u[i]);
-    }
-    pt.put(&pairs[0][0][0]);
-    __syncthreads();
-    if (k + 1 < live) load(k + 1);
     if (!STATE && a.marks != nullptr)
       st.store(a.marks + (static_cast<int64_t>(at.b) * at.tiles + k) * slab, h0, h1);
+    __syncwarp();
+    const float(*pairs)[2][1][G::NP] = sm.pairs[k & 1];
+    Decays decays;
 #pragma unroll
     for (int g = 0; g < kTile; g += 4) {
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const ulonglong2 c = reinterpret_cast<const ulonglong2&>(cells[g + i][mine]);
-        const ulonglong2 Bv = reinterpret_cast<const ulonglong2&>(pairs[g + i][0][kStates * l]);
-        h0 = ffma2(exp2_pair(fmul2(c.x, A0)), h0, fmul2(c.y, Bv.x));
-        h1 = ffma2(exp2_pair(fmul2(c.x, A1)), h1, fmul2(c.y, Bv.y));
+        const ulonglong2 c = reinterpret_cast<const ulonglong2&>(sm.cells[warp][g + i][mine]);
+        const ulonglong2 Bv = reinterpret_cast<const ulonglong2&>(pairs[g + i][0][0][kStates * l]);
+        const uint64_t a0 = exp2_pair(fmul2(c.x, A0)), a1 = exp2_pair(fmul2(c.x, A1));
+        h0 = ffma2(a0, h0, fmul2(c.y, Bv.x));
+        h1 = ffma2(a1, h1, fmul2(c.y, Bv.y));
+        decays.add(a0, a1, c.x);
         if (!STATE) {
-          const ulonglong2 Cv = reinterpret_cast<const ulonglong2&>(pairs[g + i][1][kStates * l]);
+          const ulonglong2 Cv = reinterpret_cast<const ulonglong2&>(pairs[g + i][1][0][kStates * l]);
           v[i] = sum2(ffma2(h1, Cv.y, fmul2(h0, Cv.x)));
         }
       }
       if (!STATE) {
-        using M = Meet<4, 1, L / 2>;
+        using M = Meet<4, G::CW, 16>;
         M::sum(v, lane);
         if (M::first(lane))
 #pragma unroll
-          for (int i = 0; i < M::kLeft; ++i) ys[g + M::index(lane) + i][mine] = v[i];
+          for (int i = 0; i < M::kLeft; ++i) sm.ys[warp][g + M::index(lane) + i][mine] = v[i];
       }
     }
-    __syncthreads();
-    if (!STATE)
+    decays.put_right(A0, A1, h0, h1);
+    __syncwarp();
+    if (!STATE) {
 #pragma unroll
       for (int i = 0; i < G::kItems; ++i) {
-        const int cell = tid + i * kThreads, tl = cell / G::CB, t = k * kTile + tl;
-        if (cell >= G::kCells || t >= a.T || !there) continue;
-        float y = fmaf(skip, u[i], ys[tl][cell_ch]);
-        if (Z != nullptr) y *= __fdividef(z[i], 1.0f + __expf(-z[i]));
-        Y[(row0 + t) * a.D + cell_d] = store_from_float<E>(t < n ? y : 0.0f);
+        const int tl = cell_t + i * kStep, t = k * kTile + tl;
+        if (G::kCells % 32 != 0 && tl >= kTile) break;
+        float y[W];
+        Vec<float, W> v;
+        v.load(&sm.ys[warp][tl][cell_c]);
+        v.get(y);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          y[j] = fmaf(skip[j], u[i][j], y[j]);
+          if (gated) y[j] *= z[i][j] * sigmoid(z[i][j]);
+          if (t >= n) y[j] = 0.0f;
+        }
+        if (t < a.T) store_cells<E, W, ALIGNED>(Y + (row0 + t) * a.D, cell_d, a.D, y);
       }
+    }
+    if (k + 2 < live) tiles.end(sm.raw[after]);
+    now = next;
   }
   if constexpr (STATE) {
     st.store(a.carry + (static_cast<int64_t>(at.b) * a.segments + at.seg) * slab, h0, h1);
-    // the threads of a channel, in order
-    __syncthreads();
-    float* all = &ys[0][0];
-    all[tid] = sum;
-    __syncthreads();
-    if (tid < G::CB && there) {
-      for (int i = tid + G::CB; i < kThreads; i += G::CB) sum += all[i];
-      a.sums[(static_cast<int64_t>(at.b) * a.segments + at.seg) * a.D + cell_d] = sum;
+    // the lanes of a channel, by halves
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+#pragma unroll
+      for (int bit = kPer; bit < 32; bit *= 2) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], bit);
+      if (cell_t == 0 && cell_d + j < a.D)
+        a.sums[(static_cast<int64_t>(at.b) * a.segments + at.seg) * a.D + cell_d + j] = sum[j];
     }
   } else {
-    for (int k = max(at.k0, live); k < at.k1; ++k)  // tiles without a token
-      for (int i = 0; i < G::kItems; ++i) {
-        const int cell = tid + i * kThreads, t = k * kTile + cell / G::CB;
-        if (cell < G::kCells && t < a.T && there)
-          Y[(row0 + t) * a.D + cell_d] = store_from_float<E>(0.0f);
-      }
+    const float zero[W] = {};
+    for (int t = max(at.k0, live) * kTile + cell_t; t < min(at.k1 * kTile, a.T); t += kStep)
+      store_cells<E, W, ALIGNED>(Y + (row0 + t) * a.D, cell_d, a.D, zero);  // without a token
     if (a.h_out != nullptr && at.seg == a.segments - 1) st.store(a.h_out + at.b * slab, h0, h1);
   }
 }
@@ -163,11 +196,11 @@ __global__ void __launch_bounds__(kThreads) selective_step_kernel(SelectiveArgs 
       delta = load_as_float(static_cast<const E*>(a.dt) + static_cast<int64_t>(b) * a.D + d) + bias;
       if (a.z != nullptr) z = load_as_float(static_cast<const E*>(a.z) + b * a.ldz + d);
     }
-    if (a.softplus) delta = softplus(delta);
-    float y = 0.0f, decay[kStates];
-    const uint64_t x = pk2(delta * kLog2e, delta * kLog2e);
-    upk2(exp2_pair(fmul2(x, pk2(A[0], A[1]))), decay[0], decay[1]);
-    upk2(exp2_pair(fmul2(x, pk2(A[2], A[3]))), decay[2], decay[3]);
+    if (a.softplus) {
+      float other;
+      upk2(softplus_pair(pk2(delta, delta)), delta, other);
+    }
+    float y = 0.0f;
 #pragma unroll
     for (int j = 0; j < kStates; ++j) {
       const int n = kStates * l + j;
@@ -176,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) selective_step_kernel(SelectiveArgs 
         Bv = load_as_float(static_cast<const E*>(a.Bm) + b * a.ldb + n);
         Cv = load_as_float(static_cast<const E*>(a.Cm) + b * a.ldc + n);
       }
-      h[r][j] = fmaf(decay[j], h[r][j], delta * u * Bv);
+      h[r][j] = fmaf(exp2_near(delta * kLog2e * A[j]), h[r][j], delta * u * Bv);
       y = fmaf(h[r][j], Cv, y);
     }
     st.store(a.h_out + b * slab, pk2(h[r][0], h[r][1]), pk2(h[r][2], h[r][3]));
@@ -189,15 +222,22 @@ __global__ void __launch_bounds__(kThreads) selective_step_kernel(SelectiveArgs 
   }
 }
 
-template <typename E, int L>
-cudaError_t fwd(SelectiveArgs a, cudaStream_t st) {
+template <typename E, int L, bool ALIGNED>
+cudaError_t fwd_of(const SelectiveArgs& a, cudaStream_t st) {
   const int64_t blocks = static_cast<int64_t>(a.B) * a.blocks * a.segments;
-  if (a.segments > 1) {
-    cudaError_t e = launch(selective_fwd_kernel<E, L, true>, blocks, kThreads, 0, st, a);
+    if (a.segments > 1) {
+    cudaError_t e =
+        launch(selective_fwd_kernel<E, L, ALIGNED, true>, blocks, kThreads,
+               sizeof(FwdShared<E, L, ALIGNED, true>), st, a);
     if (e == cudaSuccess) e = launch_carry(a, a.h0, false, st);
     if (e != cudaSuccess) return e;
   }
-  return launch(selective_fwd_kernel<E, L, false>, blocks, kThreads, 0, st, a);
+  return launch(selective_fwd_kernel<E, L, ALIGNED, false>, blocks, kThreads,
+                sizeof(FwdShared<E, L, ALIGNED, false>), st, a);
+}
+template <typename E, int L>
+cudaError_t fwd(const SelectiveArgs& a, cudaStream_t st) {
+  return words<E>(a, {a.y}) ? fwd_of<E, L, true>(a, st) : fwd_of<E, L, false>(a, st);
 }
 
 template <typename E, int L>
@@ -216,14 +256,17 @@ int selective_lanes(int N) {
 
 int selective_blocks(int D, int N) { return (D - 1) / (kThreads / selective_lanes(N)) + 1; }
 
-// Segments of a sequence (and their tiles): one, unless the blocks of whole sequences leave
-// most SMs without the work that hides a walk's latency.
-int selective_segments(int B, int T, int D, int N, int per_sm, int* tiles_per_segment) {
+// Segments of a sequence, and their tiles.  One, where whole sequences make two blocks or more
+// an SM (a split walks the tokens twice; training shape, 384 blocks: forward 565 us, in eight
+// segments 606, backward 1466 and 1572); else about eight blocks an SM (one prompt of 32768
+// tokens, 48 blocks: forward 2800 us whole, 1293 in 8 segments, 675 in 24), of four tiles or
+// more.
+int selective_segments(int B, int T, int D, int N, int* tiles_per_segment) {
   const int tiles = std::max(1, (T - 1) / kTile + 1);
   const int64_t blocks = static_cast<int64_t>(B) * selective_blocks(D, N);
-  const int64_t slots = 152 * per_sm;
+  constexpr int64_t kSms = 152;
   int64_t S = 1;
-  if (blocks * 2 < slots) S = std::min<int64_t>((slots * 3 / 2 - 1) / blocks + 1, tiles / 4);
+  if (blocks < 2 * kSms) S = std::min<int64_t>((8 * kSms - 1) / blocks + 1, tiles / 4);
   S = std::max<int64_t>(S, 1);
   *tiles_per_segment = static_cast<int>((tiles - 1) / S + 1);
   return (tiles - 1) / *tiles_per_segment + 1;
@@ -232,13 +275,13 @@ int selective_segments(int B, int T, int D, int N, int per_sm, int* tiles_per_se
 size_t selective_scan_fwd_workspace_bytes(int B, int T, int D, int N) {
   if (B <= 0 || T <= 0 || D <= 0 || N <= 0) return 0;
   int tiles;
-  const int S = selective_segments(B, T, D, N, kSelectiveFwdBlocks, &tiles);
+  const int S = selective_segments(B, T, D, N, &tiles);
   return S == 1 ? 0 : sizeof(float) * static_cast<size_t>(B) * S * D * (N + 1);
 }
 
 cudaError_t selective_scan_fwd_launch(SelectiveArgs a, void* workspace, cudaStream_t st) {
   a.blocks = selective_blocks(a.D, a.N);
-  a.segments = selective_segments(a.B, a.T, a.D, a.N, kSelectiveFwdBlocks, &a.tiles_per_segment);
+  a.segments = selective_segments(a.B, a.T, a.D, a.N, &a.tiles_per_segment);
   a.carry = static_cast<float*>(workspace);
   if (a.segments > 1) a.sums = a.carry + static_cast<int64_t>(a.B) * a.segments * a.D * a.N;
   a.vec = state_words(a.N, {a.A, a.h0, a.h_out, a.marks, a.carry});
