@@ -11,7 +11,7 @@
 // and the single-token step.  States and all sums are float32.
 //
 // A block of four warps takes 128 / L channels of a stretch of tokens, L lanes a channel, four
-// states a lane (L = N / 4, up to a power of two); neighbouring lanes have neighbouring
+// states a lane (L = N / 4, up to a power of two, 4 at least); neighbouring lanes have neighbouring
 // channels, so that loads of B and C from shared memory, the same for both, are half as long.  In tiles of sixteen tokens the threads
 // form delta, delta u and v once for each token and channel and leave them in shared memory
 // with B and C; then each lane walks its four states through the tile.  Sums over the
@@ -343,13 +343,16 @@ struct Stage {
     if constexpr (ALIGNED) {
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
+        // (a place without a token reads nothing, and from no address outside the tensor)
+        const bool real = token[i] < left;
+        const void* source = real ? from[i] : reinterpret_cast<const char*>(x[0]);
         if (kChunk == 16) {
           if (i + 1 < kSlots || kChunks % kThreads == 0 || bytes[i] != 0)
-            copy_async(buffer + to[i], from[i], token[i] < left, 16);
+            copy_async(buffer + to[i], source, real, 16);
         } else if (bytes[i] == 16) {
-          copy_async(buffer + to[i], from[i], token[i] < left, 16);
+          copy_async(buffer + to[i], source, real, 16);
         } else if (bytes[i] != 0) {
-          copy_async(buffer + to[i], from[i], token[i] < left, kChunk);
+          copy_async(buffer + to[i], source, real, kChunk);
         }
         from[i] += step[i];
       }
@@ -545,10 +548,6 @@ inline bool state_words(int N, std::initializer_list<const void*> states) {
 // f<E, L> for the lanes of a channel (a: the forward's arguments, in scope).
 #define SANATAN_SELECTIVE_DISPATCH(f, E, args) \
   switch (selective_lanes(a.N)) {              \
-    case 1:                                    \
-      return f<E, 1>(args, st);                \
-    case 2:                                    \
-      return f<E, 2>(args, st);                \
     case 4:                                    \
       return f<E, 4>(args, st);                \
     case 8:                                    \

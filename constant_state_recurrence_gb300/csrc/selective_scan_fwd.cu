@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) selective_step_kernel(SelectiveArgs 
 template <typename E, int L, bool ALIGNED>
 cudaError_t fwd_of(const SelectiveArgs& a, cudaStream_t st) {
   const int64_t blocks = static_cast<int64_t>(a.B) * a.blocks * a.segments;
-    if (a.segments > 1) {
+  if (a.segments > 1) {
     cudaError_t e =
         launch(selective_fwd_kernel<E, L, ALIGNED, true>, blocks, kThreads,
                sizeof(FwdShared<E, L, ALIGNED, true>), st, a);
@@ -248,8 +248,10 @@ cudaError_t step(const SelectiveArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// (Fewer than four lanes a channel would take more channels a block, and with them 100 KB of
+// shared memory and more: up to sixteen states cost what sixteen do.)
 int selective_lanes(int N) {
-  int L = 1;
+  int L = 4;
   while (kStates * L < N) L *= 2;
   return L;
 }
@@ -260,13 +262,14 @@ int selective_blocks(int D, int N) { return (D - 1) / (kThreads / selective_lane
 // an SM (a split walks the tokens twice; training shape, 384 blocks: forward 565 us, in eight
 // segments 606, backward 1466 and 1572); else about eight blocks an SM (one prompt of 32768
 // tokens, 48 blocks: forward 2800 us whole, 1293 in 8 segments, 675 in 24), of four tiles or
-// more.
+// more.  More than 64 states: always one.
 int selective_segments(int B, int T, int D, int N, int* tiles_per_segment) {
   const int tiles = std::max(1, (T - 1) / kTile + 1);
   const int64_t blocks = static_cast<int64_t>(B) * selective_blocks(D, N);
   constexpr int64_t kSms = 152;
   int64_t S = 1;
-  if (blocks < 2 * kSms) S = std::min<int64_t>((8 * kSms - 1) / blocks + 1, tiles / 4);
+  if (blocks < 2 * kSms && selective_lanes(N) < 32)
+    S = std::min<int64_t>((8 * kSms - 1) / blocks + 1, tiles / 4);
   S = std::max<int64_t>(S, 1);
   *tiles_per_segment = static_cast<int>((tiles - 1) / S + 1);
   return (tiles - 1) / *tiles_per_segment + 1;

@@ -1108,6 +1108,11 @@ def sanatan_layer_norm_bwd(s, weight, dy, stats, ds=None, want_dweight=True, wan
     return dict(dx=dx, dweight=dw, dbias=db)
 
 
+def _needs(ctx, n):
+    """needs_input_grad of n arguments, those left out of the call among them."""
+    return ctx.needs_input_grad + (False,) * (n - len(ctx.needs_input_grad))
+
+
 class LayerNorm(torch.autograd.Function):
     """autograd wrapper: y = LayerNorm.apply(x, weight, bias), or (y, s) =
     LayerNorm.apply(x, weight, bias, residual, eps) with s = x + residual."""
@@ -1124,7 +1129,7 @@ class LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight, stats = ctx.saved_tensors
-        need = ctx.needs_input_grad
+        need = _needs(ctx, 5)
         if dy is None and ds is None:
             return None, None, None, None, None
         dy = torch.zeros_like(s) if dy is None else dy.contiguous()
@@ -1227,7 +1232,7 @@ class CausalConv(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, ds_last):
         x, w, bias, s0, lens = ctx.saved_tensors
-        need = ctx.needs_input_grad
+        need = _needs(ctx, 6)
         if dy is None and ds_last is None:
             return None, None, None, None, None, None
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None \
@@ -1357,7 +1362,7 @@ class SelectiveScan(torch.autograd.Function):
             return (None,) * 11
         dy = torch.zeros_like(u) if dy is None else dy.contiguous()
         d = sanatan_selective_scan_bwd(u, dt, A, B, C, dy, marks, D, z, dt_bias, ctx.softplus,
-                                       lens=lens, want_dh0=ctx.needs_input_grad[9],
+                                       lens=lens, want_dh0=_needs(ctx, 11)[9],
                                        dh_last=None if dh_last is None else dh_last.contiguous())
         return (d["du"], d["ddt"], d["dA"], d["dB"], d["dC"], d["dD"], d["dz"], d["ddt_bias"],
                 None, d["dh0"], None)
