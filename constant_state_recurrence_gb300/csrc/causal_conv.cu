@@ -14,7 +14,10 @@
 // them in a fixed order (no atomics: the same call gives the same bits).
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 
+#include "lanes.cuh"
+#include "copy_async.cuh"
 #include "pdl.cuh"
 #include "sanatan_internal.h"
 #include "vec_io.cuh"
@@ -22,14 +25,15 @@
 namespace sanatan {
 namespace {
 
+using namespace lanes;
+
 constexpr int kThreads = 128;
-constexpr int kRun = 16;        // tokens of a thread, forward
-constexpr int kAhead = 8;       // tokens whose loads are under way together
+constexpr int kRunLong = 64, kRunShort = 16;  // tokens of a thread, forward
 constexpr int kRunBwd = 32;
+constexpr int kStep = 4;     // tokens of a group of copies
+constexpr int kGroupsFwd = 4, kGroupsBwd = 3;  // groups of a ring
 constexpr int kLanes = 32, kRows = 8;  // backward block: channels x runs
 constexpr int kParts = kConvParts;
-
-__device__ __forceinline__ float sigmoid(float c) { return __fdividef(1.0f, 1.0f + __expf(-c)); }
 
 __device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
   if (lens == nullptr) return T;
@@ -37,67 +41,130 @@ __device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
   return n < 0 ? 0 : (n > T ? T : static_cast<int>(n));
 }
 
-// A sequence's inputs: token i in [-(K-1), n) of V channels from c.
+// A sequence's inputs: token i in [-(K-1), n) of V channels.
 template <typename E, int V>
 struct Inputs {
   const E* x;        // token 0
   const float* s;    // the state's first row, or null
   int64_t ld;
   int K, D;
-  __device__ __forceinline__ void at(int i, float (&f)[V]) const {
+  __device__ __forceinline__ Lanes<V> at(int i) const {
+    float f[V];
     if (i >= 0) {
       Vec<E, V> v;
       v.load(x + i * ld);
       v.get(f);
     } else if (s != nullptr) {
-      Vec<float, V> v;
-      v.load(s + static_cast<int64_t>(K - 1 + i) * D);
-      v.get(f);
+      load_floats(s + static_cast<int64_t>(K - 1 + i) * D, f);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) f[j] = 0.0f;
     }
+    return Lanes<V>::of(f);
+  }
+};
+
+// A thread's own ring in shared memory: groups of kStep tokens of NT tensors, copied while the
+// ones before are worked on (a thread reads only what it has copied: no barrier).
+template <typename E, int V, int NT, int GROUPS, int THREADS>
+struct Ring {
+  static constexpr int kBytes = V * sizeof(E);
+  static constexpr int kSlots = GROUPS * kStep * NT;
+  static constexpr size_t kShared = static_cast<size_t>(kSlots) * THREADS * kBytes;
+  char* base;  // slot 0
+  __device__ __forceinline__ explicit Ring(char* shared) : base(shared + threadIdx.x * kBytes) {}
+  __device__ __forceinline__ char* slot(int group, int i, int q) const {
+    return base + ((group * kStep + i) * NT + q) * (THREADS * kBytes);
+  }
+  __device__ __forceinline__ void copy(int group, int i, int q, const E* from) const {
+    char* to = slot(group, i, q);
+    if constexpr (kBytes >= 4) {
+      copy_words<kBytes>(to, from);
+    } else {
+      *reinterpret_cast<E*>(to) = *from;
+    }
+  }
+  __device__ __forceinline__ Lanes<V> get(int group, int i, int q) const {
+    Vec<E, V> v;
+    float f[V];
+    v.load(reinterpret_cast<const E*>(slot(group, i, q)));
+    v.get(f);
+    return Lanes<V>::of(f);
   }
 };
 
 // Weights of V channels from c: w [D, K], the K taps last of KM (the first KM - K: zeros).
 template <int KM, int V>
-__device__ __forceinline__ void load_weights(const float* w, int c, int K, float (&f)[KM][V]) {
+__device__ __forceinline__ void load_weights(const float* w, int c, int K, Lanes<V> (&out)[KM]) {
   const int pad = KM - K;
+  float f[V][KM];
+  bool words = false;
+  if constexpr (KM == 4) {
+    words = reinterpret_cast<uintptr_t>(w) % 16 == 0;
+    if (words)
 #pragma unroll
-  for (int k = 0; k < KM; ++k)
+      for (int j = 0; j < V; ++j) load_floats(w + static_cast<int64_t>(c + j) * KM, f[j]);
+  }
+  if (!words) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      f[k][j] = k >= pad ? w[static_cast<int64_t>(c + j) * K + k - pad] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < KM; ++k)
+        f[j][k] = k >= pad ? w[static_cast<int64_t>(c + j) * K + k - pad] : 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < KM; ++k) {
+    float g[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) g[j] = f[j][k];
+    out[k] = Lanes<V>::of(g);
+  }
+}
+template <int V>
+__device__ __forceinline__ Lanes<V> load_bias(const float* bias, int c) {
+  float f[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] = bias != nullptr ? bias[c + j] : 0.0f;
+  return Lanes<V>::of(f);
 }
 
 // c_t of the window (win: the KM - 1 inputs before, x the token's own).  Taps before the
 // first are left out, not multiplied by zero: what they would reach need not be finite.
 template <int KM, int V>
-__device__ __forceinline__ void convolve(const float (&w)[KM][V], const float (&win)[KM - 1][V],
-                                         const float (&x)[V], const float (&bias)[V], int K,
-                                         float (&c)[V]) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) c[j] = fmaf(w[KM - 1][j], x[j], bias[j]);
+__device__ __forceinline__ Lanes<V> convolve(const Lanes<V> (&w)[KM], const Lanes<V> (&win)[KM - 1],
+                                             const Lanes<V>& x, const Lanes<V>& bias, int K) {
+  Lanes<V> c = fma(w[KM - 1], x, bias);
 #pragma unroll
   for (int k = 0; k < KM - 1; ++k)
-    if (KM <= 4 || k >= KM - K)
-#pragma unroll
-      for (int j = 0; j < V; ++j) c[j] = fmaf(w[k][j], win[k][j], c[j]);
+    if (KM <= 4 || k >= KM - K) c = fma(w[k], win[k], c);
+  return c;
 }
 
 template <int N, int V>
-__device__ __forceinline__ void push(float (&win)[N][V], const float (&x)[V]) {
+__device__ __forceinline__ void push(Lanes<V> (&win)[N], const Lanes<V>& x) {
 #pragma unroll
-  for (int k = 0; k + 1 < N; ++k)
-#pragma unroll
-    for (int j = 0; j < V; ++j) win[k][j] = win[k + 1][j];
-#pragma unroll
-  for (int j = 0; j < V; ++j) win[N - 1][j] = x[j];
+  for (int k = 0; k + 1 < N; ++k) win[k] = win[k + 1];
+  win[N - 1] = x;
+}
+
+template <int V>
+__device__ __forceinline__ Lanes<V> activate(const Lanes<V>& c, int act) {
+  return act == SANATAN_ACT_SILU ? mul(c, sigmoid(c)) : c;
+}
+
+template <typename E, int V>
+__device__ __forceinline__ void store(E* p, const Lanes<V>& v) {
+  float f[V];
+  v.get(f);
+  Vec<E, V> o;
+  o.put(f);
+  o.store(p);
 }
 
 template <typename E, int KM, int V>
 __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
+  extern __shared__ float4 smem4[];
+  char* smem = reinterpret_cast<char*>(smem4);
   const int vecs = a.D / V, K = a.K, pad = KM - K;
   const int64_t runs = static_cast<int64_t>(a.B) * a.runs;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
@@ -116,78 +183,68 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
     float* out = a.s_out + static_cast<int64_t>(b) * (K - 1) * a.D + c;
     for (int k = 0; k < K - 1; ++k) {
       float f[V];
-      in.at(n - (K - 1) + k, f);
-      Vec<float, V> v;
-      v.put(f);
-      v.store(out + static_cast<int64_t>(k) * a.D);
+      in.at(n - (K - 1) + k).get(f);
+      store_floats(out + static_cast<int64_t>(k) * a.D, f);
     }
     return;
   }
-  const int t0 = static_cast<int>(row % a.runs) * kRun, end = min(t0 + kRun, a.T);
+  const int t0 = static_cast<int>(row % a.runs) * a.run, end = min(t0 + a.run, a.T);
+  const int live = min(end, n);
   E* y = static_cast<E*>(a.y) + (static_cast<int64_t>(b) * a.T + t0) * a.D + c;
-  float w[KM][V], bias[V], win[KM - 1][V];
-  if (t0 < n) {
+  int t = t0;
+  if (t < live) {
+    const Ring<E, V, 1, kGroupsFwd, kThreads> ring(smem);
+    const E* x = x0 + t0 * a.ldx;  // of the next group
+    int ahead = t0, into = 0;
+    auto begin = [&] {
+#pragma unroll
+      for (int i = 0; i < kStep; ++i)
+        if (ahead + i < live) ring.copy(into, i, 0, x + i * a.ldx);
+      copy_commit();
+      ahead += kStep, x += kStep * a.ldx, into = into + 1 == kGroupsFwd ? 0 : into + 1;
+    };
+#pragma unroll
+    for (int g = 0; g + 1 < kGroupsFwd; ++g) begin();
+    Lanes<V> w[KM], win[KM - 1];
+#pragma unroll
+    for (int k = 0; k < KM - 1; ++k) win[k] = k >= pad ? in.at(t0 - (KM - 1) + k) : Lanes<V>::of(0.0f);
     load_weights<KM, V>(a.w, c, K, w);
+    const Lanes<V> bias = load_bias<V>(a.bias, c);
+    for (int now = 0; t < live; t += kStep, now = now + 1 == kGroupsFwd ? 0 : now + 1) {
+      begin();
+      copy_wait<kGroupsFwd - 1>();
 #pragma unroll
-    for (int j = 0; j < V; ++j) bias[j] = a.bias != nullptr ? a.bias[c + j] : 0.0f;
-#pragma unroll
-    for (int k = 0; k < KM - 1; ++k) {
-      if (k >= pad) {
-        in.at(t0 - (KM - 1) + k, win[k]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) win[k][j] = 0.0f;
+      for (int i = 0; i < kStep; ++i) {
+        if (t + i >= live) break;
+        const Lanes<V> xv = ring.get(now, i, 0);
+        store(y, activate(convolve<KM, V>(w, win, xv, bias, K), a.act));
+        push(win, xv);
+        y += a.D;
       }
     }
+    copy_wait<0>();
+    t = live;
   }
-  for (int t = t0; t < end; t += kAhead) {
-    Vec<E, V> raw[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (t + i < end && t + i < n) raw[i].load(x0 + (t + i) * a.ldx);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (t + i >= end) break;
-      float f[V];
-      if (t + i < n) {
-        float x[V];
-        raw[i].get(x);
-        convolve<KM, V>(w, win, x, bias, K, f);
-        push(win, x);
-        if (a.act == SANATAN_ACT_SILU)
-#pragma unroll
-          for (int j = 0; j < V; ++j) f[j] = __fdividef(f[j], 1.0f + __expf(-f[j]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = 0.0f;
-      }
-      Vec<E, V> o;
-      o.put(f);
-      o.store(y);
-      y += a.D;
-    }
-  }
+  for (; t < end; ++t, y += a.D) store(y, Lanes<V>::of(0.0f));  // behind the last token
 }
 
 template <typename E, int KM, int V>
-__global__ void __launch_bounds__(kLanes* kRows) conv_bwd_kernel(ConvBwdArgs a) {
+__global__ void __launch_bounds__(kLanes* kRows, KM <= 4 ? 2 : 1) conv_bwd_kernel(ConvBwdArgs a) {
+  extern __shared__ float4 smem4[];
+  const Ring<E, V, 2, kGroupsBwd, kLanes * kRows> ring(reinterpret_cast<char*>(smem4));
   __shared__ float sums[kRows][V][kLanes + 1];
   const int lane = threadIdx.x % kLanes, ty = threadIdx.x / kLanes;
   const int K = a.K, pad = KM - K;
   const int c = (blockIdx.x * kLanes + lane) * V;
   const bool there = c < a.D;
-  float w[KM][V], bias[V], dw[KM][V], db[V];
+  const Lanes<V> zero = Lanes<V>::of(0.0f), one = Lanes<V>::of(1.0f);
+  Lanes<V> w[KM], dw[KM], bias = zero, db = zero;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    db[j] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < KM; ++k) dw[k][j] = 0.0f;
-  }
+  for (int k = 0; k < KM; ++k) w[k] = dw[k] = zero;
   wait_for_previous();
   if (there) {
     load_weights<KM, V>(a.w, c, K, w);
-#pragma unroll
-    for (int j = 0; j < V; ++j) bias[j] = a.bias != nullptr ? a.bias[c + j] : 0.0f;
+    bias = load_bias<V>(a.bias, c);
   }
   const int64_t runs = there ? static_cast<int64_t>(a.B) * a.runs : 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.y) * kRows + ty; row < runs;
@@ -195,106 +252,98 @@ __global__ void __launch_bounds__(kLanes* kRows) conv_bwd_kernel(ConvBwdArgs a) 
     const int b = static_cast<int>(row / a.runs);
     const int n = length_of(a.lens, b, a.T);
     const int t0 = static_cast<int>(row % a.runs) * kRunBwd, end = min(t0 + kRunBwd, a.T);
-    const E* x0 = static_cast<const E*>(a.x) + static_cast<int64_t>(b) * a.T * a.ldx + c;
     const int64_t at = static_cast<int64_t>(b) * a.T * a.D + c;
+    const int64_t state = static_cast<int64_t>(b) * (K - 1) * a.D + c;
+    const E* x = static_cast<const E*>(a.x) + static_cast<int64_t>(b) * a.T * a.ldx + c;
     const E* dy = static_cast<const E*>(a.dy) + at;
     E* dx = static_cast<E*>(a.dx) + at;
-    const int64_t state = static_cast<int64_t>(b) * (K - 1) * a.D + c;
-    const Inputs<E, V> in{x0, a.s0 == nullptr ? nullptr : a.s0 + state, a.ldx, K, a.D};
-    float win[KM - 1][V], open[KM][V];  // open[k]: dx of token t - (KM - 1) + k so far
+    const Inputs<E, V> in{x, a.s0 == nullptr ? nullptr : a.s0 + state, a.ldx, K, a.D};
+    Lanes<V> win[KM - 1], open[KM];  // open[k]: dx of token t - (KM - 1) + k so far
 #pragma unroll
-    for (int k = 0; k < KM; ++k)
+    for (int k = 0; k < KM; ++k) open[k] = zero;
 #pragma unroll
-      for (int j = 0; j < V; ++j) open[k][j] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < KM - 1; ++k) {
-      if (k >= pad && t0 < n) {
-        in.at(t0 - (KM - 1) + k, win[k]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) win[k][j] = 0.0f;
-      }
-    }
-    // dx is done for tokens from first on: the state's too in the first run
-    const int first = t0 == 0 ? -(K - 1) : t0;
-    constexpr int kStep = 4;
-    for (int t1 = t0; t1 < end + K - 1; t1 += kStep) {
-      Vec<E, V> rx[kStep], rd[kStep];
+    for (int k = 0; k < KM - 1; ++k)
+      win[k] = k >= pad && t0 < n ? in.at(t0 - (KM - 1) + k) : zero;
+    // dx is done for tokens from first on: the state's too in the first run; the tokens behind
+    // the run, up to last, finish its own and are another thread's otherwise.
+    const int first = t0 == 0 ? -(K - 1) : t0, last = end + K - 1;
+    // The state behind the last token holds the inputs from `held` on.
+    const int held = a.ds_out != nullptr ? n - (K - 1) : 1 << 30;
+    x += t0 * a.ldx;
+    dy += static_cast<int64_t>(t0) * a.D;
+    int ahead = t0, into = 0;
+    auto begin = [&] {
 #pragma unroll
       for (int i = 0; i < kStep; ++i)
-        if (t1 + i < n && t1 + i < end + K - 1) {
-          rx[i].load(x0 + (t1 + i) * a.ldx);
-          rd[i].load(dy + static_cast<int64_t>(t1 + i) * a.D);
+        if (ahead + i < n && ahead + i < last) {
+          ring.copy(into, i, 0, x + i * a.ldx);
+          ring.copy(into, i, 1, dy + static_cast<int64_t>(i) * a.D);
         }
+      copy_commit();
+      ahead += kStep, x += kStep * a.ldx, dy += static_cast<int64_t>(kStep) * a.D;
+      into = into + 1 == kGroupsBwd ? 0 : into + 1;
+    };
+    // Four tokens from t; INSIDE: all of them the run's, and what they finish is, too.
+    auto tokens = [&](int t, int now, auto inside) {
+      constexpr bool INSIDE = decltype(inside)::value;
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
-        const int t = t1 + i;
-        if (t >= end + K - 1) break;
-        if (t < n) {
-          float x[V], d[V];
-          rx[i].get(x);
-          rd[i].get(d);
+        if (!INSIDE && t + i >= last) break;
+        if (INSIDE || t + i < n) {
+          const Lanes<V> xv = ring.get(now, i, 0);
+          Lanes<V> d = ring.get(now, i, 1);
           if (a.act == SANATAN_ACT_SILU) {
-            float f[V];
-            convolve<KM, V>(w, win, x, bias, K, f);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const float sg = sigmoid(f[j]);
-              d[j] *= fmaf(f[j] * sg, 1.0f - sg, sg);
-            }
+            const Lanes<V> cv = convolve<KM, V>(w, win, xv, bias, K), sg = sigmoid(cv);
+            d = mul(d, fma(mul(cv, sg), sub(one, sg), sg));
           }
 #pragma unroll
           for (int k = 0; k < KM; ++k)
-            if (KM <= 4 || k >= pad)
+            if (KM <= 4 || k >= pad) open[k] = fma(w[k], d, open[k]);
+          if (INSIDE || t + i < end) {
+            db = add(d, db);
+            dw[KM - 1] = fma(d, xv, dw[KM - 1]);
 #pragma unroll
-              for (int j = 0; j < V; ++j) open[k][j] = fmaf(w[k][j], d[j], open[k][j]);
-          if (t < end) {  // (the tokens behind the run are another thread's)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              db[j] += d[j];
-              dw[KM - 1][j] = fmaf(d[j], x[j], dw[KM - 1][j]);
-#pragma unroll
-              for (int k = 0; k < KM - 1; ++k)
-                if (KM <= 4 || k >= pad) dw[k][j] = fmaf(d[j], win[k][j], dw[k][j]);
-            }
+            for (int k = 0; k < KM - 1; ++k)
+              if (KM <= 4 || k >= pad) dw[k] = fma(d, win[k], dw[k]);
           }
-          push(win, x);
+          push(win, xv);
         }
-        // dx of token o is done
-        const int o = t - (K - 1);
-        float f[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = KM <= 4 ? open[0][j] : 0.0f;
+        const int o = t + i - (K - 1);  // its dx is done
+        Lanes<V> done = open[0];
         if (KM > 4)
 #pragma unroll
-          for (int k = 0; k < KM; ++k)
-            if (k == pad)
-#pragma unroll
-              for (int j = 0; j < V; ++j) f[j] = open[k][j];
-        if (o >= first && o < end) {
-          const int k = o - (n - (K - 1));  // the state behind the last token holds it
-          if (a.ds_out != nullptr && k >= 0 && k < K - 1) {
-            Vec<float, V> v;
-            float g[V];
-            v.load(a.ds_out + state + static_cast<int64_t>(k) * a.D);
-            v.get(g);
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[j] += g[j];
+          for (int k = 1; k < KM; ++k)
+            if (k == pad) done = open[k];
+        if (INSIDE) {
+          store(dx + static_cast<int64_t>(o) * a.D, done);
+        } else if (o >= first && o < end) {
+          float f[V];
+          if (o >= held && o < n) {
+            load_floats(a.ds_out + state + static_cast<int64_t>(o - held) * a.D, f);
+            done = add(Lanes<V>::of(f), done);
           }
           if (o >= 0) {
-            Vec<E, V> v;
-            v.put(f);
-            v.store(dx + static_cast<int64_t>(o) * a.D);
+            store(dx + static_cast<int64_t>(o) * a.D, done);
           } else if (a.ds0 != nullptr) {
-            Vec<float, V> v;
-            v.put(f);
-            v.store(a.ds0 + state + static_cast<int64_t>(K - 1 + o) * a.D);
+            done.get(f);
+            store_floats(a.ds0 + state + static_cast<int64_t>(K - 1 + o) * a.D, f);
           }
         }
-        const float zero[V] = {};
         push(open, zero);
       }
+    };
+#pragma unroll
+    for (int g = 0; g + 1 < kGroupsBwd; ++g) begin();
+    int now = 0;
+    for (int t = t0; t < last; t += kStep, now = now + 1 == kGroupsBwd ? 0 : now + 1) {
+      begin();
+      copy_wait<kGroupsBwd - 1>();
+      if (t + kStep <= min(end, n) && t - (K - 1) >= max(first, 0) && t + kStep - K < held)
+        tokens(t, now, std::true_type{});
+      else
+        tokens(t, now, std::false_type{});
     }
+    copy_wait<0>();
   }
   if (a.parts == nullptr) return;
   // The block's runs together, tap by tap: part [K + 1][D], the bias last.
@@ -302,11 +351,12 @@ __global__ void __launch_bounds__(kLanes* kRows) conv_bwd_kernel(ConvBwdArgs a) 
 #pragma unroll
   for (int k = 0; k <= KM; ++k) {
     if (k < pad) continue;
+    float f[V];
+    (k < KM ? dw[k < KM ? k : 0] : db).get(f);
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < V; ++j) sums[ty][j][lane] = k < KM ? dw[k < KM ? k : 0][j] : db[j];
+    for (int j = 0; j < V; ++j) sums[ty][j][lane] = f[j];
     __syncthreads();
-    // (V * kLanes channels, of which each thread adds up some)
     for (int i = threadIdx.x; i < V * kLanes; i += kLanes * kRows) {
       const int j = i % V, l = i / V;
       float s = 0.0f;
@@ -319,22 +369,23 @@ __global__ void __launch_bounds__(kLanes* kRows) conv_bwd_kernel(ConvBwdArgs a) 
 }
 
 // dw [D, K] and dbias [D] from n parts [K + 1][D].
-__global__ void __launch_bounds__(256) conv_parts_kernel(const float* parts, int n, int D, int K,
+__global__ void __launch_bounds__(1024) conv_parts_kernel(const float* parts, int n, int D, int K,
                                                          float* dw, float* db) {
-  __shared__ float all[8][33];
+  __shared__ float all[32][33];
   const int x = threadIdx.x % 32, ty = threadIdx.x / 32;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + x;
   const int64_t wide = static_cast<int64_t>(K + 1) * D;
   wait_for_previous();
   float v = 0.0f;
   if (i < wide)
-    for (int p = ty; p < n; p += 8) v += parts[p * wide + i];
+#pragma unroll 4
+    for (int p = ty; p < n; p += 32) v += parts[p * wide + i];
   all[ty][x] = v;
   __syncthreads();
   if (ty == 0 && i < wide) {
     float s = 0.0f;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) s += all[p][x];
+    for (int p = 0; p < 32; ++p) s += all[p][x];
     const int64_t k = i / D, c = i % D;
     if (k < K) {
       if (dw != nullptr) dw[c * K + k] = s;
@@ -355,47 +406,38 @@ __global__ void __launch_bounds__(kThreads)
   const int c = static_cast<int>(item % vecs) * V;
   wait_for_previous();
   float* s = state + n * (K - 1) * D + c;
-  float wt[KM][V], win[KM - 1][V], b[V], xv[V], f[V];
+  Lanes<V> wt[KM], win[KM - 1];
+  float f[V];
   Vec<E, V> raw;
   raw.load(x + n * ldx + c);
 #pragma unroll
   for (int k = 0; k < KM - 1; ++k) {
+    win[k] = Lanes<V>::of(0.0f);
     if (k >= pad) {
-      Vec<float, V> v;
-      v.load(s + static_cast<int64_t>(k - pad) * D);
-      v.get(win[k]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) win[k][j] = 0.0f;
+      load_floats(s + static_cast<int64_t>(k - pad) * D, f);
+      win[k] = Lanes<V>::of(f);
     }
   }
   load_weights<KM, V>(w, c, K, wt);
-#pragma unroll
-  for (int j = 0; j < V; ++j) b[j] = bias != nullptr ? bias[c + j] : 0.0f;
-  raw.get(xv);
-  convolve<KM, V>(wt, win, xv, b, K, f);
+  raw.get(f);
+  const Lanes<V> xv = Lanes<V>::of(f), b = load_bias<V>(bias, c);
+  store(y + n * D + c, activate(convolve<KM, V>(wt, win, xv, b, K), act));
   push(win, xv);
 #pragma unroll
   for (int k = 0; k < KM - 1; ++k)
     if (k >= pad) {
-      Vec<float, V> v;
-      v.put(win[k]);
-      v.store(s + static_cast<int64_t>(k - pad) * D);
+      win[k].get(f);
+      store_floats(s + static_cast<int64_t>(k - pad) * D, f);
     }
-  if (act == SANATAN_ACT_SILU)
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = __fdividef(f[j], 1.0f + __expf(-f[j]));
-  Vec<E, V> o;
-  o.put(f);
-  o.store(y + n * D + c);
 }
 
 template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t st,
-                   Args... args) {
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t shared,
+                   cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
   cfg.stream = st;
   cudaLaunchAttribute attr = pdl_attribute();
   cfg.attrs = &attr;
@@ -407,32 +449,52 @@ unsigned blocks_of(int64_t items) { return static_cast<unsigned>((items - 1) / k
 
 template <typename E, int KM, int V>
 cudaError_t fwd(ConvArgs a, cudaStream_t st) {
-  a.runs = (a.T + kRun - 1) / kRun;
+  // Long runs read fewer tokens twice, and weights less often, where they are enough to give
+  // every SM two blocks.
+  const int64_t vecs = a.D / V, longs = (a.T + kRunLong - 1) / kRunLong;
+  a.run = a.B * longs * vecs >= 152 * 2 * kThreads ? kRunLong : kRunShort;
+  a.runs = (a.T + a.run - 1) / a.run;
   const int64_t rows = static_cast<int64_t>(a.B) * a.runs + (a.s_out != nullptr ? a.B : 0);
   if (rows == 0) return cudaSuccess;
-  return launch(conv_fwd_kernel<E, KM, V>, dim3(blocks_of(rows * (a.D / V))), kThreads, st, a);
+  constexpr size_t shared = Ring<E, V, 1, kGroupsFwd, kThreads>::kShared;
+  static_assert(shared <= 48 * 1024, "no opt-in");
+  return launch(conv_fwd_kernel<E, KM, V>, dim3(blocks_of(rows * vecs)), kThreads, shared, st, a);
+}
+
+// Blocks of runs: each takes several, so that the weights' gradients are added up in registers;
+// two blocks an SM at most.
+int parts_of(int B, int runs, int D, int V) {
+  const int64_t blocks = (static_cast<int64_t>(B) * runs - 1) / kRows + 1;
+  const int64_t columns = (D - 1) / (V * kLanes) + 1;
+  return static_cast<int>(
+      std::min<int64_t>(std::min<int64_t>(kParts, blocks), std::max<int64_t>(1, 2 * 152 / columns)));
 }
 
 template <typename E, int KM, int V>
 cudaError_t bwd(ConvBwdArgs a, cudaStream_t st) {
   a.runs = std::max(1, (a.T + kRunBwd - 1) / kRunBwd);  // (the state's gradient without tokens)
-  const int n = static_cast<int>(
-      std::min<int64_t>(kParts, (static_cast<int64_t>(a.B) * a.runs - 1) / kRows + 1));
+  const int n = parts_of(a.B, a.runs, a.D, V);
   const bool sums = a.dw != nullptr || a.dbias != nullptr;
   if (!sums) a.parts = nullptr;
-  const cudaError_t e =
-      launch(conv_bwd_kernel<E, KM, V>, dim3((a.D - 1) / (V * kLanes) + 1, n), kLanes * kRows, st,
-             a);
+  constexpr size_t shared = Ring<E, V, 2, kGroupsBwd, kLanes * kRows>::kShared;
+  if (shared > 40 * 1024) {  // (with the block's own)
+    const cudaError_t e =
+        cudaFuncSetAttribute(conv_bwd_kernel<E, KM, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(shared));
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t e = launch(conv_bwd_kernel<E, KM, V>, dim3((a.D - 1) / (V * kLanes) + 1, n),
+                               kLanes * kRows, shared, st, a);
   if (e != cudaSuccess || !sums) return e;
   const int64_t wide = static_cast<int64_t>(a.K + 1) * a.D;
-  return launch(conv_parts_kernel, dim3(static_cast<unsigned>((wide - 1) / 32 + 1)), 256, st,
+  return launch(conv_parts_kernel, dim3(static_cast<unsigned>((wide - 1) / 32 + 1)), 1024, 0, st,
                 static_cast<const float*>(a.parts), n, a.D, a.K, a.dw, a.dbias);
 }
 
 template <typename E, int KM, int V>
 cudaError_t step(const ConvArgs& a, cudaStream_t st) {
   return launch(conv_step_kernel<E, KM, V>, dim3(blocks_of(static_cast<int64_t>(a.B) * (a.D / V))),
-                kThreads, st, a.s_out, static_cast<const E*>(a.x), a.ldx, a.w, a.bias, a.act, a.B,
+                kThreads, 0, st, a.s_out, static_cast<const E*>(a.x), a.ldx, a.w, a.bias, a.act, a.B,
                 a.D, a.K, static_cast<E*>(a.y));
 }
 
@@ -445,39 +507,39 @@ bool words(int V, int D, int64_t ldx, std::initializer_list<const void*> tensors
   for (const void* p : tensors)
     if (!at_bytes(p, V * sizeof(E))) return false;
   for (const void* p : states)
-    if (!at_bytes(p, V > 1 ? 16 : 4)) return false;
+    if (!at_bytes(p, V >= 4 ? 16 : 4 * V)) return false;
   return true;
 }
 
 }  // namespace
 
-// f<E, KM, V> for the taps and the widest words that every address allows.
-#define SANATAN_CONV_DISPATCH(f, E, a, st, vec)                      \
+// f<E, KM, V> for the taps, with V channels a thread where every address allows it.
+#define SANATAN_CONV_DISPATCH(f, E, V, a, st, vec)                   \
   switch (a.K) {                                                     \
     case 2:                                                          \
-      return vec ? f<E, 2, 4>(a, st) : f<E, 2, 1>(a, st);            \
+      return vec ? f<E, 2, V>(a, st) : f<E, 2, 1>(a, st);            \
     case 3:                                                          \
-      return vec ? f<E, 3, 4>(a, st) : f<E, 3, 1>(a, st);            \
+      return vec ? f<E, 3, V>(a, st) : f<E, 3, 1>(a, st);            \
     case 4:                                                          \
-      return vec ? f<E, 4, 4>(a, st) : f<E, 4, 1>(a, st);            \
+      return vec ? f<E, 4, V>(a, st) : f<E, 4, 1>(a, st);            \
     default:                                                         \
-      return vec ? f<E, 8, 4>(a, st) : f<E, 8, 1>(a, st);            \
+      return vec ? f<E, 8, 4>(a, st) : f<E, 8, 1>(a, st); \
   }
 
 size_t causal_conv_bwd_workspace_bytes(int B, int T, int D, int K) {
   if (B <= 0 || T < 0 || D <= 0 || K < 1) return 0;
-  const int64_t runs = static_cast<int64_t>(B) * std::max(1, T / kRunBwd + (T % kRunBwd != 0));
-  const size_t n = static_cast<size_t>(std::min<int64_t>(kParts, (runs - 1) / kRows + 1));
-  return sizeof(float) * n * (K + 1) * static_cast<size_t>(D);
+  // (one channel a thread has the fewest blocks of runs, four the most)
+  const int n = parts_of(B, std::max(1, T / kRunBwd + (T % kRunBwd != 0)), D, 4);
+  return sizeof(float) * static_cast<size_t>(n) * (K + 1) * static_cast<size_t>(D);
 }
 
 cudaError_t causal_conv_fwd_launch(const ConvArgs& a, cudaStream_t st) {
   if (a.dtype == SANATAN_F32) {
     const bool vec = words<float>(4, a.D, a.ldx, {a.x, a.y}, {a.s0, a.s_out});
-    SANATAN_CONV_DISPATCH(fwd, float, a, st, vec)
+    SANATAN_CONV_DISPATCH(fwd, float, 4, a, st, vec)
   }
-  const bool vec = words<__nv_bfloat16>(4, a.D, a.ldx, {a.x, a.y}, {a.s0, a.s_out});
-  SANATAN_CONV_DISPATCH(fwd, __nv_bfloat16, a, st, vec)
+  const bool vec = words<__nv_bfloat16>(8, a.D, a.ldx, {a.x, a.y}, {a.s0, a.s_out});
+  SANATAN_CONV_DISPATCH(fwd, __nv_bfloat16, 8, a, st, vec)
 }
 
 cudaError_t causal_conv_bwd_launch(const ConvBwdArgs& a, cudaStream_t st) {
@@ -489,19 +551,19 @@ cudaError_t causal_conv_bwd_launch(const ConvBwdArgs& a, cudaStream_t st) {
   }
   if (a.dtype == SANATAN_F32) {
     const bool vec = words<float>(4, a.D, a.ldx, {a.x, a.dy, a.dx}, {a.s0, a.ds_out, a.ds0});
-    SANATAN_CONV_DISPATCH(bwd, float, a, st, vec)
+    SANATAN_CONV_DISPATCH(bwd, float, 4, a, st, vec)
   }
   const bool vec = words<__nv_bfloat16>(4, a.D, a.ldx, {a.x, a.dy, a.dx}, {a.s0, a.ds_out, a.ds0});
-  SANATAN_CONV_DISPATCH(bwd, __nv_bfloat16, a, st, vec)
+  SANATAN_CONV_DISPATCH(bwd, __nv_bfloat16, 4, a, st, vec)
 }
 
 cudaError_t causal_conv_step_launch(const ConvArgs& a, cudaStream_t st) {
   if (a.dtype == SANATAN_F32) {
     const bool vec = words<float>(4, a.D, a.ldx, {a.x, a.y}, {a.s_out});
-    SANATAN_CONV_DISPATCH(step, float, a, st, vec)
+    SANATAN_CONV_DISPATCH(step, float, 4, a, st, vec)
   }
   const bool vec = words<__nv_bfloat16>(4, a.D, a.ldx, {a.x, a.y}, {a.s_out});
-  SANATAN_CONV_DISPATCH(step, __nv_bfloat16, a, st, vec)
+  SANATAN_CONV_DISPATCH(step, __nv_bfloat16, 4, a, st, vec)
 }
 
 }  // namespace sanatan

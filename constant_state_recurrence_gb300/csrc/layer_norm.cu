@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <initializer_list>
 
+#include "copy_async.cuh"
 #include "pdl.cuh"
 #include "sanatan_internal.h"
 #include "vec_io.cuh"
@@ -25,10 +26,13 @@ namespace sanatan {
 namespace {
 
 constexpr int kRowWarps = 4;      // rows of a block, a warp a row
-constexpr int kWarpValues = 32;   // values of a lane, rows of up to 1024
 constexpr int kMostThreads = 1024;
-constexpr int kGroupThreads = 384;  // threads of a backward block that holds several groups
+constexpr int kRows = 2;          // of a group at a time, backward
+constexpr int kGroupThreads = 288;  // threads of a backward block that holds several groups
 constexpr int kParts = kNormParts;
+constexpr int kAhead = 2;         // turns of a group whose rows are under way, backward
+template <int R>
+constexpr int kRing = (kAhead + 1) * R * 3;  // 16-byte places of a thread
 constexpr int kLoopThreads = 512;
 
 template <typename E>
@@ -111,13 +115,29 @@ __device__ __forceinline__ float rounded_sum(float x, float r) {
   return load_as_float(&s);
 }
 
-// Weight and bias of a column (null: 1 and 0).
+// Weight and bias of a column (null: 1 and 0), and of a part's.
 __device__ __forceinline__ float weight_of(const float* w, int c) { return w ? w[c] : 1.0f; }
 __device__ __forceinline__ float bias_of(const float* b, int c) { return b ? b[c] : 0.0f; }
+template <typename E, bool ALIGNED>
+__device__ __forceinline__ void param_of(const float* p, float none, int t, int G, int i, int D,
+                                         float (&f)[kVec<E>]) {
+  using P = Part<E, ALIGNED>;
+#pragma unroll
+  for (int j = 0; j < P::V; ++j) f[j] = none;
+  if (p == nullptr) return;
+  if (ALIGNED) {
+    if (P::col(t, G, i, 0) < D) load_floats(p + P::col(t, G, i, 0), f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < P::V; ++j)
+      if (P::col(t, G, i, j) < D) f[j] = p[P::col(t, G, i, j)];
+  }
+}
 
 // A row in registers: WARP: of a warp, NV parts a lane; else of the block.
 template <typename E, int NV, bool ALIGNED, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kRowWarps : kMostThreads)
+__global__ void __launch_bounds__(WARP ? 32 * kRowWarps : kMostThreads,
+                                  WARP ? (NV * kVec<E> <= 24 ? 8 : 6) : 1)
     norm_fwd_kernel(NormArgs a) {
   using P = Part<E, ALIGNED>;
   constexpr int V = P::V;
@@ -173,12 +193,11 @@ __global__ void __launch_bounds__(WARP ? 32 * kRowWarps : kMostThreads)
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float f[V];
+    float w[V], f[V];
+    param_of<E, ALIGNED>(a.weight, 1.0f, t, G, i, D, w);
+    param_of<E, ALIGNED>(a.bias, 0.0f, t, G, i, D, f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = P::col(t, G, i, j);
-      f[j] = c < D ? fmaf(s[i][j] * rstd, weight_of(a.weight, c), bias_of(a.bias, c)) : 0.0f;
-    }
+    for (int j = 0; j < V; ++j) f[j] = fmaf(s[i][j] * rstd, w[j], f[j]);
     P::store(static_cast<E*>(a.y) + row * D, t, G, i, D, f);
   }
 }
@@ -256,45 +275,77 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Groups of G threads, one load of a row a thread, R rows at a time.
+// Groups of G threads, one load of a row a thread, R rows at a time.  Where rows are words, the
+// rows of the next kAhead turns are copied to a ring in shared memory meanwhile, in which each
+// thread has places of its own (32768 x 768 bf16: see the head).
 template <typename E, bool ALIGNED, int R, int MOST>
-__global__ void __launch_bounds__(MOST) norm_bwd_kernel(NormBwdArgs a, int G, float* parts) {
+__global__ void __launch_bounds__(MOST, MOST == kGroupThreads ? 2 : 1)
+    norm_bwd_kernel(NormBwdArgs a, int G, float* parts) {
   using P = Part<E, ALIGNED>;
   constexpr int V = P::V;
   constexpr int N = 2 * R;
   extern __shared__ float4 smem4[];
-  // [groups][2][warps of a group][N] sums, then [2 * V][G] columns of the groups before
+  // the ring [turn][row][s | dy | ds][thread], then [groups][2][warps of a group][N] sums, then
+  // [2 * V][G] columns of the groups before
   const int groups = blockDim.x / G, warps = G / 32;
   const int group = threadIdx.x / G, t = threadIdx.x % G, lane = threadIdx.x % 32;
-  float* red = reinterpret_cast<float*>(smem4) + group * (2 * warps * N);
-  float* columns = reinterpret_cast<float*>(smem4) + groups * (2 * warps * N);
+  float4* ring = smem4 + threadIdx.x;
+  float* sums = reinterpret_cast<float*>(smem4 + (ALIGNED ? kRing<R> * blockDim.x : 0));
+  float* red = sums + group * (2 * warps * N);
+  float* columns = sums + groups * (2 * warps * N);
   const int D = a.D;
   const float inv = 1.0f / D;
+  const bool there = P::col(t, G, 0, 0) < D;
   float w[V], dw[V], db[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) dw[j] = db[j] = 0.0f;
   wait_for_previous();
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = P::col(t, G, 0, j);
-    w[j] = c < D ? weight_of(a.weight, c) : 0.0f;
-  }
+  param_of<E, ALIGNED>(a.weight, 1.0f, t, G, 0, D, w);  // (past the end dy is zero)
   const int mine = warp_sums_index<N>(lane);
-  int turn = 0;
+  int turn = 0, into = 0, now = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups * R;
-  for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * groups + group) * R; row0 < a.rows;
-       row0 += step, turn ^= 1) {
-    P s[R], dy[R], ds[R];
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * groups + group) * R;
+  int64_t ahead = first;
+  auto place = [&](int k, int r, int q) { return ring + ((k * R + r) * 3 + q) * blockDim.x; };
+  auto copy = [&] {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (there && ahead + r < a.rows) {
+        const int64_t at = (ahead + r) * D + P::col(t, G, 0, 0);
+        copy_words<16>(place(into, r, 0), static_cast<const E*>(a.s) + at);
+        copy_words<16>(place(into, r, 1), static_cast<const E*>(a.dy) + at);
+        if (a.ds != nullptr) copy_words<16>(place(into, r, 2), static_cast<const E*>(a.ds) + at);
+      }
+    copy_commit();
+    ahead += step, into = into == kAhead ? 0 : into + 1;
+  };
+  auto load = [&](P& p, int r, int q, const void* x, int64_t row) {
+    if constexpr (ALIGNED) {
+      if (there && row < a.rows)
+        p.v.load(reinterpret_cast<const E*>(place(now, r, q)));
+      else
+        p.v.raw = {};
+    } else {
+      // (a row past the end: zeros, nothing is read)
+      p.load(static_cast<const E*>(x) + row * D, t, G, 0, row < a.rows ? D : 0);
+    }
+  };
+  if constexpr (ALIGNED)
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) copy();
+  for (int64_t row0 = first; row0 < a.rows; row0 += step, turn ^= 1) {
+    P s[R], dy[R];
     float mean[R], rstd[R];
+    if constexpr (ALIGNED) {
+      copy();
+      copy_wait<kAhead>();
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t row = row0 + r;
-      const int d = row < a.rows ? D : 0;  // (a row past the end: zeros, nothing is read)
-      s[r].load(static_cast<const E*>(a.s) + row * D, t, G, 0, d);
-      dy[r].load(static_cast<const E*>(a.dy) + row * D, t, G, 0, d);
-      if (a.ds != nullptr) ds[r].load(static_cast<const E*>(a.ds) + row * D, t, G, 0, d);
-      mean[r] = d ? a.stats[2 * row] : 0.0f;
-      rstd[r] = d ? a.stats[2 * row + 1] : 0.0f;
+      load(s[r], r, 0, a.s, row0 + r);
+      load(dy[r], r, 1, a.dy, row0 + r);
+      mean[r] = row0 + r < a.rows ? a.stats[2 * (row0 + r)] : 0.0f;
+      rstd[r] = row0 + r < a.rows ? a.stats[2 * (row0 + r) + 1] : 0.0f;
     }
     float v[N];
 #pragma unroll
@@ -313,15 +364,15 @@ __global__ void __launch_bounds__(MOST) norm_bwd_kernel(NormBwdArgs a, int G, fl
       }
     }
     const float sum = warp_sums<N>(v, lane);
-    float* now = red + turn * (warps * N);  // (the other half may still be read)
-    if (lane < N) now[(t / 32) * N + mine] = sum;
+    float* half = red + turn * (warps * N);  // (the other half may still be read)
+    if (lane < N) half[(t / 32) * N + mine] = sum;
     group_sync(1 + group, G);
     float total[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) total[k] = 0.0f;
     for (int k = 0; k < warps; ++k)
 #pragma unroll
-      for (int q = 0; q < N; ++q) total[q] += now[k * N + q];
+      for (int q = 0; q < N; ++q) total[q] += half[k * N + q];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (row0 + r >= a.rows) break;
@@ -335,13 +386,17 @@ __global__ void __launch_bounds__(MOST) norm_bwd_kernel(NormBwdArgs a, int G, fl
         f[j] = rstd[r] * (fmaf(g[j], w[j], -c1) - n * c2);
       }
       if (a.ds != nullptr) {
-        ds[r].get(g);
+        P ds;
+        load(ds, r, 2, a.ds, row0 + r);
+        ds.get(g);
 #pragma unroll
         for (int j = 0; j < V; ++j) f[j] += g[j];
       }
       P::store(static_cast<E*>(a.dx) + (row0 + r) * D, t, G, 0, D, f);
     }
+    now = now == kAhead ? 0 : now + 1;
   }
+  if constexpr (ALIGNED) copy_wait<0>();
   if (parts == nullptr) return;
   // The groups' columns, one group after the other, then the block's part.
   for (int k = 0; k < groups; ++k) {
@@ -420,21 +475,22 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(NormBwdArgs a, float*
 }
 
 // dw and db from the blocks' parts [n][2][D].
-__global__ void __launch_bounds__(256) norm_parts_kernel(const float* parts, int n, int D,
-                                                         float* dw, float* db) {
-  __shared__ float all[8][33];
+__global__ void __launch_bounds__(1024) norm_parts_kernel(const float* parts, int n, int D,
+                                                          float* dw, float* db) {
+  __shared__ float all[32][33];
   const int x = threadIdx.x % 32, ty = threadIdx.x / 32;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x, wide = 2 * static_cast<int64_t>(D);
   wait_for_previous();
   float v = 0.0f;
   if (c < wide)
-    for (int k = ty; k < n; k += 8) v += parts[k * wide + c];
+#pragma unroll 4
+    for (int k = ty; k < n; k += 32) v += parts[k * wide + c];
   all[ty][x] = v;
   __syncthreads();
   if (ty == 0 && c < wide) {
     float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += all[k][x];
+    for (int k = 0; k < 32; ++k) sum += all[k][x];
     if (c < D) {
       if (dw != nullptr) dw[c] = sum;
     } else if (db != nullptr) {
@@ -446,6 +502,11 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(const float* parts, int
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t shared,
                    cudaStream_t st, Args... args) {
+  if (shared > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -463,12 +524,19 @@ template <typename E, bool ALIGNED>
 cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
   constexpr int V = kVec<E>;
   const unsigned rows = static_cast<unsigned>(a.rows);
-  if (a.D <= 32 * kWarpValues) {
+  if (a.D <= 1024) {
     const dim3 grid((rows - 1) / kRowWarps + 1);
-    return a.D <= 32 * V ? launch(norm_fwd_kernel<E, 1, ALIGNED, true>, grid, 32 * kRowWarps, 0,
-                                  st, a)
-                         : launch(norm_fwd_kernel<E, kWarpValues / V, ALIGNED, true>, grid,
-                                  32 * kRowWarps, 0, st, a);
+    // 8, 16, 24 or 32 values a lane
+    switch ((a.D - 1) / 256) {
+      case 0:
+        return launch(norm_fwd_kernel<E, 8 / V, ALIGNED, true>, grid, 32 * kRowWarps, 0, st, a);
+      case 1:
+        return launch(norm_fwd_kernel<E, 16 / V, ALIGNED, true>, grid, 32 * kRowWarps, 0, st, a);
+      case 2:
+        return launch(norm_fwd_kernel<E, 24 / V, ALIGNED, true>, grid, 32 * kRowWarps, 0, st, a);
+      default:
+        return launch(norm_fwd_kernel<E, 32 / V, ALIGNED, true>, grid, 32 * kRowWarps, 0, st, a);
+    }
   }
   if (a.D <= kMostThreads * V)
     return launch(norm_fwd_kernel<E, 1, ALIGNED, false>, dim3(rows), up32((a.D - 1) / V + 1), 0,
@@ -487,11 +555,12 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t st) {
     const int G = up32((a.D - 1) / V + 1);
     const bool several = G <= kGroupThreads;
     // (at most twelve groups: one has a barrier of its own, of sixteen)
-    const int groups = several ? kGroupThreads / G : 1, R = several ? 4 : 1;
+    const int groups = several ? kGroupThreads / G : 1, R = several ? kRows : 1;
     n = static_cast<int>(std::min<int64_t>(kParts, (a.rows - 1) / (groups * R) + 1));
     const size_t shared =
-        sizeof(float) * (groups * (2 * (G / 32) * 2 * R) + (groups > 1 ? 2 * V * G : 0));
-    e = several ? launch(norm_bwd_kernel<E, ALIGNED, 4, kGroupThreads>, dim3(n), G * groups,
+        sizeof(float) * (groups * (2 * (G / 32) * 2 * R) + (groups > 1 ? 2 * V * G : 0)) +
+        (ALIGNED ? static_cast<size_t>(kAhead + 1) * R * 3 * G * groups * 16 : 0);
+    e = several ? launch(norm_bwd_kernel<E, ALIGNED, kRows, kGroupThreads>, dim3(n), G * groups,
                          shared, st, a, G, parts)
                 : launch(norm_bwd_kernel<E, ALIGNED, 1, kMostThreads>, dim3(n), G, shared, st, a,
                          G, parts);
@@ -504,7 +573,7 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t st) {
     }
   }
   if (e != cudaSuccess || !columns) return e;
-  return launch(norm_parts_kernel, dim3(static_cast<unsigned>((2ll * a.D - 1) / 32 + 1)), 256, 0,
+  return launch(norm_parts_kernel, dim3(static_cast<unsigned>((2ll * a.D - 1) / 32 + 1)), 1024, 0,
                 st, static_cast<const float*>(parts), n, a.D, a.dweight, a.dbias);
 }
 
@@ -522,7 +591,7 @@ size_t layer_norm_bwd_workspace_bytes(int64_t rows, int D) {
 }
 
 cudaError_t layer_norm_fwd_launch(const NormArgs& a, cudaStream_t st) {
-  const bool vec = vectors(a.D, a.dtype, {a.x, a.residual, a.sum, a.y});
+  const bool vec = vectors(a.D, a.dtype, {a.x, a.residual, a.sum, a.y, a.weight, a.bias});
   if (a.dtype == SANATAN_F32) return vec ? fwd<float, true>(a, st) : fwd<float, false>(a, st);
   return vec ? fwd<__nv_bfloat16, true>(a, st) : fwd<__nv_bfloat16, false>(a, st);
 }
@@ -534,7 +603,7 @@ cudaError_t layer_norm_bwd_launch(const NormBwdArgs& a, cudaStream_t st) {
     if (e == cudaSuccess && a.dbias != nullptr) e = cudaMemsetAsync(a.dbias, 0, row, st);
     return e;
   }
-  const bool vec = vectors(a.D, a.dtype, {a.s, a.dy, a.ds, a.dx});
+  const bool vec = vectors(a.D, a.dtype, {a.s, a.dy, a.ds, a.dx, a.weight});
   if (a.dtype == SANATAN_F32) return vec ? bwd<float, true>(a, st) : bwd<float, false>(a, st);
   return vec ? bwd<__nv_bfloat16, true>(a, st) : bwd<__nv_bfloat16, false>(a, st);
 }

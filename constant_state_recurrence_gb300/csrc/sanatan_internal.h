@@ -313,7 +313,7 @@ struct ConvArgs {
   const float* s0 = nullptr;       // [B, K - 1, D] or null
   void* y = nullptr;
   float* s_out = nullptr;          // [B, K - 1, D] or null (the step's state)
-  int runs = 0;                    // of a sequence (set by the launcher)
+  int run = 0, runs = 0;           // tokens of a run, runs of a sequence (set by the launcher)
 };
 struct ConvBwdArgs {
   const void* x = nullptr;

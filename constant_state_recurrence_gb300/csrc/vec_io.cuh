@@ -45,6 +45,34 @@ struct Vec {
   __device__ __forceinline__ void store(E* p) const { *reinterpret_cast<type*>(p) = raw; }
 };
 
+// V neighbouring floats (16 bytes at a time where V allows it).
+template <int V>
+__device__ __forceinline__ void load_floats(const float* p, float (&f)[V]) {
+  constexpr int N = V % 4 == 0 ? 4 : V;
+#pragma unroll
+  for (int i = 0; i < V; i += N) {
+    Vec<float, N> v;
+    float g[N];
+    v.load(p + i);
+    v.get(g);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[i + j] = g[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_floats(float* p, const float (&f)[V]) {
+  constexpr int N = V % 4 == 0 ? 4 : V;
+#pragma unroll
+  for (int i = 0; i < V; i += N) {
+    Vec<float, N> v;
+    float g[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) g[j] = f[i + j];
+    v.put(g);
+    v.store(p + i);
+  }
+}
+
 inline bool at_bytes(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 }  // namespace sanatan
