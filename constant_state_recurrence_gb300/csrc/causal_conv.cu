@@ -29,9 +29,8 @@ using namespace lanes;
 
 constexpr int kThreads = 128;
 constexpr int kRunLong = 64, kRunShort = 16;  // tokens of a thread, forward
-constexpr int kRunBwd = 32;
 constexpr int kStep = 4;     // tokens of a group of copies
-constexpr int kGroupsFwd = 4, kGroupsBwd = 3;  // groups of a ring
+constexpr int kGroupsFwd = 4, kGroupsBwd = 4;  // groups of a ring
 constexpr int kLanes = 32, kRows = 8;  // backward block: channels x runs
 constexpr int kParts = kConvParts;
 
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(kLanes* kRows, KM <= 4 ? 2 : 1) conv_bwd_kerne
        row += static_cast<int64_t>(gridDim.y) * kRows) {
     const int b = static_cast<int>(row / a.runs);
     const int n = length_of(a.lens, b, a.T);
-    const int t0 = static_cast<int>(row % a.runs) * kRunBwd, end = min(t0 + kRunBwd, a.T);
+    const int t0 = static_cast<int>(row % a.runs) * a.run, end = min(t0 + a.run, a.T);
     const int64_t at = static_cast<int64_t>(b) * a.T * a.D + c;
     const int64_t state = static_cast<int64_t>(b) * (K - 1) * a.D + c;
     const E* x = static_cast<const E*>(a.x) + static_cast<int64_t>(b) * a.T * a.ldx + c;
@@ -461,19 +460,35 @@ cudaError_t fwd(ConvArgs a, cudaStream_t st) {
   return launch(conv_fwd_kernel<E, KM, V>, dim3(blocks_of(rows * vecs)), kThreads, shared, st, a);
 }
 
-// Blocks of runs: each takes several, so that the weights' gradients are added up in registers;
-// two blocks an SM at most.
-int parts_of(int B, int runs, int D, int V) {
-  const int64_t blocks = (static_cast<int64_t>(B) * runs - 1) / kRows + 1;
+// Blocks of runs (kRows of them a block at a time) and tokens of a run, backward: as many
+// blocks as two an SM make, each of which adds up the weights' gradients in registers over its
+// runs; and of the run lengths the one that costs a thread the fewest tokens, those that it
+// reads twice (K - 1 before a run and behind it) among them.
+struct Runs {
+  int n, run, runs;
+};
+Runs runs_of(int B, int T, int D, int K, int V) {
   const int64_t columns = (D - 1) / (V * kLanes) + 1;
-  return static_cast<int>(
-      std::min<int64_t>(std::min<int64_t>(kParts, blocks), std::max<int64_t>(1, 2 * 152 / columns)));
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(kParts, 2 * 152 / columns));
+  Runs best{1, 16, std::max(1, T / 16 + (T % 16 != 0))};  // (one run: the state's gradient)
+  int64_t least = INT64_MAX;
+  for (int run = 16; run <= 64; run += 8) {
+    const int64_t runs = std::max(1, T / run + (T % run != 0));
+    const int64_t rounds = (B * runs - 1) / (blocks * kRows) + 1, cost = rounds * (run + 3 * K);
+    if (cost < least) {
+      least = cost;
+      best = {static_cast<int>(std::min(blocks, (B * runs - 1) / kRows + 1)), run,
+              static_cast<int>(runs)};
+    }
+  }
+  return best;
 }
 
 template <typename E, int KM, int V>
 cudaError_t bwd(ConvBwdArgs a, cudaStream_t st) {
-  a.runs = std::max(1, (a.T + kRunBwd - 1) / kRunBwd);  // (the state's gradient without tokens)
-  const int n = parts_of(a.B, a.runs, a.D, V);
+  const Runs r = runs_of(a.B, a.T, a.D, a.K, V);
+  a.run = r.run, a.runs = r.runs;
+  const int n = r.n;
   const bool sums = a.dw != nullptr || a.dbias != nullptr;
   if (!sums) a.parts = nullptr;
   constexpr size_t shared = Ring<E, V, 2, kGroupsBwd, kLanes * kRows>::kShared;
@@ -528,8 +543,7 @@ bool words(int V, int D, int64_t ldx, std::initializer_list<const void*> tensors
 
 size_t causal_conv_bwd_workspace_bytes(int B, int T, int D, int K) {
   if (B <= 0 || T < 0 || D <= 0 || K < 1) return 0;
-  // (one channel a thread has the fewest blocks of runs, four the most)
-  const int n = parts_of(B, std::max(1, T / kRunBwd + (T % kRunBwd != 0)), D, 4);
+  const int n = std::max(runs_of(B, T, D, K, 1).n, runs_of(B, T, D, K, 4).n);
   return sizeof(float) * static_cast<size_t>(n) * (K + 1) * static_cast<size_t>(D);
 }
 

@@ -331,7 +331,7 @@ struct ConvBwdArgs {
   float* dbias = nullptr;          // [D] or null
   float* ds0 = nullptr;            // [B, K - 1, D] or null
   float* parts = nullptr;          // causal_conv_bwd_workspace_bytes
-  int runs = 0;
+  int run = 0, runs = 0;
 };
 size_t causal_conv_bwd_workspace_bytes(int B, int T, int D, int K);
 cudaError_t causal_conv_fwd_launch(const ConvArgs& a, cudaStream_t st);

@@ -168,8 +168,12 @@ __global__ void __launch_bounds__(kThreads) selective_fwd_kernel(SelectiveArgs a
 
 constexpr int kStepRows = 4;  // sequences of a thread, their states under way together
 
-template <typename E, int L>
+// One token: four sequences of a channel at a time, L neighbouring lanes a channel.  A lane's
+// own sequence of the four is the one whose sum it ends with; it forms delta and the gate of
+// that one alone, and the others' come by shuffles.  WORDS: B and C four values at a time.
+template <typename E, int L, bool WORDS>
 __global__ void __launch_bounds__(kThreads) selective_step_kernel(SelectiveArgs a) {
+  using M = Meet<4, 1, L / 2>;
   const int lane = threadIdx.x % 32, l = lane % L;
   const int64_t channels = (static_cast<int64_t>(a.D) + Geo<L>::CB - 1) / Geo<L>::CB;
   const int d = static_cast<int>(blockIdx.x % channels) * Geo<L>::CB +
@@ -184,42 +188,58 @@ __global__ void __launch_bounds__(kThreads) selective_step_kernel(SelectiveArgs 
   for (int r = 0; r < kStepRows; ++r)
     if (b0 + r < a.B) st.load(a.h_out + (b0 + r) * slab, h[r]);
   st.load(a.A, A);
-  const float bias = there && a.dt_bias != nullptr ? a.dt_bias[d] : 0.0f;
-  const float skip = there && a.skip != nullptr ? a.skip[d] : 0.0f;
+  const int own = b0 + M::index(lane);
+  const bool real = there && own < a.B;
+  float u = 0.0f, delta = 0.0f, z = 0.0f;
+  if (real) {
+    const int64_t at = static_cast<int64_t>(own) * a.D + d;
+    u = load_as_float(static_cast<const E*>(a.u) + at);
+    delta = load_as_float(static_cast<const E*>(a.dt) + at);
+    if (a.dt_bias != nullptr) delta += a.dt_bias[d];
+    if (a.z != nullptr) z = load_as_float(static_cast<const E*>(a.z) + own * a.ldz + d);
+  }
+  if (a.softplus) {
+    float other;
+    upk2(softplus_pair(pk2(delta, delta)), delta, other);
+  }
+  float y[kStepRows];
 #pragma unroll
   for (int r = 0; r < kStepRows; ++r) {
-    const int b = b0 + r;
-    if (b >= a.B) break;
-    float u = 0.0f, delta = 0.0f, z = 0.0f;
-    if (there) {
-      u = load_as_float(static_cast<const E*>(a.u) + static_cast<int64_t>(b) * a.D + d);
-      delta = load_as_float(static_cast<const E*>(a.dt) + static_cast<int64_t>(b) * a.D + d) + bias;
-      if (a.z != nullptr) z = load_as_float(static_cast<const E*>(a.z) + b * a.ldz + d);
+    // (index() has the lane's first bit stand for 2, the second for 1)
+    const int from = (lane & ~3) | (r >> 1) | (r & 1) << 1;
+    const float dr = __shfl_sync(0xffffffffu, delta, from);
+    const float du = dr * __shfl_sync(0xffffffffu, u, from), x = dr * kLog2e;
+    y[r] = 0.0f;
+    if (b0 + r >= a.B) continue;
+    float Bv[kStates] = {}, Cv[kStates] = {};
+    const E* Bm = static_cast<const E*>(a.Bm) + (b0 + r) * a.ldb + kStates * l;
+    const E* Cm = static_cast<const E*>(a.Cm) + (b0 + r) * a.ldc + kStates * l;
+    if (WORDS) {
+      if (kStates * l < a.N) {
+        Vec<E, kStates> v;
+        v.load(Bm);
+        v.get(Bv);
+        v.load(Cm);
+        v.get(Cv);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kStates; ++j)
+        if (kStates * l + j < a.N) Bv[j] = load_as_float(Bm + j), Cv[j] = load_as_float(Cm + j);
     }
-    if (a.softplus) {
-      float other;
-      upk2(softplus_pair(pk2(delta, delta)), delta, other);
-    }
-    float y = 0.0f;
 #pragma unroll
     for (int j = 0; j < kStates; ++j) {
-      const int n = kStates * l + j;
-      float Bv = 0.0f, Cv = 0.0f;
-      if (n < a.N) {
-        Bv = load_as_float(static_cast<const E*>(a.Bm) + b * a.ldb + n);
-        Cv = load_as_float(static_cast<const E*>(a.Cm) + b * a.ldc + n);
-      }
-      h[r][j] = fmaf(exp2_near(delta * kLog2e * A[j]), h[r][j], delta * u * Bv);
-      y = fmaf(h[r][j], Cv, y);
+      h[r][j] = fmaf(exp2_near(x * A[j]), h[r][j], du * Bv[j]);
+      y[r] = fmaf(h[r][j], Cv[j], y[r]);
     }
-    st.store(a.h_out + b * slab, pk2(h[r][0], h[r][1]), pk2(h[r][2], h[r][3]));
-#pragma unroll
-    for (int bit = 1; bit < L; bit *= 2) y += __shfl_xor_sync(0xffffffffu, y, bit);
-    y = fmaf(skip, u, y);
-    if (a.z != nullptr) y *= __fdividef(z, 1.0f + __expf(-z));
-    if (l == 0 && there)
-      static_cast<E*>(a.y)[static_cast<int64_t>(b) * a.D + d] = store_from_float<E>(y);
+    st.store(a.h_out + (b0 + r) * slab, pk2(h[r][0], h[r][1]), pk2(h[r][2], h[r][3]));
   }
+  M::sum(y, lane);
+  if (!M::first(lane) || !real) return;
+  float out = y[0];
+  if (a.skip != nullptr) out = fmaf(a.skip[d], u, out);
+  if (a.z != nullptr) out *= z * sigmoid(z);
+  static_cast<E*>(a.y)[static_cast<int64_t>(own) * a.D + d] = store_from_float<E>(out);
 }
 
 template <typename E, int L, bool ALIGNED>
@@ -243,7 +263,10 @@ cudaError_t fwd(const SelectiveArgs& a, cudaStream_t st) {
 template <typename E, int L>
 cudaError_t step(const SelectiveArgs& a, cudaStream_t st) {
   const int64_t channels = (a.D - 1) / Geo<L>::CB + 1, rows = (a.B - 1) / kStepRows + 1;
-  return launch(selective_step_kernel<E, L>, channels * rows, kThreads, 0, st, a);
+  const bool word = a.N % kStates == 0 && a.ldb % kStates == 0 && a.ldc % kStates == 0 &&
+                    at_bytes(a.Bm, kStates * sizeof(E)) && at_bytes(a.Cm, kStates * sizeof(E));
+  return word ? launch(selective_step_kernel<E, L, true>, channels * rows, kThreads, 0, st, a)
+              : launch(selective_step_kernel<E, L, false>, channels * rows, kThreads, 0, st, a);
 }
 
 }  // namespace
