@@ -313,7 +313,7 @@ struct Stage {
   __device__ __forceinline__ void place(const SelectiveArgs& a, int k, int dir) {
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
-      int c = threadIdx.x + i * kThreads;
+      int c = threadIdx.x % kThreads + i * kThreads;
       from[i] = reinterpret_cast<const char*>(x[0]);
       step[i] = 0, to[i] = 0, token[i] = kNever, bytes[i] = 0;
       int base = 0;
@@ -367,7 +367,7 @@ struct Stage {
       if (x[q] == nullptr) continue;
 #pragma unroll
       for (int i = 0; i < (q < NT ? kOne : kPairOne); ++i) {
-        const int c = threadIdx.x + i * kThreads;
+        const int c = threadIdx.x % kThreads + i * kThreads;
         const int t = q < NT ? c / G::CB : c / G::NP, v = q < NT ? d0 + c % G::CB : c % G::NP;
         const bool real = t < kTile && t < left && v < (q < NT ? D : N);
         // (one load whether real or not: a branch would wait for it)
@@ -387,7 +387,7 @@ struct Stage {
       char* base = buffer + (q < NT ? q * kCell : NT * kCell + (q - NT) * kPair);
 #pragma unroll
       for (int i = 0; i < (q < NT ? kOne : kPairOne); ++i) {
-        const int c = threadIdx.x + i * kThreads;
+        const int c = threadIdx.x % kThreads + i * kThreads;
         const int t = q < NT ? c / G::CB : c / G::NP, v = q < NT ? c % G::CB : c % G::NP;
         if (t < kTile)
           *reinterpret_cast<E*>(base + t * (q < NT ? kPitch : kPairPitch) + v * kSize) =
@@ -428,7 +428,7 @@ __device__ __forceinline__ void Stage<E, L, ALIGNED, NT>::pairs_to_float(
     const char* buffer, int N, float (*pairs)[2][ORDERS][WIDE]) {
 #pragma unroll
   for (int i = 0; i < G::kQuadItems; ++i) {
-    const int k = threadIdx.x + i * kThreads, q = k % L, which = k / L % 2, t = k / (2 * L);
+    const int k = threadIdx.x % kThreads + i * kThreads, q = k % L, which = k / L % 2, t = k / (2 * L);
     if (G::kQuads % kThreads != 0 && k >= G::kQuads) break;
     Vec<E, 4> v;
     float f[4];

@@ -4,19 +4,28 @@
 namespace sanatan {
 namespace {
 
+constexpr int kFwdThreads = 2 * kThreads;
+
 template <typename E, int L, bool ALIGNED, bool STATE>
 struct FwdShared {
   using G = Geo<L>;
   using Tiles = Stage<E, L, ALIGNED, STATE ? 2 : 3>;  // u, dt, z
-  float4 cells[kWarps][kTile][G::kRowPitch];          // delta, delta, delta u, delta u
+  float4 cells[2][kWarps][kTile][G::kRowPitch];       // delta, delta, delta u, delta u
   float pairs[2][kTile][2][1][G::NP];
-  float ys[kWarps][kTile][G::CW];
-  char raw[3][Tiles::kBytes];
+  float ys[2][kWarps][kTile][G::CW];
+  char raw[2][Tiles::kBytes];
 };
 
 // STATE: only the segment's result from a zero state, and its sum of delta.
+//
+// Warps 0 .. 3 walk tile k.  Warps 4 .. 7 work beside them, a warp for the channels of one of
+// the first four: they have tile k + 2 copied, form the cells of tile k + 1 and finish the
+// outputs of tile k - 1.  All meet once a tile.  (Whole sequences leave an SM ten walking
+// warps at the training shape, and each is as slow as its own instructions: walking and the
+// rest by the same four warps took 604 us.)
 template <typename E, int L, bool ALIGNED, bool STATE>
-__global__ void __launch_bounds__(kThreads) selective_fwd_kernel(SelectiveArgs a) {
+__global__ void __launch_bounds__(kFwdThreads, L <= 8 ? 3 : 1)
+    selective_fwd_kernel(SelectiveArgs a) {
   using G = Geo<L>;
   constexpr int W = G::W;
   using Sm = FwdShared<E, L, ALIGNED, STATE>;
@@ -24,41 +33,80 @@ __global__ void __launch_bounds__(kThreads) selective_fwd_kernel(SelectiveArgs a
   extern __shared__ float4 smem4[];
   Sm& sm = *reinterpret_cast<Sm*>(smem4);
   const Place<L> at(a);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, l = lane / G::CW;
-  const int mine = lane % G::CW;
-  const int d0 = at.cb * G::CB, w0 = d0 + warp * G::CW, d = w0 + mine;
-  // The lane's cells: W channels from cell_c of the warp's, tokens cell_t, cell_t + ...
-  constexpr int kPer = G::CW / W, kStep = 32 / kPer;
-  const int cell_c = lane % kPer * W, cell_t = lane / kPer, cell_d = w0 + cell_c;
-  const StatePlace st(d, l, a.D, a.N, a.vec);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 % kWarps;
+  const bool walks = threadIdx.x < kThreads;
+  const int d0 = at.cb * G::CB, w0 = d0 + warp * G::CW;
   wait_for_previous();
   const int n = length_of(a.lens, at.b, a.T);
   const int64_t slab = static_cast<int64_t>(a.D) * a.N, row0 = static_cast<int64_t>(at.b) * a.T;
+  const int64_t part = static_cast<int64_t>(at.b) * a.segments + at.seg;
+  const int live = min(at.k1, (n + kTile - 1) / kTile);  // tiles from here on hold no token
+  if (walks) {
+    const int l = lane / G::CW, mine = lane % G::CW;
+    const StatePlace st(w0 + mine, l, a.D, a.N, a.vec);
+    uint64_t A0, A1, h0, h1;
+    {
+      float f[kStates];
+      st.load(a.A, f);
+      A0 = pk2(f[0] * kLog2e, f[1] * kLog2e), A1 = pk2(f[2] * kLog2e, f[3] * kLog2e);
+      const float* from = STATE             ? nullptr
+                          : a.segments > 1 ? a.carry + part * slab
+                                           : (a.h0 != nullptr ? a.h0 + at.b * slab : nullptr);
+      f[0] = f[1] = f[2] = f[3] = 0.0f;
+      if (from != nullptr) st.load(from, f);
+      h0 = pk2(f[0], f[1]), h1 = pk2(f[2], f[3]);
+    }
+    if (at.k0 < live) {
+      __syncthreads();  // (the first tile's copies)
+      __syncthreads();  // (its cells)
+    }
+    for (int k = at.k0; k < live; ++k) {
+      if (!STATE && a.marks != nullptr)
+        st.store(a.marks + (static_cast<int64_t>(at.b) * at.tiles + k) * slab, h0, h1);
+      const float(*pairs)[2][1][G::NP] = sm.pairs[k & 1];
+      const float4(*cells)[G::kRowPitch] = sm.cells[k & 1][warp];
+      Decays decays;
+#pragma unroll
+      for (int g = 0; g < kTile; g += 4) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const ulonglong2 c = reinterpret_cast<const ulonglong2&>(cells[g + i][mine]);
+          const ulonglong2 Bv =
+              reinterpret_cast<const ulonglong2&>(pairs[g + i][0][0][kStates * l]);
+          const uint64_t a0 = exp2_pair(fmul2(c.x, A0)), a1 = exp2_pair(fmul2(c.x, A1));
+          h0 = ffma2(a0, h0, fmul2(c.y, Bv.x));
+          h1 = ffma2(a1, h1, fmul2(c.y, Bv.y));
+          decays.add(a0, a1, c.x);
+          if (!STATE) {
+            const ulonglong2 Cv =
+                reinterpret_cast<const ulonglong2&>(pairs[g + i][1][0][kStates * l]);
+            v[i] = sum2(ffma2(h1, Cv.y, fmul2(h0, Cv.x)));
+          }
+        }
+        if (!STATE) {
+          using M = Meet<4, G::CW, 16>;
+          M::sum(v, lane);
+          if (M::first(lane))
+#pragma unroll
+            for (int i = 0; i < M::kLeft; ++i)
+              sm.ys[k & 1][warp][g + M::index(lane) + i][mine] = v[i];
+        }
+      }
+      decays.put_right(A0, A1, h0, h1);
+      __syncthreads();
+    }
+    if (STATE)
+      st.store(a.carry + part * slab, h0, h1);
+    else if (a.h_out != nullptr && at.seg == a.segments - 1)
+      st.store(a.h_out + at.b * slab, h0, h1);
+    return;
+  }
+  // The lane's cells: W channels from cell_c of the warp's, tokens cell_t, cell_t + ...
+  constexpr int kPer = G::CW / W, kStep = 32 / kPer;
+  const int cell_c = lane % kPer * W, cell_t = lane / kPer, cell_d = w0 + cell_c;
   E* Y = static_cast<E*>(a.y);
   const bool gated = !STATE && a.z != nullptr;
-  const int live = min(at.k1, (n + kTile - 1) / kTile);  // tiles from here on hold no token
-  Tiles tiles;
-  if constexpr (STATE)
-    tiles.init({a.u, a.dt, a.Bm, nullptr}, {a.D, a.D, a.ldb, 0}, a, row0, n, d0, at.k0, 1);
-  else
-    tiles.init({a.u, a.dt, a.z, a.Bm, a.Cm}, {a.D, a.D, a.ldz, a.ldb, a.ldc}, a, row0, n, d0,
-               at.k0, 1);
-  // Tile k is worked on while B and C of tile k + 1 become floats and tile k + 2 is under way.
-  if (at.k0 < live) tiles.begin(sm.raw[0], at.k0), tiles.end(sm.raw[0]);
-  if (at.k0 + 1 < live) tiles.begin(sm.raw[1], at.k0 + 1), tiles.end(sm.raw[1]);
-  uint64_t A0, A1, h0, h1;
-  {
-    float f[kStates];
-    st.load(a.A, f);
-    A0 = pk2(f[0] * kLog2e, f[1] * kLog2e), A1 = pk2(f[2] * kLog2e, f[3] * kLog2e);
-    const float* from = STATE ? nullptr
-                        : a.segments > 1
-                            ? a.carry + (static_cast<int64_t>(at.b) * a.segments + at.seg) * slab
-                            : (a.h0 != nullptr ? a.h0 + at.b * slab : nullptr);
-    f[0] = f[1] = f[2] = f[3] = 0.0f;
-    if (from != nullptr) st.load(from, f);
-    h0 = pk2(f[0], f[1]), h1 = pk2(f[2], f[3]);
-  }
   float bias[W], skip[W], sum[W];
 #pragma unroll
   for (int j = 0; j < W; ++j) {
@@ -67,102 +115,86 @@ __global__ void __launch_bounds__(kThreads) selective_fwd_kernel(SelectiveArgs a
     skip[j] = there && a.skip != nullptr ? a.skip[cell_d + j] : 0.0f;
     sum[j] = 0.0f;
   }
-  if (at.k0 < live) {
-    copy_wait<0>();
-    __syncthreads();
-    Tiles::pairs_to_float(sm.raw[0], a.N, sm.pairs[at.k0 & 1]);
-  }
-  int now = 0;  // the buffer of tile k
-  for (int k = at.k0; k < live; ++k) {
-    const int next = now == 2 ? 0 : now + 1, after = next == 2 ? 0 : next + 1;
-    copy_wait<0>();
-    __syncthreads();
-    if (k + 2 < live) tiles.begin(sm.raw[after], k + 2);
-    if (k + 1 < live) Tiles::pairs_to_float(sm.raw[next], a.N, sm.pairs[(k + 1) & 1]);
+  Tiles tiles;
+  if constexpr (STATE)
+    tiles.init({a.u, a.dt, a.Bm, nullptr}, {a.D, a.D, a.ldb, 0}, a, row0, n, d0, at.k0, 1);
+  else
+    tiles.init({a.u, a.dt, a.z, a.Bm, a.Cm}, {a.D, a.D, a.ldz, a.ldb, a.ldc}, a, row0, n, d0,
+               at.k0, 1);
+  struct Kept {
     float u[G::kItems][W], z[G::kItems][W];
+  };
+  auto prepare = [&](int k, Kept& kept) {
+    Tiles::pairs_to_float(sm.raw[k & 1], a.N, sm.pairs[k & 1]);
 #pragma unroll
     for (int i = 0; i < G::kItems; ++i) {
       const int t = cell_t + i * kStep;
       if (G::kCells % 32 != 0 && t >= kTile) break;
       float delta[W];
-      Tiles::get(sm.raw[now], 0, t, warp * G::CW + cell_c, u[i]);
-      Tiles::get(sm.raw[now], 1, t, warp * G::CW + cell_c, delta);
-      if (gated) Tiles::get(sm.raw[now], 2, t, warp * G::CW + cell_c, z[i]);
+      Tiles::get(sm.raw[k & 1], 0, t, warp * G::CW + cell_c, kept.u[i]);
+      Tiles::get(sm.raw[k & 1], 1, t, warp * G::CW + cell_c, delta);
+      if (gated) Tiles::get(sm.raw[k & 1], 2, t, warp * G::CW + cell_c, kept.z[i]);
       steps<W>(delta, bias, a.softplus, k * kTile + t < n);
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         if (STATE) sum[j] += delta[j];
-        const float du = delta[j] * u[i][j];
-        sm.cells[warp][t][cell_c + j] = make_float4(delta[j], delta[j], du, du);
+        const float du = delta[j] * kept.u[i][j];
+        sm.cells[k & 1][warp][t][cell_c + j] = make_float4(delta[j], delta[j], du, du);
       }
     }
-    if (!STATE && a.marks != nullptr)
-      st.store(a.marks + (static_cast<int64_t>(at.b) * at.tiles + k) * slab, h0, h1);
-    __syncwarp();
-    const float(*pairs)[2][1][G::NP] = sm.pairs[k & 1];
-    Decays decays;
+  };
+  auto finish = [&](int k, const Kept& kept) {
 #pragma unroll
-    for (int g = 0; g < kTile; g += 4) {
-      float v[4];
+    for (int i = 0; i < G::kItems; ++i) {
+      const int tl = cell_t + i * kStep, t = k * kTile + tl;
+      if (G::kCells % 32 != 0 && tl >= kTile) break;
+      float y[W];
+      Vec<float, W> v;
+      v.load(&sm.ys[k & 1][warp][tl][cell_c]);
+      v.get(y);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const ulonglong2 c = reinterpret_cast<const ulonglong2&>(sm.cells[warp][g + i][mine]);
-        const ulonglong2 Bv = reinterpret_cast<const ulonglong2&>(pairs[g + i][0][0][kStates * l]);
-        const uint64_t a0 = exp2_pair(fmul2(c.x, A0)), a1 = exp2_pair(fmul2(c.x, A1));
-        h0 = ffma2(a0, h0, fmul2(c.y, Bv.x));
-        h1 = ffma2(a1, h1, fmul2(c.y, Bv.y));
-        decays.add(a0, a1, c.x);
-        if (!STATE) {
-          const ulonglong2 Cv = reinterpret_cast<const ulonglong2&>(pairs[g + i][1][0][kStates * l]);
-          v[i] = sum2(ffma2(h1, Cv.y, fmul2(h0, Cv.x)));
-        }
+      for (int j = 0; j < W; ++j) {
+        y[j] = fmaf(skip[j], kept.u[i][j], y[j]);
+        if (gated) y[j] *= kept.z[i][j] * sigmoid(kept.z[i][j]);
+        if (t >= n) y[j] = 0.0f;
       }
-      if (!STATE) {
-        using M = Meet<4, G::CW, 16>;
-        M::sum(v, lane);
-        if (M::first(lane))
-#pragma unroll
-          for (int i = 0; i < M::kLeft; ++i) sm.ys[warp][g + M::index(lane) + i][mine] = v[i];
-      }
+      if (t < a.T) store_cells<E, W, ALIGNED>(Y + (row0 + t) * a.D, cell_d, a.D, y);
     }
-    decays.put_right(A0, A1, h0, h1);
-    __syncwarp();
-    if (!STATE) {
-#pragma unroll
-      for (int i = 0; i < G::kItems; ++i) {
-        const int tl = cell_t + i * kStep, t = k * kTile + tl;
-        if (G::kCells % 32 != 0 && tl >= kTile) break;
-        float y[W];
-        Vec<float, W> v;
-        v.load(&sm.ys[warp][tl][cell_c]);
-        v.get(y);
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          y[j] = fmaf(skip[j], u[i][j], y[j]);
-          if (gated) y[j] *= z[i][j] * sigmoid(z[i][j]);
-          if (t >= n) y[j] = 0.0f;
-        }
-        if (t < a.T) store_cells<E, W, ALIGNED>(Y + (row0 + t) * a.D, cell_d, a.D, y);
-      }
-    }
-    if (k + 2 < live) tiles.end(sm.raw[after]);
-    now = next;
+  };
+  Kept before, now, next;  // of tiles k - 1, k, k + 1
+  if (at.k0 < live) {
+    tiles.begin(sm.raw[at.k0 & 1], at.k0);
+    tiles.end(sm.raw[at.k0 & 1]);
+    copy_wait<0>();
+    __syncthreads();
+    if (at.k0 + 1 < live) tiles.begin(sm.raw[(at.k0 + 1) & 1], at.k0 + 1);
+    prepare(at.k0, now);
+    if (at.k0 + 1 < live) tiles.end(sm.raw[(at.k0 + 1) & 1]);
+    copy_wait<0>();
+    __syncthreads();
+  }
+  for (int k = at.k0; k < live; ++k) {
+    if (k + 2 < live) tiles.begin(sm.raw[k & 1], k + 2);
+    if (k + 1 < live) prepare(k + 1, next);
+    if (!STATE && k > at.k0) finish(k - 1, before);
+    if (k + 2 < live) tiles.end(sm.raw[k & 1]);
+    copy_wait<0>();
+    __syncthreads();
+    before = now, now = next;
   }
   if constexpr (STATE) {
-    st.store(a.carry + (static_cast<int64_t>(at.b) * a.segments + at.seg) * slab, h0, h1);
     // the lanes of a channel, by halves
 #pragma unroll
     for (int j = 0; j < W; ++j) {
 #pragma unroll
       for (int bit = kPer; bit < 32; bit *= 2) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], bit);
-      if (cell_t == 0 && cell_d + j < a.D)
-        a.sums[(static_cast<int64_t>(at.b) * a.segments + at.seg) * a.D + cell_d + j] = sum[j];
+      if (cell_t == 0 && cell_d + j < a.D) a.sums[part * a.D + cell_d + j] = sum[j];
     }
   } else {
+    if (at.k0 < live) finish(live - 1, before);
     const float zero[W] = {};
     for (int t = max(at.k0, live) * kTile + cell_t; t < min(at.k1 * kTile, a.T); t += kStep)
       store_cells<E, W, ALIGNED>(Y + (row0 + t) * a.D, cell_d, a.D, zero);  // without a token
-    if (a.h_out != nullptr && at.seg == a.segments - 1) st.store(a.h_out + at.b * slab, h0, h1);
   }
 }
 
@@ -247,12 +279,12 @@ cudaError_t fwd_of(const SelectiveArgs& a, cudaStream_t st) {
   const int64_t blocks = static_cast<int64_t>(a.B) * a.blocks * a.segments;
   if (a.segments > 1) {
     cudaError_t e =
-        launch(selective_fwd_kernel<E, L, ALIGNED, true>, blocks, kThreads,
+        launch(selective_fwd_kernel<E, L, ALIGNED, true>, blocks, kFwdThreads,
                sizeof(FwdShared<E, L, ALIGNED, true>), st, a);
     if (e == cudaSuccess) e = launch_carry(a, a.h0, false, st);
     if (e != cudaSuccess) return e;
   }
-  return launch(selective_fwd_kernel<E, L, ALIGNED, false>, blocks, kThreads,
+  return launch(selective_fwd_kernel<E, L, ALIGNED, false>, blocks, kFwdThreads,
                 sizeof(FwdShared<E, L, ALIGNED, false>), st, a);
 }
 template <typename E, int L>
