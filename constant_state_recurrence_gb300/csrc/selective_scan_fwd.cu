@@ -315,7 +315,7 @@ int selective_blocks(int D, int N) { return (D - 1) / (kThreads / selective_lane
 
 // Segments of a sequence, and their tiles.  One, where whole sequences make two blocks or more
 // an SM (a split walks the tokens twice; training shape, 384 blocks: forward 565 us, in eight
-// segments 606, backward 1466 and 1572); else about eight blocks an SM (one prompt of 32768
+// segments 606, backward 1466 and 1572); else about six blocks an SM (one prompt of 32768
 // tokens, 48 blocks: forward 2800 us whole, 1293 in 8 segments, 675 in 24), of four tiles or
 // more.  More than 64 states: always one.
 int selective_segments(int B, int T, int D, int N, int* tiles_per_segment) {
@@ -324,7 +324,7 @@ int selective_segments(int B, int T, int D, int N, int* tiles_per_segment) {
   constexpr int64_t kSms = 152;
   int64_t S = 1;
   if (blocks < 2 * kSms && selective_lanes(N) < 32)
-    S = std::min<int64_t>((8 * kSms - 1) / blocks + 1, tiles / 4);
+    S = std::min<int64_t>((6 * kSms - 1) / blocks + 1, tiles / 4);
   S = std::max<int64_t>(S, 1);
   *tiles_per_segment = static_cast<int>((tiles - 1) / S + 1);
   return (tiles - 1) / *tiles_per_segment + 1;
