@@ -7,17 +7,23 @@
 //
 // Bound: bytes (two tensors forward, three backward).  A thread has V neighbouring
 // channels of a run of tokens and keeps the last K - 1 inputs in registers, so that a value is
-// loaded once but for K - 1 tokens before a run (and, backward, behind it).  Backward, the
-// forward's sum is formed again; the thread walks its run once, with the K unfinished dx in
-// registers: dc_t goes into each, and dx_{t-K+1} is then done.  The weights' gradients stay in
-// registers over all runs of a thread; blocks leave partial sums, and a second kernel adds
-// them in a fixed order (no atomics: the same call gives the same bits).
+// loaded once but for K - 1 tokens before a run (and, backward, behind it).  Loads are
+// asynchronous copies into a ring of the thread's own in shared memory, twelve tokens ahead:
+// registers for as many loads would leave few threads.  Arithmetic is packed, two channels an
+// instruction.  Backward, the forward's sum is formed again; the thread walks its run once,
+// with the K unfinished dx in registers: dc_t goes into each, and dx_{t-K+1} is then done.
+// The weights' gradients stay in registers over all runs of a thread; blocks leave partial
+// sums, and a second kernel adds them in a fixed order (no atomics: the same call gives the same
+// bits).  B 8 T 4096 D 1536 K 4 bf16, x a half of wider rows, GB300: forward 44 us, 4.6 TB/s
+// (0.67 of the measured copy rate), backward 82, 3.7 TB/s (0.54).  With loads into
+// registers, four tokens ahead, and weights loaded value by value every sixteen tokens (each such
+// load of a warp touches 32 lines) 92 and 153.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
 
-#include "lanes.cuh"
 #include "copy_async.cuh"
+#include "lanes.cuh"
 #include "pdl.cuh"
 #include "sanatan_internal.h"
 #include "vec_io.cuh"

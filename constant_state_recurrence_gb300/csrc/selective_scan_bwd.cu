@@ -2,9 +2,12 @@
 //
 // A tile is walked forward from its mark to the states before every fourth token, which are put
 // aside, then back by fours: decays and states of four tokens are formed again, then their
-// gradients.  Bound: the wavefronts of shared memory, 25 to 30 a token and warp (cells, B, C
-// and the shuffles).  With all decays in registers and all states in shared memory they were 42,
-// and the backward of B 8 T 4096 D 1536 N 16 bf16 1466 us.
+// gradients.  Bound: instructions, 129 a token and warp (a quarter of them the sums over
+// channels and states), half of the issue slots used by the ten warps that an SM has at the
+// training shape.  With all decays of a tile in registers and all states in shared memory it was
+// the latter's wavefronts, 42 a token and warp: 1466 us instead of 1422, one prompt of 32768
+// tokens 1840 instead of 1567.  Cells as pairs twice over, without the moves that make pairs of
+// them: 1563.
 #include "selective_scan.cuh"
 
 namespace sanatan {

@@ -314,10 +314,11 @@ int selective_lanes(int N) {
 int selective_blocks(int D, int N) { return (D - 1) / (kThreads / selective_lanes(N)) + 1; }
 
 // Segments of a sequence, and their tiles.  One, where whole sequences make two blocks or more
-// an SM (a split walks the tokens twice; training shape, 384 blocks: forward 565 us, in eight
-// segments 606, backward 1466 and 1572); else about six blocks an SM (one prompt of 32768
-// tokens, 48 blocks: forward 2800 us whole, 1293 in 8 segments, 675 in 24), of four tiles or
-// more.  More than 64 states: always one.
+// an SM (a split walks the tokens twice; training shape, 384 blocks: forward 439 us, backward
+// 1422 and, when both walked slower, 1466 whole and 1572 in eight segments); else about six
+// blocks an SM (one prompt of 32768 tokens, 48 blocks: 10, 13, 19 and 38 segments forward 852, 747,
+// 616 and 622 us, backward 2330, 1847, 1484 and 1471), of four tiles or more.  More than 64
+// states: always one.
 int selective_segments(int B, int T, int D, int N, int* tiles_per_segment) {
   const int tiles = std::max(1, (T - 1) / kTile + 1);
   const int64_t blocks = static_cast<int64_t>(B) * selective_blocks(D, N);

@@ -627,13 +627,15 @@ SANATAN_API int sanatan_causal_conv_step(float* state, const void* x, int64_t ld
  *     y_t = (sum_n C_t[n] h_t[n] + skip[d] u) * g,  g = 1 or (with z) z / (1 + exp(-z)).
  *   u, dt, y [B, T, D] dtype;  z [B, T, D] dtype, ldz, or NULL
  *   Bm, Cm   [B, T, N] dtype, ldb, ldc;  N in 1 .. 128 (SANATAN_ERR_UNSUPPORTED above)
- *   A        [D, N] f32 (negative: the state decays);  skip, dt_bias [D] f32 or NULL (0)
+ *   A        [D, N] f32, finite (negative: the state decays);  skip, dt_bias [D] f32 or NULL (0)
  *   h0       [B, D, N] f32 or NULL (zero);  h_out [B, D, N] f32 or NULL, may be h0
  *   marks    sanatan_selective_scan_marks_size(...) bytes or NULL: f32 [B, ceil(T / 16), D,
  *            N], the states before tokens 0, 16, 32, ... of every sequence (those behind
  *            its last token are not written)
  *   workspace: sanatan_selective_scan_fwd_workspace_size(...) bytes (NULL if 0).
- *   Decays delta A below -126 ln 2 count as 0.  T = 0 copies h0 (or zeros) to h_out.
+ *   Decays exp(delta A) below 2^-126 count as 0.  Values that are not finite reach only
+ *   later tokens of their own sequence and channel (a B or C: of all its channels).
+ *   T = 0 copies h0 (or zeros) to h_out.
  * sanatan_selective_scan_bwd -- gradients of sum(y * dy) + sum(h_out * dh_out), with the
  *   marks that the forward wrote for the same inputs (h0 is among them): du, ddt [B, T, D]
  *   dtype, dz [B, T, D] dtype (NULL exactly where z is), dA [D, N] f32, dB, dC [B, T, N]
