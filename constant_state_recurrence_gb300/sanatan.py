@@ -1053,6 +1053,15 @@ def _input(x, name, dims=None):
     return x.shape, x.device, x.dtype
 
 
+def _columns(w, name, most):
+    """The number of columns of a matrix [D, 1 .. most] (_fit checks the rest)."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if w.dim() != 2 or not 1 <= w.shape[1] <= most:
+        raise ValueError(f"{name} has shape {tuple(w.shape)}, expected [D, 1 .. {most}]")
+    return w.shape[1]
+
+
 def layer_norm_bwd_workspace_size(rows, D):
     return int(lib().sanatan_layer_norm_bwd_workspace_size(rows, D))
 
@@ -1148,10 +1157,7 @@ def _act(activation):
 def _conv_args(x, w, bias, activation, dims):
     """(shape, device, dtype, ld of x, K, w's and bias's addresses, activation)"""
     shape, dev, dt = _input(x, "x", dims)
-    _need(w, "w", (torch.float32,))
-    if w.dim() != 2 or not 1 <= w.shape[1] <= CONV_TAPS:
-        raise ValueError(f"w has shape {tuple(w.shape)}, expected [D, 1 .. {CONV_TAPS}]")
-    K = w.shape[1]
+    K = _columns(w, "w", CONV_TAPS)
     ld = _rows(x, "x", dt, shape, dev)
     wp = _fit(w, "w", torch.float32, (shape[-1], K), dev).data_ptr()
     return shape, dev, dt, ld, K, wp, _opt(bias, "bias", torch.float32, (shape[-1],), dev), \
@@ -1254,10 +1260,7 @@ def selective_scan_bwd_workspace_size(B, T, D, N):
 def _selective_args(u, dt, A, B, C, D, z, dt_bias, softplus, dims):
     """(u's shape, device, dtype, N, the arguments that the three calls share)"""
     shape, dev, ty = _input(u, "u", dims)
-    _need(A, "A", (torch.float32,))
-    if A.dim() != 2 or not 1 <= A.shape[1] <= SELECTIVE_STATES:
-        raise ValueError(f"A has shape {tuple(A.shape)}, expected [D, 1 .. {SELECTIVE_STATES}]")
-    N, width = A.shape[1], shape[-1]
+    N, width = _columns(A, "A", SELECTIVE_STATES), shape[-1]
     pair = (*shape[:-1], N)
     _fit(u, "u", ty, shape, dev)
     _fit(dt, "dt", ty, shape, dev)
