@@ -1102,9 +1102,21 @@ int sanatan_selective_scan_bwd(const void* u, const void* dt, const void* z, int
   a.D = D;
   a.N = N;
   if (int s = check_selective(a)) return s;
-  if (D == 0) return SANATAN_OK;
   const size_t e = size_of(dtype);
   const int64_t tokens = static_cast<int64_t>(B) * T;
+  args.dB = dB;
+  args.dC = dC;
+  if (D == 0) {  // (dB and dC are sums over no channels)
+    const size_t pair = span(tokens, N, N, e);
+    if (pair == 0) return SANATAN_OK;
+    if (!at_elements({dB, dC}, e)) return SANATAN_ERR_INVALID;
+    if (clash({{dB, pair}, {dC, pair}}, {{Bm, span(tokens, ldb, N, e)},
+                                         {Cm, span(tokens, ldc, N, e)},
+                                         {lens, static_cast<size_t>(B) * 8}}))
+      return SANATAN_ERR_INVALID;
+    if (int s = check_arch()) return s;
+    return from_cuda(selective_scan_bwd_launch(args, nullptr, static_cast<cudaStream_t>(stream)));
+  }
   if (!at_elements({dA}, 4) || !at_elements({dskip, ddt_bias, dh0, dh_out}, 4, true))
     return SANATAN_ERR_INVALID;
   if (tokens > 0 && (!at_elements({dy, du, ddt, dB, dC}, e) || !at_elements({dz}, e, z == nullptr) ||
@@ -1133,8 +1145,6 @@ int sanatan_selective_scan_bwd(const void* u, const void* dt, const void* z, int
   args.ddt = ddt;
   args.dz = dz;
   args.dA = dA;
-  args.dB = dB;
-  args.dC = dC;
   args.dskip = dskip;
   args.ddt_bias = ddt_bias;
   args.dh0 = dh0;

@@ -543,6 +543,11 @@ size_t selective_scan_bwd_workspace_bytes(int B, int T, int D, int N) {
 
 cudaError_t selective_scan_bwd_launch(SelectiveBwdArgs args, void* workspace, cudaStream_t st) {
   SelectiveArgs& a = args.f;
+  if (a.D == 0) {
+    const size_t all = static_cast<size_t>(a.B) * a.T * a.N * (a.dtype == SANATAN_F32 ? 4 : 2);
+    cudaError_t e = cudaMemsetAsync(args.dB, 0, all, st);
+    return e == cudaSuccess ? cudaMemsetAsync(args.dC, 0, all, st) : e;
+  }
   if (a.B == 0) {
     const size_t row = static_cast<size_t>(a.D) * sizeof(float);
     cudaError_t e = cudaMemsetAsync(args.dA, 0, row * a.N, st);

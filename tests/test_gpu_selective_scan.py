@@ -171,7 +171,8 @@ def check(b, T, D, N, dtype, soft=True, gated=True, h0=True, lens=None, seed=0, 
     (1, 1, 1, 1), (1, 2, 3, 2), (2, 5, 8, 4), (1, 15, 32, 16), (2, 16, 33, 16), (1, 17, 31, 16),
     (3, 33, 40, 16), (2, 50, 130, 3), (1, 40, 7, 13), (2, 20, 24, 8), (1, 64, 9, 5),
     (1, 35, 16, 32), (2, 18, 5, 17), (1, 33, 6, 64), (1, 20, 3, 50), (1, 19, 4, 128),
-    (1, 17, 2, 99), (9, 3, 64, 16), (1, 70, 5, 16), (2, 66, 8, 64)])
+    (1, 17, 2, 99), (9, 3, 64, 16), (1, 70, 5, 16), (2, 66, 8, 64),
+    (1, 70, 4, 128), (2, 90, 3, 100)])
 def test_against_the_definition(b, T, D, N, dtype):
     check(b, T, D, N, dtype, seed=T + D + N, h0=T % 2 == 1, gated=(T + D) % 3 != 0)
 
@@ -236,6 +237,19 @@ def test_no_tokens_and_no_sequences():
     x, dy, dh = make(0, 5, 12, 16, F32, 7)
     _, g = run(x, dy, dh)
     assert not any(g[k].any() for k in ("dA", "dD", "ddt_bias"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_no_channels(dtype):
+    """dB and dC are sums over channels: zeros, written whole."""
+    x, dy, dh = make(2, 5, 0, 16, dtype, 7)
+    left = torch.full((2, 2, 5, 16), float("nan"), dtype=dtype, device=dev())
+    del left   # (what the outputs may be allocated on)
+    (y, h, _), g = run(x, dy, dh)
+    assert y.shape == (2, 5, 0) and h.shape == (2, 0, 16)
+    assert g["dB"].shape == g["dC"].shape == (2, 5, 16)
+    assert torch.equal(g["dB"], torch.zeros_like(g["dB"]))
+    assert torch.equal(g["dC"], torch.zeros_like(g["dC"]))
 
 
 def test_the_same_bits_and_states_in_place():

@@ -158,13 +158,21 @@ def test_scan(lib):
         assert call(lib, ldb=15) == call(lib, ldc=15) == call(lib, ldz=7) == INVALID
         assert call(lib, N=129, ldb=129, ldc=129) == UNSUPPORTED
         assert call(lib, D=(1 << 30) + 1, ldz=1 << 40) == UNSUPPORTED
-        assert call(lib, D=0) == OK
         for name in ("u", "dt", "Bm", "Cm", "A"):
             assert call(lib, **{name: None}) == call(lib, **{name: at(30, 2)}) == INVALID, name
         for name in ("z", "skip", "dt_bias"):
             assert call(lib, **{name: at(30, 2)}) == INVALID, name
         assert right(call(lib, skip=None, dt_bias=None))
         assert right(call(lib, u=at(30, 4), Bm=at(31, 12), A=at(32, 4)))
+    assert scan_fwd(lib, D=0) == scan_step(lib, D=0) == OK
+    # without channels dB and dC are still there, and zeros
+    none = dict(D=0, u=None, dt=None, z=None, A=None, dy=None, marks=None, du=None, ddt=None,
+                dz=None, dA=None, workspace=None, ws=0)
+    assert right(scan_bwd(lib, **none))
+    assert scan_bwd(lib, **none, T=0) == scan_bwd(lib, **none, B=0) == OK
+    for name in ("dB", "dC"):
+        for wrong in (None, at(30, 2), at(4), at(5)):
+            assert scan_bwd(lib, **dict(none, **{name: wrong})) == INVALID, name
     for call in (scan_fwd, scan_bwd):
         assert call(lib, B=-1) == call(lib, T=-1) == INVALID
         assert call(lib, B=1 << 16, D=1 << 15, ldz=1 << 15) == UNSUPPORTED
