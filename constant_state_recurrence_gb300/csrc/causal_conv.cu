@@ -14,8 +14,8 @@
 // with the K unfinished dx in registers: dc_t goes into each, and dx_{t-K+1} is then done.
 // The weights' gradients stay in registers over all runs of a thread; blocks leave partial
 // sums, and a second kernel adds them in a fixed order (no atomics: the same call gives the same
-// bits).  B 8 T 4096 D 1536 K 4 bf16, x a half of wider rows, GB300: forward 44 us, 4.6 TB/s
-// (0.67 of the measured copy rate), backward 82, 3.7 TB/s (0.54).  With loads into
+// bits).  B 8 T 4096 D 1536 K 4 bf16, x a half of wider rows, GB300: forward 39 us, 5.1 TB/s
+// (0.75 of the measured copy rate), backward 82, 3.7 TB/s (0.54).  With loads into
 // registers, four tokens ahead, and weights loaded value by value every sixteen tokens (each such
 // load of a warp touches 32 lines) 92 and 153.
 #include <algorithm>
@@ -34,7 +34,7 @@ namespace {
 using namespace lanes;
 
 constexpr int kThreads = 128;
-constexpr int kRunLong = 64, kRunShort = 16;  // tokens of a thread, forward
+constexpr int kRunShort = 16, kRunLong = 96;  // tokens of a thread, forward: from, to
 constexpr int kStep = 4;     // tokens of a group of copies
 constexpr int kGroupsFwd = 4, kGroupsBwd = 4;  // groups of a ring
 constexpr int kLanes = 32, kRows = 8;  // backward block: channels x runs
@@ -454,15 +454,28 @@ unsigned blocks_of(int64_t items) { return static_cast<unsigned>((items - 1) / k
 
 template <typename E, int KM, int V>
 cudaError_t fwd(ConvArgs a, cudaStream_t st) {
-  // Long runs read fewer tokens twice, and weights less often, where they are enough to give
-  // every SM two blocks.
-  const int64_t vecs = a.D / V, longs = (a.T + kRunLong - 1) / kRunLong;
-  a.run = a.B * longs * vecs >= 152 * 2 * kThreads ? kRunLong : kRunShort;
+  const int64_t vecs = a.D / V, states = a.s_out != nullptr ? a.B : 0;
+  constexpr size_t shared = Ring<E, V, 1, kGroupsFwd, kThreads>::kShared;
+  static_assert(shared <= 48 * 1024, "no opt-in");
+  static const int64_t at_once = [] {  // blocks that the SMs hold
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &n, conv_fwd_kernel<E, KM, V>, kThreads, shared);
+    return 152ll * (e == cudaSuccess && n > 0 ? n : 4);
+  }();
+  // The run length whose rounds of blocks take a thread the fewest tokens, those about a run's
+  // start (3 K: what is read twice, weights) among them.  B 8 T 4096 D 1536 bf16, with the call
+  // around it: 84 tokens, one round, 45 us; 64, a second round that is not full, 49; 16, five
+  // rounds, 64.  B 4 T 2048 D 1536 f32: 28 tokens 22.5, 64 24.6.
+  int64_t least = INT64_MAX;
+  for (int run = kRunShort; run <= kRunLong; run += kStep) {
+    const int64_t items = (static_cast<int64_t>(a.B) * ((a.T + run - 1) / run) + states) * vecs;
+    const int64_t rounds = (items - 1) / (at_once * kThreads) + 1, cost = rounds * (run + 3 * a.K);
+    if (cost < least) least = cost, a.run = run;
+  }
   a.runs = (a.T + a.run - 1) / a.run;
   const int64_t rows = static_cast<int64_t>(a.B) * a.runs + (a.s_out != nullptr ? a.B : 0);
   if (rows == 0) return cudaSuccess;
-  constexpr size_t shared = Ring<E, V, 1, kGroupsFwd, kThreads>::kShared;
-  static_assert(shared <= 48 * 1024, "no opt-in");
   return launch(conv_fwd_kernel<E, KM, V>, dim3(blocks_of(rows * vecs)), kThreads, shared, st, a);
 }
 
