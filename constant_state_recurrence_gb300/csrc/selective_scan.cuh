@@ -114,28 +114,42 @@ __device__ __forceinline__ float exp2_near(float x) {
 
 // What the decays of a tile multiply a lane's states by: their product as they were rounded,
 // and the sum of delta, which gives what it should be, 2^(A sum delta).  Their ratio puts
-// the state right once a tile, so that the bias of sixteen decays (3e-7) is all that is ever
-// in a state, whatever its memory.  (The series for every decay instead: 973 us for the forward
-// of B 8 T 4096 D 1536 N 16 bf16, 750 so.)
+// the state right once a tile, so that the bias of sixteen decays (at most 16 x 0.8 steps, 8e-7)
+// is all that is ever in a state, whatever its memory.  (The series for every decay instead:
+// 973 us for the forward of B 8 T 4096 D 1536 N 16 bf16, 750 so.)
+//
+// Steps of both signs (without a softplus): a product may leave float32, or lose its digits
+// among its smallest numbers, and come back though the sum is small.  What a product reaches
+// on the way is at most 2^(|A| sum |delta|): where that is large the state stays as walked.
 struct Decays {
   uint64_t q0, q1, sum;
   __device__ __forceinline__ Decays() : q0(pk2(1.0f, 1.0f)), q1(q0), sum(pk2(0.0f, 0.0f)) {}
   __device__ __forceinline__ void add(uint64_t a0, uint64_t a1, uint64_t delta) {
     q0 = fmul2(q0, a0), q1 = fmul2(q1, a1), sum = fadd2(sum, delta);
   }
-  // (x of 8 and more: the memory is two tokens, and q may have no digits left)
-  __device__ __forceinline__ static float ratio(float x, float q) {
-    return fabsf(x) < 8.0f ? exp2_near(x) * rcp(q) : 1.0f;
+  // (a reach |A| sum |delta| of 8 and more: the memory is two tokens, or q may have no digits)
+  __device__ __forceinline__ static float ratio(float x, float reach, float q) {
+    return fabsf(reach) < 8.0f ? exp2_near(x) * rcp(q) : 1.0f;
   }
-  __device__ __forceinline__ void put_right(uint64_t A0, uint64_t A1, uint64_t& h0,
-                                            uint64_t& h1) const {
-    float x[kStates], q[kStates];
+  // cells: the tile's, of the lane's channel, `pitch` apart, delta first.
+  __device__ __forceinline__ void put_right(uint64_t A0, uint64_t A1, uint64_t& h0, uint64_t& h1,
+                                            bool soft, const float4* cells, int pitch) const {
+    float x[kStates], q[kStates], reach[kStates];
     upk2(fmul2(sum, A0), x[0], x[1]);
     upk2(fmul2(sum, A1), x[2], x[3]);
+#pragma unroll
+    for (int j = 0; j < kStates; ++j) reach[j] = x[j];  // (of a softplus: no step is negative)
+    if (!soft) {
+      float s = 0.0f;
+#pragma unroll 1
+      for (int t = 0; t < kTile; ++t) s += fabsf(cells[t * pitch].x);
+      upk2(fmul2(pk2(s, s), A0), reach[0], reach[1]);
+      upk2(fmul2(pk2(s, s), A1), reach[2], reach[3]);
+    }
     upk2(q0, q[0], q[1]);
     upk2(q1, q[2], q[3]);
-    h0 = fmul2(h0, pk2(ratio(x[0], q[0]), ratio(x[1], q[1])));
-    h1 = fmul2(h1, pk2(ratio(x[2], q[2]), ratio(x[3], q[3])));
+    h0 = fmul2(h0, pk2(ratio(x[0], reach[0], q[0]), ratio(x[1], reach[1], q[1])));
+    h1 = fmul2(h1, pk2(ratio(x[2], reach[2], q[2]), ratio(x[3], reach[3], q[3])));
   }
 };
 

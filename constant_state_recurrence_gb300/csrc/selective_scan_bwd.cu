@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) selective_bwd_state_kernel(Selective
       g1 = fmul2(a1, ffma2(c.y, Cv.y, g1));
       decays.add(a0, a1, c.x);
     }
-    decays.put_right(A0, A1, g0, g1);
+    decays.put_right(A0, A1, g0, g1, a.softplus, &sm.cells[warp][0][mine], G::kRowPitch);
     __syncwarp();
     if (k - 2 >= at.k0) tiles.end(sm.raw[after]);
     now = next;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
           sm.sums[warp][k8 / 4][g + k8 % 4][mine] = s[q];
         }
     }
-    decays.put_right(A0, A1, g0, g1);
+    decays.put_right(A0, A1, g0, g1, a.softplus, &sm.cells[warp][0][mine], G::kRowPitch);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < G::kItems; ++i) {

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kFwdThreads, L <= 8 ? 3 : 1)
               sm.ys[k & 1][warp][g + M::index(lane) + i][mine] = v[i];
         }
       }
-      decays.put_right(A0, A1, h0, h1);
+      decays.put_right(A0, A1, h0, h1, a.softplus, &cells[0][mine], G::kRowPitch);
       __syncthreads();
     }
     if (STATE)
