@@ -503,6 +503,14 @@ __device__ __forceinline__ void store_cells(E* row, int d, int D, const float (&
   }
 }
 
+// decay h + own for a decay of 2^x.  A segment's decay may be outside float32 where no state
+// is: its fourth root is multiplied in step by step there, and nothing makes nothing of it.
+__device__ __forceinline__ float carried(float x, float h, float own) {
+  if (fabsf(x) < 126.0f) return fmaf(ex2(x), h, own);
+  const float root = ex2(0.25f * x);
+  return h == 0.0f ? own : fmaf(h * root * root * root, root, own);
+}
+
 // The carries of S segments, in place: H[b][s][D][N] becomes the state before segment s
 // (reverse: the gradient behind it); sums [b][s][D] of delta.
 __global__ void __launch_bounds__(256)
@@ -516,9 +524,9 @@ __global__ void __launch_bounds__(256)
   float h = first != nullptr ? first[i] : 0.0f;
   for (int k = 0; k < S; ++k) {
     const int64_t s = b * S + (reverse ? S - 1 - k : k);
-    const float own = H[s * slab + at], decay = ex2(a * sums[s * D + d]);
+    const float own = H[s * slab + at];
     H[s * slab + at] = h;
-    h = fmaf(decay, h, own);
+    h = carried(a * sums[s * D + d], h, own);
   }
 }
 

@@ -633,8 +633,9 @@ SANATAN_API int sanatan_causal_conv_step(float* state, const void* x, int64_t ld
  *            N], the states before tokens 0, 16, 32, ... of every sequence (those behind
  *            its last token are not written)
  *   workspace: sanatan_selective_scan_fwd_workspace_size(...) bytes (NULL if 0).
- *   Decays exp(delta A) below 2^-126 count as 0.  Values that are not finite reach only
- *   later tokens of their own sequence and channel (a B or C: of all its channels).
+ *   A token's decay exp(delta A) counts as 0 below 2^-126 and as infinite above 2^128.
+ *   Values that are not finite reach only later tokens of their own sequence and channel (a B
+ *   or C: of all its channels).
  *   T = 0 copies h0 (or zeros) to h_out.
  * sanatan_selective_scan_bwd -- gradients of sum(y * dy) + sum(h_out * dh_out), with the
  *   marks that the forward wrote for the same inputs (h0 is among them): du, ddt [B, T, D]

@@ -123,3 +123,43 @@ def test_a_tile_whose_decays_leave_float32(A, steps):
     assert np.abs(f64(h) / h64 - 1).max() <= room
     assert np.abs(f64(h1) / h64 - 1).max() <= room
     assert np.abs(f64(y1) / (N * h64) - 1).max() <= room + 8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("D,N", [(8, 16), (5, 7), (8, 40)])
+def test_segments_of_growing_states(D, N):
+    """A segment's decay may be beyond float32 where no state is: nothing put in before the
+    last tokens, and gradients of the first alone."""
+    x, dy, _ = make(1, 256, D, N, F32, D + N, gated=False, h0=False)
+    x["A"], x["dt"], x["dt_bias"] = x["A"].abs().clamp(1.5, 2.0), torch.ones(1, 256, D), None
+    assert S.selective_scan_fwd_workspace_size(1, 256, D, N) > 0
+    x["u"][:, :-25] = 0
+    dy[:, 25:] = 0
+    against(x, dy, None, F32)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("D,N", [(8, 16), (3, 33)])
+def test_a_segment_carries_what_fits(D, N, sign):
+    """Two segments: exp(102) up and as much down, or down and up.  A state that has the room
+    for it is carried, though the segment's decay alone has none in float32.  (No inputs: the
+    state is a product of 128 decays, each off by 20 e, and of the segments' exponents, which
+    are exact but for the power of two: 3000 e.)"""
+    T = 128
+    dt = torch.ones(1, T, D) * sign
+    dt[:, T // 2:] = -sign
+    A = torch.full((D, N), 1.6)
+    h0 = (1 + torch.rand(1, D, N, generator=torch.Generator().manual_seed(1))) * \
+        (1e-30 if sign > 0 else 1e20)
+    assert S.selective_scan_fwd_workspace_size(1, T, D, N) > 0
+    zero, one = torch.zeros(1, T, D), torch.ones(1, T, N)
+    d = [t.to(dev()) for t in (zero, dt, A, one, one)]
+    y, h, marks = S.sanatan_selective_scan_fwd(*d, softplus=False, h0=h0.to(dev()),
+                                               want_state=True, want_marks=True)
+    path = np.cumsum(f64(dt)[0, :, 0] * np.float64(np.float32(1.6)))
+    assert np.abs(f64(h) / (f64(h0) * np.exp(path[-1])) - 1).max() <= 3000 * 2.0 ** -24
+    want = (f64(h0)[0].sum(-1) * np.exp(path)[:, None])
+    assert np.abs(f64(y)[0] / want - 1).max() <= 3000 * 2.0 ** -24
+    dh = torch.full((1, D, N), 1e20 if sign > 0 else 1e-30)    # (from behind: the other way)
+    g = S.sanatan_selective_scan_bwd(*d, zero.to(dev()), marks, softplus=False,
+                                     dh_last=dh.to(dev()), want_dh0=True)
+    assert np.abs(f64(g["dh0"]) / (f64(dh) * np.exp(path[-1])) - 1).max() <= 3000 * 2.0 ** -24
