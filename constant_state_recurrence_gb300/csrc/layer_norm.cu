@@ -506,11 +506,6 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* parts, in
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t shared,
                    cudaStream_t st, Args... args) {
-  if (shared > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -523,6 +518,33 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t sha
 }
 
 constexpr int up32(int n) { return (n + 31) / 32 * 32; }
+
+// Shared memory of a backward block of `groups` groups of G threads.
+template <typename E, bool ALIGNED, int R>
+constexpr size_t bwd_shared(int groups, int G) {
+  return sizeof(float) *
+             (groups * (2 * (G / 32) * 2 * R) + (groups > 1 ? 2 * kVec<E> * G : 0)) +
+         (ALIGNED ? static_cast<size_t>(kRing<R>) * G * groups * 16 : 0);
+}
+
+// The limit of shared memory belongs to the function, for all threads and streams of a device:
+// it is set to what any width takes, so that two calls at once set the same.
+template <typename E, bool ALIGNED, int R, int MOST>
+cudaError_t launch_bwd(const NormBwdArgs& a, int n, int groups, int G, float* parts,
+                       cudaStream_t st) {
+  // (one group of MOST threads, or several: G is at most half of them, groups G all)
+  constexpr size_t kOne = bwd_shared<E, ALIGNED, R>(1, MOST);
+  constexpr size_t kMost = kOne + sizeof(float) * (R == kRows ? kVec<E> * MOST : 0);
+  static_assert(R < kRows || MOST / 32 < 16, "a group has a barrier of its own, of sixteen");
+  const auto kernel = norm_bwd_kernel<E, ALIGNED, R, MOST>;
+  if (kMost > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
+    if (e != cudaSuccess) return e;
+  }
+  return launch(kernel, dim3(n), G * groups, bwd_shared<E, ALIGNED, R>(groups, G), st, a, G,
+                parts);
+}
 
 template <typename E, bool ALIGNED>
 cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
@@ -558,16 +580,10 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t st) {
   if (a.D <= kMostThreads * V) {
     const int G = up32((a.D - 1) / V + 1);
     const bool several = G <= kGroupThreads;
-    // (at most twelve groups: one has a barrier of its own, of sixteen)
     const int groups = several ? kGroupThreads / G : 1, R = several ? kRows : 1;
     n = static_cast<int>(std::min<int64_t>(kParts, (a.rows - 1) / (groups * R) + 1));
-    const size_t shared =
-        sizeof(float) * (groups * (2 * (G / 32) * 2 * R) + (groups > 1 ? 2 * V * G : 0)) +
-        (ALIGNED ? static_cast<size_t>(kAhead + 1) * R * 3 * G * groups * 16 : 0);
-    e = several ? launch(norm_bwd_kernel<E, ALIGNED, kRows, kGroupThreads>, dim3(n), G * groups,
-                         shared, st, a, G, parts)
-                : launch(norm_bwd_kernel<E, ALIGNED, 1, kMostThreads>, dim3(n), G, shared, st, a,
-                         G, parts);
+    e = several ? launch_bwd<E, ALIGNED, kRows, kGroupThreads>(a, n, groups, G, parts, st)
+                : launch_bwd<E, ALIGNED, 1, kMostThreads>(a, n, groups, G, parts, st);
   } else {
     e = launch(norm_bwd_long_kernel<E>, dim3(static_cast<unsigned>(a.rows)), kLoopThreads, 0, st,
                a);
