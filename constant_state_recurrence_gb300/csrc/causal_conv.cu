@@ -25,6 +25,7 @@
 #include "copy_async.cuh"
 #include "lanes.cuh"
 #include "pdl.cuh"
+#include "per_device.h"
 #include "sanatan_internal.h"
 #include "vec_io.cuh"
 
@@ -452,17 +453,31 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t sha
 
 unsigned blocks_of(int64_t items) { return static_cast<unsigned>((items - 1) / kThreads + 1); }
 
+// Forward blocks that the current device holds at once; asked once a device (again after a
+// failure).
+template <typename E, int KM, int V>
+cudaError_t held(int* blocks) {
+  static PerDevice<int> known;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return known.get(dev, blocks, [](int* out) {
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &n, conv_fwd_kernel<E, KM, V>, kThreads, Ring<E, V, 1, kGroupsFwd, kThreads>::kShared);
+    *out = kSms * std::max(n, 1);
+    return e;
+  });
+}
+
 template <typename E, int KM, int V>
 cudaError_t fwd(ConvArgs a, cudaStream_t st) {
   const int64_t vecs = a.D / V, states = a.s_out != nullptr ? a.B : 0;
   constexpr size_t shared = Ring<E, V, 1, kGroupsFwd, kThreads>::kShared;
   static_assert(shared <= 48 * 1024, "no opt-in");
-  static const int64_t at_once = [] {  // blocks that the SMs hold
-    int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &n, conv_fwd_kernel<E, KM, V>, kThreads, shared);
-    return 152ll * (e == cudaSuccess && n > 0 ? n : 4);
-  }();
+  int at_once = 0;  // blocks that the device holds
+  const cudaError_t e = held<E, KM, V>(&at_once);
+  if (e != cudaSuccess) return e;
   // The run length whose rounds of blocks take a thread the fewest tokens, those about a run's
   // start (3 K: what is read twice, weights) among them.  B 8 T 4096 D 1536 bf16, with the call
   // around it: 84 tokens, one round, 45 us; 64, a second round that is not full, 49; 16, five
@@ -470,7 +485,8 @@ cudaError_t fwd(ConvArgs a, cudaStream_t st) {
   int64_t least = INT64_MAX;
   for (int run = kRunShort; run <= kRunLong; run += kStep) {
     const int64_t items = (static_cast<int64_t>(a.B) * ((a.T + run - 1) / run) + states) * vecs;
-    const int64_t rounds = (items - 1) / (at_once * kThreads) + 1, cost = rounds * (run + 3 * a.K);
+    const int64_t rounds = (items - 1) / (static_cast<int64_t>(at_once) * kThreads) + 1;
+    const int64_t cost = rounds * (run + 3 * a.K);
     if (cost < least) least = cost, a.run = run;
   }
   a.runs = (a.T + a.run - 1) / a.run;
@@ -488,7 +504,7 @@ struct Runs {
 };
 Runs runs_of(int B, int T, int D, int K, int V) {
   const int64_t columns = (D - 1) / (V * kLanes) + 1;
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(kParts, 2 * 152 / columns));
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(kParts, 2 * kSms / columns));
   Runs best{1, 16, std::max(1, T / 16 + (T % 16 != 0))};  // (one run: the state's gradient)
   int64_t least = INT64_MAX;
   for (int run = 16; run <= 64; run += 8) {

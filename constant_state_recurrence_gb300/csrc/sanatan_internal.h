@@ -268,6 +268,8 @@ struct CacheArgs {
 int64_t state_cache_blocks(int64_t inner);
 cudaError_t state_cache_launch(CacheArgs a, bool write, cudaStream_t st);
 
+constexpr int kSms = 152;  // of a GB300, for the plans of the layers below
+
 // Layer norm of rows of D values (layer_norm.cu).
 constexpr int kNormParts = 304;    // partial sums of dw and db: blocks of the backward at most
 struct NormArgs {

@@ -322,7 +322,6 @@ int selective_blocks(int D, int N) { return (D - 1) / (kThreads / selective_lane
 int selective_segments(int B, int T, int D, int N, int* tiles_per_segment) {
   const int tiles = std::max(1, (T - 1) / kTile + 1);
   const int64_t blocks = static_cast<int64_t>(B) * selective_blocks(D, N);
-  constexpr int64_t kSms = 152;
   int64_t S = 1;
   if (blocks < 2 * kSms && selective_lanes(N) < 32)
     S = std::min<int64_t>((6 * kSms - 1) / blocks + 1, tiles / 4);

@@ -1,7 +1,8 @@
 """What the layer norm, the short causal convolution and the selective scan ask of the CUDA
 runtime, with a stand-in for the runtime that notes each call and launches nothing: a kernel's
 limit of shared memory does not depend on the call (it is the function's, shared by all
-threads).  On the CPU, in processes of their own."""
+threads), and a failed question to the runtime is that call's own.  On the CPU, in processes
+of their own."""
 import json
 import os
 import shutil
@@ -122,3 +123,23 @@ for dtype in (0, 1):
         elif x[0] == "launch" and x[2] > 48 * 1024:
             assert x[2] <= max(limits[x[1]])
     assert limits and all(len(sizes) == 1 for sizes in limits.values()), limits
+
+
+def test_a_failed_question_is_the_calls_own(calls):
+    """The convolution's run length comes from how many blocks the device holds: a call whose
+    question fails returns an error and launches nothing, the next asks again, a device's answer
+    is kept, and is not another device's."""
+    one = "say('status', conv_fwd(8, 4096, 1536, 4, 1))\n"
+    want = {}
+    for device in (0, 1):
+        log = calls(f"fake.fake_device({device})\n" + one)
+        assert [x[0] for x in log] == ["asked", "launch", "status"] and log[2][1] == 0
+        want[device] = log[1][3]
+    assert want[0] != want[1]
+    log = calls("fake.fake_failures(2)\n" + 4 * one + "fake.fake_device(1)\n" + 2 * one
+                + "fake.fake_device(0)\n" + one)
+    assert [x[:1] + x[1:] if x[0] == "status" else x[0] for x in log] == [
+        "asked", ["status", 3], "asked", ["status", 3], "asked", "launch", ["status", 0], "launch",
+        ["status", 0], "asked", "launch", ["status", 0], "launch", ["status", 0], "launch",
+        ["status", 0]]
+    assert [x[3] for x in log if x[0] == "launch"] == [want[0], want[0], want[1], want[1], want[0]]
