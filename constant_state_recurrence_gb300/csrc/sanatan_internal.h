@@ -388,10 +388,15 @@ struct SelectiveBwdArgs {
   float* dskip = nullptr;           // [D] or null
   float* ddt_bias = nullptr;        // [D] or null
   float* dh0 = nullptr;             // [B, D, N] or null
-  // parts in the workspace (set by the launcher)
-  float* pairs = nullptr;           // [blocks of channels, B, T, 2, N]: dB, dC
+  // set by the launcher
+  int pieces = 1, piece = 0;        // of a segment, walked one after the other from the last
+  int tiles_per_piece = 0;
+  // parts in the workspace
+  float* pairs = nullptr;           // dB, dC: [blocks of channels, B, T, 2, N], or of a
+                                    // piece: [.., B, segments, tiles_per_piece * 16, 2, N]
   float* params = nullptr;          // [B, segments, D, N]: dA
   float* channels = nullptr;        // [B, segments, 2, D]: dskip, ddt_bias
+  float* lanes = nullptr;           // [B, segments, 2, 16, D]: theirs, between two pieces
 };
 size_t selective_scan_bwd_workspace_bytes(int B, int T, int D, int N);
 cudaError_t selective_scan_bwd_launch(SelectiveBwdArgs a, void* workspace, cudaStream_t st);

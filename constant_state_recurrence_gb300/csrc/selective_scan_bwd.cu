@@ -8,6 +8,15 @@
 // the latter's wavefronts, 42 a token and warp: 1466 us instead of 1422, one prompt of 32768
 // tokens 1840 instead of 1567.  Cells as pairs twice over, without the moves that make pairs of
 // them: 1563.
+//
+// dB and dC are sums over channels: each block of 128 / L channels leaves its part of them for
+// every token, in all L / 4 times the marks.  Beyond four lanes a channel and 512 MB the parts
+// are kept no larger than the marks: segments are walked in pieces, from the last, by a launch
+// each that takes all segments, with the gradient behind a piece and the sums over tokens in
+// memory between two (so that nothing is added in another order), and a piece's parts are
+// added up before the next overwrites them.  B 4 T 4096 D 4096 N 128 bf16: 17.2 GB and 18.8 ms
+// in one piece, 2.2 GB and 19.3 ms in eight; B 1 T 4096 D 1536 N 128: 1.6 GB and 2.57 ms, 0.54
+// and 2.75 in three.
 #include "selective_scan.cuh"
 
 namespace sanatan {
@@ -222,7 +231,12 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
   E* DU = static_cast<E*>(args.du);
   E* DDT = static_cast<E*>(args.ddt);
   E* DZ = static_cast<E*>(args.dz);
-  const int live = min(at.k1, (n + kTile - 1) / kTile);
+  // The piece's tiles k0 .. k1 of the segment's (four lanes a channel: always all of them).
+  constexpr bool kPieces = L > 4;
+  const int k0 = kPieces ? min(at.k0 + args.piece * args.tiles_per_piece, at.k1) : at.k0;
+  const int k1 = kPieces ? min(k0 + args.tiles_per_piece, at.k1) : at.k1;
+  const bool first = !kPieces || args.piece + 1 == args.pieces, last = !kPieces || args.piece == 0;
+  const int live = min(k1, (n + kTile - 1) / kTile);
   Tiles tiles;
   tiles.init({a.u, a.dt, a.z, args.dy, a.Bm, a.Cm}, {a.D, a.D, a.ldz, a.D, a.ldb, a.ldc}, a, row0,
              n, d0, live - 1, -1);
@@ -231,19 +245,25 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
     st.load(args.marks + (static_cast<int64_t>(at.b) * at.tiles + k) * slab, rmark);
     tiles.begin(sm.raw, k);
   };
-  if (at.k0 < live) begin(live - 1), tiles.end(sm.raw);
+  if (k0 < live) begin(live - 1), tiles.end(sm.raw);
   uint64_t A0, A1, g0, g1, dA0 = pk2(0.0f, 0.0f), dA1 = dA0;
   {
     float f[kStates];
     st.load(a.A, f);
     reorder(f, x);
     A0 = pk2(f[0] * kLog2e, f[1] * kLog2e), A1 = pk2(f[2] * kLog2e, f[3] * kLog2e);
-    const float* from = a.segments > 1 ? a.carry + part * slab
-                        : (args.dh_out != nullptr ? args.dh_out + at.b * slab : nullptr);
+    const float* from = a.segments > 1 || !first
+                            ? a.carry + part * slab
+                            : (args.dh_out != nullptr ? args.dh_out + at.b * slab : nullptr);
     f[0] = f[1] = f[2] = f[3] = 0.0f;
     if (from != nullptr) st.load(from, f);
     reorder(f, x);
     g0 = pk2(f[0], f[1]), g1 = pk2(f[2], f[3]);
+    if (!first) {
+      st.load(args.params + part * slab, f);
+      reorder(f, x);
+      dA0 = pk2(f[0], f[1]), dA1 = pk2(f[2], f[3]);
+    }
   }
   float bias[W], skip[W], dskip[W], dbias[W];
 #pragma unroll
@@ -252,18 +272,28 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
     bias[j] = there && a.dt_bias != nullptr ? a.dt_bias[cell_d + j] : 0.0f;
     skip[j] = there && a.skip != nullptr ? a.skip[cell_d + j] : 0.0f;
     dskip[j] = dbias[j] = 0.0f;
+    if (!first && there && cell_t < kTile) {
+      const float* from = args.lanes + (part * 2 * kTile + cell_t) * a.D + cell_d + j;
+      dskip[j] = from[0], dbias[j] = from[static_cast<int64_t>(kTile) * a.D];
+    }
   }
   {
     const float zero[W] = {};
-    for (int t = max(at.k0, live) * kTile + cell_t; t < min(at.k1 * kTile, a.T); t += kStep) {
+    for (int t = max(k0, live) * kTile + cell_t; t < min(k1 * kTile, a.T); t += kStep) {
       store_cells<E, W, ALIGNED>(DU + (row0 + t) * a.D, cell_d, a.D, zero);  // without a token
       store_cells<E, W, ALIGNED>(DDT + (row0 + t) * a.D, cell_d, a.D, zero);
       if (gated) store_cells<E, W, ALIGNED>(DZ + (row0 + t) * a.D, cell_d, a.D, zero);
     }
   }
-  // dB and dC of the block's channels and tile k: [block of channels][b][t][B | C][N]
+  // dB and dC of the block's channels and tile k: [block of channels][b][t][B | C][N], or
+  // [block of channels][b][segment][t of the piece][B | C][N]
   auto put_pairs = [&](int k) {
-    float* out = args.pairs + (static_cast<int64_t>(at.cb) * a.B * a.T + row0) * 2 * a.N;
+    const int64_t rows = static_cast<int64_t>(args.tiles_per_piece) * kTile;
+    const int64_t row = kPieces && args.pieces > 1
+                            ? (static_cast<int64_t>(at.cb) * a.B * a.segments + part) * rows -
+                                  static_cast<int64_t>(k0) * kTile
+                            : static_cast<int64_t>(at.cb) * a.B * a.T + row0;
+    float* out = args.pairs + row * 2 * a.N;
 #pragma unroll
     for (int i = 0; i < G::kQuadItems; ++i) {
       const int q = tid + i * kThreads, s = q % L * 4, which = q / L % 2, tl = q / (2 * L);
@@ -285,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
       }
     }
   };
-  for (int k = live - 1; k >= at.k0; --k) {
+  for (int k = live - 1; k >= k0; --k) {
     copy_wait<0>();
     __syncthreads();
     if (k + 1 < live) put_pairs(k + 1);
@@ -314,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
     reorder(rmark, x);
     uint64_t h0 = pk2(rmark[0], rmark[1]), h1 = pk2(rmark[2], rmark[3]);
     __syncthreads();
-    if (k > at.k0) begin(k - 1);
+    if (k > k0) begin(k - 1);
     auto cell_of = [&](int t) { return sm.cells[warp][t][mine]; };
     auto pair_of = [&](int t, int which) {
       return reinterpret_cast<const ulonglong2&>(sm.pairs[t][which][order][kStates * l]);
@@ -424,23 +454,34 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
         if (gated) store_cells<E, W, ALIGNED>(DZ + (row0 + t) * a.D, cell_d, a.D, dz);
       }
     }
-    if (k > at.k0) tiles.end(sm.raw);
+    if (k > k0) tiles.end(sm.raw);
   }
-  if (at.k0 < live) {
+  if (k0 < live) {
     __syncthreads();
-    put_pairs(at.k0);
+    put_pairs(k0);
   }
   float f[kStates];
-  if (args.dh0 != nullptr && at.seg == 0) {
+  float* to = !last ? a.carry + part * slab
+                    : (args.dh0 != nullptr && at.seg == 0 ? args.dh0 + at.b * slab : nullptr);
+  if (to != nullptr) {
     upk2(g0, f[0], f[1]);
     upk2(g1, f[2], f[3]);
     reorder(f, x);
-    st.store(args.dh0 + at.b * slab, pk2(f[0], f[1]), pk2(f[2], f[3]));
+    st.store(to, pk2(f[0], f[1]), pk2(f[2], f[3]));
   }
   upk2(dA0, f[0], f[1]);
   upk2(dA1, f[2], f[3]);
   reorder(f, x);
   st.store(args.params + part * slab, pk2(f[0], f[1]), pk2(f[2], f[3]));
+  if (!last) {
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+      if (cell_t < kTile && cell_d + j < a.D) {
+        float* out = args.lanes + (part * 2 * kTile + cell_t) * a.D + cell_d + j;
+        out[0] = dskip[j], out[static_cast<int64_t>(kTile) * a.D] = dbias[j];
+      }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < W; ++j) {
 #pragma unroll
@@ -455,23 +496,33 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
   }
 }
 
-// dB and dC [B, T, N] from the blocks' parts; zeros behind the last token.
-template <typename E>
+// dB and dC [B, T, N] from the blocks' parts, of all tokens or of a piece of every segment;
+// zeros behind the last token.
+template <typename E, bool PIECE>
 __global__ void __launch_bounds__(256) selective_pairs_kernel(SelectiveBwdArgs args) {
   const SelectiveArgs& a = args.f;
-  const int64_t wide = 2 * static_cast<int64_t>(a.N), all = static_cast<int64_t>(a.B) * a.T * wide;
+  const int64_t rows = PIECE ? static_cast<int64_t>(a.segments) * args.tiles_per_piece * kTile : a.T;
+  const int64_t wide = 2 * static_cast<int64_t>(a.N), all = a.B * rows * wide;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   wait_for_previous();
   if (i >= all) return;
   const int64_t row = i / wide;
   const int q = static_cast<int>(i % wide), which = q / a.N, s = q % a.N;
-  const int b = static_cast<int>(row / a.T), t = static_cast<int>(row % a.T);
+  const int b = static_cast<int>(row / rows);
+  int64_t t = row % rows;
+  if (PIECE) {
+    const int each = args.tiles_per_piece * kTile, seg = static_cast<int>(t / each);
+    const int64_t end = static_cast<int64_t>(seg + 1) * a.tiles_per_segment * kTile;
+    t = t % each + (static_cast<int64_t>(seg) * a.tiles_per_segment +
+                    static_cast<int64_t>(args.piece) * args.tiles_per_piece) * kTile;
+    if (t >= end || t >= a.T) return;
+  }
   float sum = 0.0f;
   if (t < length_of(a.lens, b, a.T))
 #pragma unroll 8
     for (int k = 0; k < a.blocks; ++k) sum += args.pairs[k * all + i];
   E* out = static_cast<E*>(which == 0 ? args.dB : args.dC);
-  out[row * a.N + s] = store_from_float<E>(sum);
+  out[(static_cast<int64_t>(b) * a.T + t) * a.N + s] = store_from_float<E>(sum);
 }
 
 // dA, dskip and ddt_bias from the parts of sequences and segments.
@@ -505,15 +556,22 @@ cudaError_t bwd_of(const SelectiveBwdArgs& args, cudaStream_t st) {
     if (e == cudaSuccess) e = launch_carry(a, args.dh_out, true, st);
     if (e != cudaSuccess) return e;
   }
-  e = launch(selective_bwd_kernel<E, L, ALIGNED>, blocks, kThreads,
-             sizeof(BwdShared<E, L, ALIGNED>), st, args);
-  const int64_t pairs = static_cast<int64_t>(a.B) * a.T * 2 * a.N;
-  if (e == cudaSuccess && pairs > 0)
-    e = launch(selective_pairs_kernel<E>, (pairs - 1) / 256 + 1, 256, 0, st, args);
+  SelectiveBwdArgs now = args;
+  const int64_t rows = args.pieces == 1 ? a.T
+                                        : static_cast<int64_t>(a.segments) * args.tiles_per_piece *
+                                              kTile;
+  const int64_t pairs = a.B * rows * 2 * a.N;
+  for (now.piece = args.pieces - 1; now.piece >= 0; --now.piece) {
+    e = launch(selective_bwd_kernel<E, L, ALIGNED>, blocks, kThreads,
+               sizeof(BwdShared<E, L, ALIGNED>), st, now);
+    if (e == cudaSuccess && pairs > 0)
+      e = launch(args.pieces == 1 ? selective_pairs_kernel<E, false>
+                                  : selective_pairs_kernel<E, true>,
+                 (pairs - 1) / 256 + 1, 256, 0, st, now);
+    if (e != cudaSuccess) return e;
+  }
   const int64_t params = static_cast<int64_t>(a.D) * (a.N + 2);
-  if (e == cudaSuccess)
-    e = launch(selective_params_kernel, (params - 1) / 256 + 1, 256, 0, st, args);
-  return e;
+  return launch(selective_params_kernel, (params - 1) / 256 + 1, 256, 0, st, args);
 }
 template <typename E, int L>
 cudaError_t bwd(const SelectiveBwdArgs& args, cudaStream_t st) {
@@ -521,24 +579,42 @@ cudaError_t bwd(const SelectiveBwdArgs& args, cudaStream_t st) {
                                                                 : bwd_of<E, L, false>(args, st);
 }
 
-struct Sizes {
-  size_t pairs, params, channels, carry, sums;
+constexpr size_t kPairBytes = size_t{512} << 20;  // of dB's and dC's parts, or the marks' if more
+
+// Segments, pieces and the floats of the workspace's parts.
+struct Plan {
+  int segments, tiles_per_segment, pieces, tiles_per_piece;
+  size_t pairs, params, channels, carry, sums, lanes;
 };
-Sizes sizes(int B, int T, int D, int N, int segments) {
-  const size_t bs = static_cast<size_t>(B) * segments, several = segments > 1 ? 1 : 0;
+Plan plan(int B, int T, int D, int N) {
+  Plan p{};
+  p.segments = selective_segments(B, T, D, N, &p.tiles_per_segment);
+  const size_t blocks = selective_blocks(D, N), pair = 2 * static_cast<size_t>(N), tokens = T;
+  const size_t marks = static_cast<size_t>(B) * ((tokens + kTile - 1) / kTile) * D * N;
+  const size_t most = std::max(kPairBytes / sizeof(float), marks);
+  p.pairs = blocks * B * tokens * pair;
+  p.pieces = 1, p.tiles_per_piece = p.tiles_per_segment;
+  if (selective_lanes(N) > 4 && p.pairs > most) {
+    const size_t pieces = std::min<size_t>((p.pairs - 1) / most + 1, p.tiles_per_segment);
+    p.tiles_per_piece = static_cast<int>((p.tiles_per_segment - 1) / pieces + 1);
+    p.pieces = (p.tiles_per_segment - 1) / p.tiles_per_piece + 1;
+  }
+  const size_t bs = static_cast<size_t>(B) * p.segments;
+  if (p.pieces > 1) p.pairs = blocks * bs * p.tiles_per_piece * kTile * pair;
+  p.params = bs * D * N, p.channels = bs * 2 * D;
+  p.carry = p.segments > 1 || p.pieces > 1 ? bs * D * N : 0, p.sums = p.segments > 1 ? bs * D : 0;
+  p.lanes = p.pieces > 1 ? bs * 2 * kTile * D : 0;
   // (each a multiple of four floats, so that the next starts at 16 bytes)
-  auto up = [](size_t n) { return (n + 3) / 4 * 4; };
-  return {up(static_cast<size_t>(selective_blocks(D, N)) * B * T * 2 * N), up(bs * D * N),
-          up(bs * 2 * D), up(several * bs * D * N), up(several * bs * D)};
+  for (size_t* n : {&p.pairs, &p.params, &p.channels, &p.carry, &p.sums}) *n = (*n + 3) / 4 * 4;
+  return p;
 }
 
 }  // namespace
 
 size_t selective_scan_bwd_workspace_bytes(int B, int T, int D, int N) {
   if (B <= 0 || T < 0 || D <= 0 || N <= 0) return 0;
-  int tiles;
-  const Sizes s = sizes(B, T, D, N, selective_segments(B, T, D, N, &tiles));
-  return sizeof(float) * (s.pairs + s.params + s.channels + s.carry + s.sums);
+  const Plan p = plan(B, T, D, N);
+  return sizeof(float) * (p.pairs + p.params + p.channels + p.carry + p.sums + p.lanes);
 }
 
 cudaError_t selective_scan_bwd_launch(SelectiveBwdArgs args, void* workspace, cudaStream_t st) {
@@ -557,13 +633,15 @@ cudaError_t selective_scan_bwd_launch(SelectiveBwdArgs args, void* workspace, cu
     return e;
   }
   a.blocks = selective_blocks(a.D, a.N);
-  a.segments = selective_segments(a.B, a.T, a.D, a.N, &a.tiles_per_segment);
-  const Sizes s = sizes(a.B, a.T, a.D, a.N, a.segments);
+  const Plan p = plan(a.B, a.T, a.D, a.N);
+  a.segments = p.segments, a.tiles_per_segment = p.tiles_per_segment;
+  args.pieces = p.pieces, args.tiles_per_piece = p.tiles_per_piece;
   args.pairs = static_cast<float*>(workspace);
-  args.params = args.pairs + s.pairs;
-  args.channels = args.params + s.params;
-  a.carry = args.channels + s.channels;
-  a.sums = a.carry + s.carry;
+  args.params = args.pairs + p.pairs;
+  args.channels = args.params + p.params;
+  a.carry = args.channels + p.channels;
+  a.sums = a.carry + p.carry;
+  args.lanes = a.sums + p.sums;
   a.vec = state_words(a.N, {a.A, args.marks, args.dh_out, args.dh0, args.pairs});
   if (a.dtype == SANATAN_F32) SANATAN_SELECTIVE_DISPATCH(bwd, float, args)
   SANATAN_SELECTIVE_DISPATCH(bwd, __nv_bfloat16, args)

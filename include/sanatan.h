@@ -642,8 +642,10 @@ SANATAN_API int sanatan_causal_conv_step(float* state, const void* x, int64_t ld
  *   dtype, dz [B, T, D] dtype (NULL exactly where z is), dA [D, N] f32, dB, dC [B, T, N]
  *   dtype, dskip, ddt_bias [D] f32 or NULL, dh0 [B, D, N] f32 or NULL, may be dh_out
  *   ([B, D, N] f32 or NULL).
- *   workspace: sanatan_selective_scan_bwd_workspace_size(...) bytes: dB's and dC's parts,
- *   8 N bytes for each token and block of channels (32 channels at N = 16).
+ *   workspace: sanatan_selective_scan_bwd_workspace_size(...) bytes: mostly dB's and dC's
+ *   parts, 8 N bytes for each token and block of channels (32 channels up to N = 16, 16 up to
+ *   32, 8 up to 64, then 4); beyond N = 16 at most about 512 MB or what the marks take,
+ *   whichever is more.
  * sanatan_selective_scan_step -- one token of nseq sequences: h [nseq, D, N] f32 is updated
  *   in place; u, dt, z, y [nseq, D], Bm, Cm [nseq, N] dtype (ld: between two sequences).
  */
