@@ -522,11 +522,22 @@ __global__ void __launch_bounds__(256)
   const int64_t slab = static_cast<int64_t>(D) * N, b = i / slab, at = i % slab, d = at / N;
   const float a = A[at] * kLog2e;
   float h = first != nullptr ? first[i] : 0.0f;
-  for (int k = 0; k < S; ++k) {
-    const int64_t s = b * S + (reverse ? S - 1 - k : k);
-    const float own = H[s * slab + at];
-    H[s * slab + at] = h;
-    h = carried(a * sums[s * D + d], h, own);
+  constexpr int kAhead = 4;  // segments whose loads are under way together
+  for (int k = 0; k < S; k += kAhead) {
+    float own[kAhead], x[kAhead];
+    int64_t s[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (k + j < S) {
+        s[j] = b * S + (reverse ? S - 1 - k - j : k + j);
+        own[j] = H[s[j] * slab + at], x[j] = a * sums[s[j] * D + d];
+      }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (k + j < S) {
+        H[s[j] * slab + at] = h;
+        h = carried(x[j], h, own[j]);
+      }
   }
 }
 
