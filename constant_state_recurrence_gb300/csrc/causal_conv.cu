@@ -41,12 +41,6 @@ constexpr int kGroupsFwd = 4, kGroupsBwd = 4;  // groups of a ring
 constexpr int kLanes = 32, kRows = 8;  // backward block: channels x runs
 constexpr int kParts = kConvParts;
 
-__device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
-  if (lens == nullptr) return T;
-  const int64_t n = lens[b];
-  return n < 0 ? 0 : (n > T ? T : static_cast<int>(n));
-}
-
 // A sequence's inputs: token i in [-(K-1), n) of V channels.
 template <typename E, int V>
 struct Inputs {
@@ -213,7 +207,8 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
     for (int g = 0; g + 1 < kGroupsFwd; ++g) begin();
     Lanes<V> w[KM], win[KM - 1];
 #pragma unroll
-    for (int k = 0; k < KM - 1; ++k) win[k] = k >= pad ? in.at(t0 - (KM - 1) + k) : Lanes<V>::of(0.0f);
+    for (int k = 0; k < KM - 1; ++k)
+      win[k] = k >= pad ? in.at(t0 - (KM - 1) + k) : Lanes<V>::of(0.0f);
     load_weights<KM, V>(a.w, c, K, w);
     const Lanes<V> bias = load_bias<V>(a.bias, c);
     for (int now = 0; t < live; t += kStep, now = now + 1 == kGroupsFwd ? 0 : now + 1) {
@@ -437,20 +432,6 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t shared,
-                   cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = st;
-  cudaLaunchAttribute attr = pdl_attribute();
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 unsigned blocks_of(int64_t items) { return static_cast<unsigned>((items - 1) / kThreads + 1); }
 
 // Forward blocks that the current device holds at once; asked once a device (again after a
@@ -492,7 +473,8 @@ cudaError_t fwd(ConvArgs a, cudaStream_t st) {
   a.runs = (a.T + a.run - 1) / a.run;
   const int64_t rows = static_cast<int64_t>(a.B) * a.runs + (a.s_out != nullptr ? a.B : 0);
   if (rows == 0) return cudaSuccess;
-  return launch(conv_fwd_kernel<E, KM, V>, dim3(blocks_of(rows * vecs)), kThreads, shared, st, a);
+  return launch_pdl(conv_fwd_kernel<E, KM, V>, dim3(blocks_of(rows * vecs)), kThreads, shared, st,
+                    a);
 }
 
 // Blocks of runs (kRows of them a block at a time) and tokens of a run, backward: as many
@@ -533,19 +515,21 @@ cudaError_t bwd(ConvBwdArgs a, cudaStream_t st) {
                              static_cast<int>(shared));
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = launch(conv_bwd_kernel<E, KM, V>, dim3((a.D - 1) / (V * kLanes) + 1, n),
-                               kLanes * kRows, shared, st, a);
+  const dim3 grid((a.D - 1) / (V * kLanes) + 1, n);
+  const cudaError_t e =
+      launch_pdl(conv_bwd_kernel<E, KM, V>, grid, kLanes * kRows, shared, st, a);
   if (e != cudaSuccess || !sums) return e;
   const int64_t wide = static_cast<int64_t>(a.K + 1) * a.D;
-  return launch(conv_parts_kernel, dim3(static_cast<unsigned>((wide - 1) / 32 + 1)), 1024, 0, st,
-                static_cast<const float*>(a.parts), n, a.D, a.K, a.dw, a.dbias);
+  return launch_pdl(conv_parts_kernel, dim3(static_cast<unsigned>((wide - 1) / 32 + 1)), 1024, 0,
+                    st, static_cast<const float*>(a.parts), n, a.D, a.K, a.dw, a.dbias);
 }
 
 template <typename E, int KM, int V>
 cudaError_t step(const ConvArgs& a, cudaStream_t st) {
-  return launch(conv_step_kernel<E, KM, V>, dim3(blocks_of(static_cast<int64_t>(a.B) * (a.D / V))),
-                kThreads, 0, st, a.s_out, static_cast<const E*>(a.x), a.ldx, a.w, a.bias, a.act, a.B,
-                a.D, a.K, static_cast<E*>(a.y));
+  const int64_t items = static_cast<int64_t>(a.B) * (a.D / V);
+  return launch_pdl(conv_step_kernel<E, KM, V>, dim3(blocks_of(items)), kThreads, 0, st, a.s_out,
+                    static_cast<const E*>(a.x), a.ldx, a.w, a.bias, a.act, a.B, a.D, a.K,
+                    static_cast<E*>(a.y));
 }
 
 // Whether rows of D values with ldx values between those of x are words of V values at

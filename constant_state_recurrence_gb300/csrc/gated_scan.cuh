@@ -43,6 +43,7 @@
 #include <cudaTypedefs.h>
 
 #include "f32x2.cuh"
+#include "fast_math.cuh"
 #include "pdl.cuh"
 #include "per_device.h"
 #include "sanatan_internal.h"
@@ -97,19 +98,6 @@ __device__ __forceinline__ V4 shfl_xor(const V4& v, int mask) {
   return v4(f[0], f[1], f[2], f[3]);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-
 // The smaller of x and `most`; NaN stays NaN.
 __device__ __forceinline__ float at_most(float x, float most) {
   float r;
@@ -157,12 +145,6 @@ __device__ __forceinline__ void gate(const V4& g, V4& a, V4& keep) {
     keep = mul(e, a);
     a = sub(a, mul(a, fma(a, e, sub(a, one))));  // r - 1 is exact where it matters, r >= 1/2
   }
-}
-
-__device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
-  if (lens == nullptr) return T;
-  const int64_t n = lens[b];
-  return n < 0 ? 0 : (n > T ? T : static_cast<int>(n));
 }
 
 // Four values of a row in memory.

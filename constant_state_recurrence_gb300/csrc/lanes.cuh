@@ -2,27 +2,10 @@
 #pragma once
 
 #include "f32x2.cuh"
+#include "fast_math.cuh"
 
 namespace sanatan {
 namespace lanes {
-
-__device__ __forceinline__ float exp2_fast(float x) {  // within 2 ulp; below 2^-126: 0
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_fast(float x) {  // within 1 ulp; above 2^126: 0
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-constexpr float kLog2E = 1.4426950408889634f;
-
-// 1 / (1 + exp(-x)).
-__device__ __forceinline__ float sigmoid_fast(float x) {
-  return rcp_fast(1.0f + exp2_fast(x * -kLog2E));
-}
 
 template <int V>
 struct Lanes {
@@ -96,12 +79,12 @@ template <int V>
 __device__ __forceinline__ Lanes<V> sigmoid(const Lanes<V>& x) {
   const Lanes<V> one = Lanes<V>::of(1.0f);
   float f[V];
-  mul(x, Lanes<V>::of(-kLog2E)).get(f);
+  mul(x, Lanes<V>::of(-kLog2e)).get(f);
 #pragma unroll
-  for (int j = 0; j < V; ++j) f[j] = exp2_fast(f[j]);
+  for (int j = 0; j < V; ++j) f[j] = ex2(f[j]);
   fma(Lanes<V>::of(f), one, one).get(f);
 #pragma unroll
-  for (int j = 0; j < V; ++j) f[j] = rcp_fast(f[j]);
+  for (int j = 0; j < V; ++j) f[j] = rcp(f[j]);
   return Lanes<V>::of(f);
 }
 

@@ -13,11 +13,10 @@
 // value by value and 112 registers a thread 60.  Backward: a group of threads holds one load of
 // a row each, takes two rows at a time, so that the sums over a row cost one barrier for two, and
 // keeps its columns' dw and db in registers over all rows of the block; the rows of its next two
-// turns are copied to shared memory meanwhile.  47 us with the sums, 4.3 TB/s (0.63), 41 without;
-// (First without copies ahead: four rows
-// at a time and 12 warps an SM 57, two and 24 warps 62.)  Blocks leave partial sums, which a second kernel adds in a fixed order (no
-// atomics: the same call gives the same bits).  Rows longer than that are read again from L2
-// instead of held.
+// turns are copied to shared memory meanwhile.  47 us with the sums, 4.3 TB/s (0.63), 41 without.
+// (At first, without copies ahead: four rows at a time and 12 warps an SM 57, two and 24 warps
+// 62.)  Blocks leave partial sums, which a second kernel adds in a fixed order (no atomics: the
+// same call gives the same bits).  Rows longer than that are read again from L2 instead of held.
 #include <algorithm>
 #include <initializer_list>
 
@@ -503,20 +502,6 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const float* parts, in
   }
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, size_t shared,
-                   cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = st;
-  cudaLaunchAttribute attr = pdl_attribute();
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 constexpr int up32(int n) { return (n + 31) / 32 * 32; }
 
 // Shared memory of a backward block of `groups` groups of G threads.
@@ -542,8 +527,8 @@ cudaError_t launch_bwd(const NormBwdArgs& a, int n, int groups, int G, float* pa
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
     if (e != cudaSuccess) return e;
   }
-  return launch(kernel, dim3(n), G * groups, bwd_shared<E, ALIGNED, R>(groups, G), st, a, G,
-                parts);
+  return launch_pdl(kernel, dim3(n), G * groups, bwd_shared<E, ALIGNED, R>(groups, G), st, a, G,
+                    parts);
 }
 
 template <typename E, bool ALIGNED>
@@ -551,23 +536,24 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t st) {
   constexpr int V = kVec<E>;
   const unsigned rows = static_cast<unsigned>(a.rows);
   if (a.D <= 1024) {
+    constexpr int kRowThreads = 32 * kRowWarps;
     const dim3 grid((rows - 1) / kRowWarps + 1);
     // 8, 16, 24 or 32 values a lane
     switch ((a.D - 1) / 256) {
       case 0:
-        return launch(norm_fwd_kernel<E, 8 / V, ALIGNED, true>, grid, 32 * kRowWarps, 0, st, a);
+        return launch_pdl(norm_fwd_kernel<E, 8 / V, ALIGNED, true>, grid, kRowThreads, 0, st, a);
       case 1:
-        return launch(norm_fwd_kernel<E, 16 / V, ALIGNED, true>, grid, 32 * kRowWarps, 0, st, a);
+        return launch_pdl(norm_fwd_kernel<E, 16 / V, ALIGNED, true>, grid, kRowThreads, 0, st, a);
       case 2:
-        return launch(norm_fwd_kernel<E, 24 / V, ALIGNED, true>, grid, 32 * kRowWarps, 0, st, a);
+        return launch_pdl(norm_fwd_kernel<E, 24 / V, ALIGNED, true>, grid, kRowThreads, 0, st, a);
       default:
-        return launch(norm_fwd_kernel<E, 32 / V, ALIGNED, true>, grid, 32 * kRowWarps, 0, st, a);
+        return launch_pdl(norm_fwd_kernel<E, 32 / V, ALIGNED, true>, grid, kRowThreads, 0, st, a);
     }
   }
   if (a.D <= kMostThreads * V)
-    return launch(norm_fwd_kernel<E, 1, ALIGNED, false>, dim3(rows), up32((a.D - 1) / V + 1), 0,
-                  st, a);
-  return launch(norm_fwd_long_kernel<E>, dim3(rows), kLoopThreads, 0, st, a);
+    return launch_pdl(norm_fwd_kernel<E, 1, ALIGNED, false>, dim3(rows),
+                      up32((a.D - 1) / V + 1), 0, st, a);
+  return launch_pdl(norm_fwd_long_kernel<E>, dim3(rows), kLoopThreads, 0, st, a);
 }
 
 template <typename E, bool ALIGNED>
@@ -585,16 +571,16 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t st) {
     e = several ? launch_bwd<E, ALIGNED, kRows, kGroupThreads>(a, n, groups, G, parts, st)
                 : launch_bwd<E, ALIGNED, 1, kMostThreads>(a, n, groups, G, parts, st);
   } else {
-    e = launch(norm_bwd_long_kernel<E>, dim3(static_cast<unsigned>(a.rows)), kLoopThreads, 0, st,
-               a);
+    e = launch_pdl(norm_bwd_long_kernel<E>, dim3(static_cast<unsigned>(a.rows)), kLoopThreads, 0,
+                   st, a);
     if (e == cudaSuccess && columns) {
       n = static_cast<int>(std::min<int64_t>(32, (a.rows - 1) / 8 + 1));
-      e = launch(norm_columns_kernel<E>, dim3((a.D - 1) / 32 + 1, n), 256, 0, st, a, parts);
+      e = launch_pdl(norm_columns_kernel<E>, dim3((a.D - 1) / 32 + 1, n), 256, 0, st, a, parts);
     }
   }
   if (e != cudaSuccess || !columns) return e;
-  return launch(norm_parts_kernel, dim3(static_cast<unsigned>((2ll * a.D - 1) / 32 + 1)), 1024, 0,
-                st, static_cast<const float*>(parts), n, a.D, a.dweight, a.dbias);
+  return launch_pdl(norm_parts_kernel, dim3(static_cast<unsigned>((2ll * a.D - 1) / 32 + 1)), 1024,
+                    0, st, static_cast<const float*>(parts), n, a.D, a.dweight, a.dbias);
 }
 
 bool vectors(int D, int dtype, std::initializer_list<const void*> all) {

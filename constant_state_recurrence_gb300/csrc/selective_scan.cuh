@@ -41,7 +41,9 @@
 #include <algorithm>
 #include <initializer_list>
 
+#include "copy_async.cuh"
 #include "f32x2.cuh"
+#include "fast_math.cuh"
 #include "pdl.cuh"
 #include "sanatan_internal.h"
 #include "sanatan_math.cuh"
@@ -56,7 +58,7 @@ constexpr int kTile = kSelectiveMark;  // tokens of a tile, and between two mark
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStates = 4;             // of a lane
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSegmentLanes = 16;      // more lanes a channel: never cut into segments
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int L>
@@ -64,38 +66,21 @@ struct Geo {
   static constexpr int CW = 32 / L;          // channels of a warp
   static constexpr int CB = CW * kWarps;     // of a block
   static constexpr int NP = kStates * L;     // states, with those that fill up
-  // A warp's cells, (token, channel) pairs of a tile, W neighbouring channels at a time.
+  // A warp's cells, (token, channel) pairs of a tile: a lane has one token of W neighbouring
+  // channels; where that makes sixteen lanes, the others have none.
   static constexpr int W = CW < 4 ? CW : 4;
-  static constexpr int kCells = kTile * CW / W;            // of a warp
-  static constexpr int kItems = (kCells + 31) / 32;        // of a lane
+  static constexpr bool kAllLanes = CW / W == 2;
   static constexpr int kRowPitch = CW + 1;                 // of float4: no bank conflicts
-  // B and C of a tile, four states at a time.
-  static constexpr int kQuads = kTile * 2 * L;
-  static constexpr int kQuadItems = (kQuads + kThreads - 1) / kThreads;
+  // B and C of a tile, four states at a time: quads of a thread.
+  static constexpr int kQuadItems = kTile * 2 * L / kThreads;
+  static_assert(L >= 4 && kTile * CW / W <= 32 && kTile * 2 * L % kThreads == 0);
 };
 
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float sum2(uint64_t v) {
   float a, b;
   upk2(v, a, b);
   return a + b;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ float rcp(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // 2^x of a pair by the hardware, which is 0.1 to 0.8 steps of 2^-24 low on average (measured,
 // by binades of x).  A memory of n tokens multiplies that by n: see Decays.
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
@@ -153,8 +138,6 @@ struct Decays {
   }
 };
 
-__device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(x * -kLog2e)); }
-
 // log(1 + exp(x)) = max(x, 0) + log(1 + e) of a pair, e = exp(-|x|) <= 1, with log(1 + e) = 2
 // atanh(r), r = e / (2 + e) <= 1/3: the series r + r^3 / 3 + r^5 / 5 ... to r^13 is within
 // 2^-26 of its value, for all e alike, so that the small steps of delta have all their digits.
@@ -173,12 +156,6 @@ __device__ __forceinline__ uint64_t softplus_pair(uint64_t x) {
   p = ffma2(p, q, both(1.0f));
   // (a NaN goes through r; fmaxf alone would drop it)
   return ffma2(fmul2(r, both(2.0f)), p, pk2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
-}
-
-__device__ __forceinline__ int length_of(const int64_t* lens, int b, int T) {
-  if (lens == nullptr) return T;
-  const int64_t n = lens[b];
-  return n < 0 ? 0 : (n > T ? T : static_cast<int>(n));
 }
 
 // Halves M values a lane over lane bits LO .. HI (powers of two) while there are several, then
@@ -225,7 +202,7 @@ struct Meet {
 // Where a block works.
 template <int L>
 struct Place {
-  int b, seg, cb, tiles, k0, k1, n;  // k0 .. k1: the segment's tiles; n: tokens that are there
+  int b, seg, cb, tiles, k0, k1;  // k0 .. k1: the segment's tiles
   __device__ __forceinline__ Place(const SelectiveArgs& a) {
     cb = blockIdx.x % a.blocks;
     const unsigned rest = blockIdx.x / a.blocks;
@@ -234,7 +211,6 @@ struct Place {
     tiles = (a.T + kTile - 1) / kTile;
     k0 = seg * a.tiles_per_segment;
     k1 = min(k0 + a.tiles_per_segment, tiles);
-    n = 0;
   }
 };
 
@@ -270,25 +246,6 @@ struct StatePlace {
     }
   }
 };
-
-__device__ __forceinline__ void copy_async(void* to, const void* from, bool real, int bytes) {
-  const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-  const int n = real ? bytes : 0;  // (the rest is filled with zeros)
-  if (bytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n)
-                 : "memory");
-  else if (bytes == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(n)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(n)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
 
 // A tile of the tensors of a block, as they are in memory, on its way to shared memory while
 // tiles before are worked on: NT tensors of [B, T, D] (its channels), then B and C.  Where
@@ -371,11 +328,11 @@ struct Stage {
         const void* source = real ? from[i] : reinterpret_cast<const char*>(x[0]);
         if (kChunk == 16) {
           if (i + 1 < kSlots || kChunks % kThreads == 0 || bytes[i] != 0)
-            copy_async(buffer + to[i], source, real, 16);
+            copy_or_zeros(buffer + to[i], source, real, 16);
         } else if (bytes[i] == 16) {
-          copy_async(buffer + to[i], source, real, 16);
+          copy_or_zeros(buffer + to[i], source, real, 16);
         } else if (bytes[i] != 0) {
-          copy_async(buffer + to[i], source, real, kChunk);
+          copy_or_zeros(buffer + to[i], source, real, kChunk);
         }
         from[i] += step[i];
       }
@@ -451,8 +408,8 @@ __device__ __forceinline__ void Stage<E, L, ALIGNED, NT>::pairs_to_float(
     const char* buffer, int N, float (*pairs)[2][ORDERS][WIDE]) {
 #pragma unroll
   for (int i = 0; i < G::kQuadItems; ++i) {
-    const int k = threadIdx.x % kThreads + i * kThreads, q = k % L, which = k / L % 2, t = k / (2 * L);
-    if (G::kQuads % kThreads != 0 && k >= G::kQuads) break;
+    const int k = threadIdx.x % kThreads + i * kThreads;
+    const int q = k % L, which = k / L % 2, t = k / (2 * L);
     Vec<E, 4> v;
     float f[4];
     v.load(reinterpret_cast<const E*>(buffer + NT * kCell + which * kPair + t * kPairPitch) +
@@ -549,15 +506,7 @@ cudaError_t launch(void (*kernel)(Params...), int64_t blocks, int threads, size_
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared));
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = st;
-  cudaLaunchAttribute attr = pdl_attribute();
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), threads, shared, st, args...);
 }
 
 cudaError_t launch_carry(const SelectiveArgs& a, const float* first, bool reverse,

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) selective_bwd_state_kernel(Selective
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, l = lane / G::CW;
   const int mine = lane % G::CW;
   const int d0 = at.cb * G::CB, w0 = d0 + warp * G::CW, d = w0 + mine;
-  constexpr int kPer = G::CW / W, kStep = 32 / kPer;
+  constexpr int kPer = G::CW / W;
   const int cell_c = lane % kPer * W, cell_t = lane / kPer, cell_d = w0 + cell_c;
   const StatePlace st(d, l, a.D, a.N, a.vec);
   wait_for_previous();
@@ -81,10 +81,8 @@ __global__ void __launch_bounds__(kThreads) selective_bwd_state_kernel(Selective
     __syncthreads();
     if (k - 2 >= at.k0) tiles.begin(sm.raw[after], k - 2);
     if (k > at.k0) Tiles::pairs_to_float(sm.raw[next], a.N, sm.pairs[(k - 1) & 1]);
-#pragma unroll
-    for (int i = 0; i < G::kItems; ++i) {
-      const int t = cell_t + i * kStep;
-      if (G::kCells % 32 != 0 && t >= kTile) break;
+    if (G::kAllLanes || cell_t < kTile) {
+      const int t = cell_t;
       float delta[W], v[W], z[W];
       Tiles::get(sm.raw[now], 0, t, warp * G::CW + cell_c, delta);
       Tiles::get(sm.raw[now], 2, t, warp * G::CW + cell_c, v);
@@ -171,11 +169,9 @@ __device__ __forceinline__ void sum_channels(uint64_t b0, uint64_t b1, uint64_t 
     if constexpr (CW >= 4) {
       p += __shfl_xor_sync(0xffffffffu, q, Bits<L>::B);
       r += __shfl_xor_sync(0xffffffffu, s, Bits<L>::B);
-      if constexpr (CW >= 8) {
+      if constexpr (CW == 8) {
         const bool up = lane & 1;
         p = (up ? r : p) + __shfl_xor_sync(0xffffffffu, up ? p : r, 1);
-#pragma unroll
-        for (int bit = 8; bit < CW; bit *= 2) p += __shfl_xor_sync(0xffffffffu, p, bit);
       }
     }
     out[0] = p, out[1] = CW >= 4 ? r : q, out[2] = r, out[3] = s;
@@ -191,8 +187,8 @@ template <int L>
 __device__ __forceinline__ void put_channels(const float (&v)[8], int lane, int x, float* to) {
   constexpr int CW = Geo<L>::CW, NP = Geo<L>::NP;
   float* at = to + kStates * (lane / CW);
-  if constexpr (CW >= 8) {
-    if (lane % CW < 8) at[(lane & 1) * NP + x] = v[0];
+  if constexpr (CW == 8) {
+    at[(lane & 1) * NP + x] = v[0];
   } else if constexpr (CW == 4) {
     at[x] = v[0];
     at[NP + x] = v[1];
@@ -298,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
     for (int i = 0; i < G::kQuadItems; ++i) {
       const int q = tid + i * kThreads, s = q % L * 4, which = q / L % 2, tl = q / (2 * L);
       const int t = k * kTile + tl;
-      if ((G::kQuads % kThreads != 0 && q >= G::kQuads) || t >= n || s >= a.N) continue;
+      if (t >= n || s >= a.N) continue;
       float sum[4] = {};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -319,24 +315,22 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
     copy_wait<0>();
     __syncthreads();
     if (k + 1 < live) put_pairs(k + 1);
-    float u[G::kItems][W], raw[G::kItems][W], z[G::kItems][W], dy[G::kItems][W];
-#pragma unroll
-    for (int i = 0; i < G::kItems; ++i) {
-      const int t = cell_t + i * kStep;
-      if (G::kCells % 32 != 0 && t >= kTile) break;
+    float u[W], raw[W], z[W], dy[W];
+    if (G::kAllLanes || cell_t < kTile) {
+      const int t = cell_t;
       const int c = warp * G::CW + cell_c;
       float delta[W];
-      Tiles::get(sm.raw, 0, t, c, u[i]);
-      Tiles::get(sm.raw, 1, t, c, raw[i]);
-      if (gated) Tiles::get(sm.raw, 2, t, c, z[i]);
-      Tiles::get(sm.raw, 3, t, c, dy[i]);
+      Tiles::get(sm.raw, 0, t, c, u);
+      Tiles::get(sm.raw, 1, t, c, raw);
+      if (gated) Tiles::get(sm.raw, 2, t, c, z);
+      Tiles::get(sm.raw, 3, t, c, dy);
 #pragma unroll
-      for (int j = 0; j < W; ++j) delta[j] = raw[i][j];
+      for (int j = 0; j < W; ++j) delta[j] = raw[j];
       steps<W>(delta, bias, a.softplus, k * kTile + t < n);
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        const float du = delta[j] * u[i][j];
-        const float v = gated ? dy[i][j] * z[i][j] * sigmoid(z[i][j]) : dy[i][j];
+        const float du = delta[j] * u[j];
+        const float v = gated ? dy[j] * z[j] * sigmoid(z[j]) : dy[j];
         sm.cells[warp][t][cell_c + j] = make_float4(delta[j], du, v, v);
       }
     }
@@ -418,10 +412,8 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
     }
     decays.put_right(A0, A1, g0, g1, a.softplus, &sm.cells[warp][0][mine], G::kRowPitch);
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < G::kItems; ++i) {
-      const int tl = cell_t + i * kStep, t = k * kTile + tl;
-      if (G::kCells % 32 != 0 && tl >= kTile) break;
+    if (G::kAllLanes || cell_t < kTile) {
+      const int tl = cell_t, t = k * kTile + tl;
       float sB[W], sA[W], du[W], ddt[W], dz[W];
       Vec<float, W> r;
       r.load(&sm.sums[warp][0][tl][cell_c]);
@@ -438,14 +430,14 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
         const float4 cell = sm.cells[warp][tl][cell_c + j];
         const float delta = cell.x, v = cell.z;
         du[j] = fmaf(delta, sB[j], skip[j] * v);
-        ddt[j] = fmaf(u[i][j], sB[j], sA[j] * kLn2);
-        if (a.softplus) ddt[j] *= sigmoid(raw[i][j] + bias[j]);
+        ddt[j] = fmaf(u[j], sB[j], sA[j] * kLn2);
+        if (a.softplus) ddt[j] *= sigmoid(raw[j] + bias[j]);
         if (gated) {
-          const float y0 = fmaf(skip[j], u[i][j], dz[j]), sg = sigmoid(z[i][j]);
-          dz[j] = dy[i][j] * y0 * fmaf(z[i][j] * sg, 1.0f - sg, sg);
+          const float y0 = fmaf(skip[j], u[j], dz[j]), sg = sigmoid(z[j]);
+          dz[j] = dy[j] * y0 * fmaf(z[j] * sg, 1.0f - sg, sg);
         }
         if (!real) du[j] = ddt[j] = dz[j] = 0.0f;
-        dskip[j] = fmaf(v, u[i][j], dskip[j]);  // (zeros where there is no token)
+        dskip[j] = fmaf(v, u[j], dskip[j]);  // (zeros where there is no token)
         dbias[j] += ddt[j];
       }
       if (t < a.T) {
@@ -501,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, L == 4 ? 3 : 1)
 template <typename E, bool PIECE>
 __global__ void __launch_bounds__(256) selective_pairs_kernel(SelectiveBwdArgs args) {
   const SelectiveArgs& a = args.f;
-  const int64_t rows = PIECE ? static_cast<int64_t>(a.segments) * args.tiles_per_piece * kTile : a.T;
+  const int64_t rows =
+      PIECE ? static_cast<int64_t>(a.segments) * args.tiles_per_piece * kTile : a.T;
   const int64_t wide = 2 * static_cast<int64_t>(a.N), all = a.B * rows * wide;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   wait_for_previous();
@@ -550,12 +543,13 @@ cudaError_t bwd_of(const SelectiveBwdArgs& args, cudaStream_t st) {
   const SelectiveArgs& a = args.f;
   const int64_t blocks = static_cast<int64_t>(a.B) * a.blocks * a.segments;
   cudaError_t e;
-  if (a.segments > 1) {
-    e = launch(selective_bwd_state_kernel<E, L, ALIGNED>, blocks, kThreads,
-               sizeof(BwdStateShared<E, L, ALIGNED>), st, args);
-    if (e == cudaSuccess) e = launch_carry(a, args.dh_out, true, st);
-    if (e != cudaSuccess) return e;
-  }
+  if constexpr (L <= kSegmentLanes)
+    if (a.segments > 1) {
+      e = launch(selective_bwd_state_kernel<E, L, ALIGNED>, blocks, kThreads,
+                 sizeof(BwdStateShared<E, L, ALIGNED>), st, args);
+      if (e == cudaSuccess) e = launch_carry(a, args.dh_out, true, st);
+      if (e != cudaSuccess) return e;
+    }
   SelectiveBwdArgs now = args;
   const int64_t rows = args.pieces == 1 ? a.T
                                         : static_cast<int64_t>(a.segments) * args.tiles_per_piece *

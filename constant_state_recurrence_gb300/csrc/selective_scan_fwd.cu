@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kFwdThreads, L <= 8 ? 3 : 1)
       st.store(a.h_out + at.b * slab, h0, h1);
     return;
   }
-  // The lane's cells: W channels from cell_c of the warp's, tokens cell_t, cell_t + ...
+  // The lane's cells: W channels from cell_c of the warp's, token cell_t of a tile.
   constexpr int kPer = G::CW / W, kStep = 32 / kPer;
   const int cell_c = lane % kPer * W, cell_t = lane / kPer, cell_d = w0 + cell_c;
   E* Y = static_cast<E*>(a.y);
@@ -122,44 +122,37 @@ __global__ void __launch_bounds__(kFwdThreads, L <= 8 ? 3 : 1)
     tiles.init({a.u, a.dt, a.z, a.Bm, a.Cm}, {a.D, a.D, a.ldz, a.ldb, a.ldc}, a, row0, n, d0,
                at.k0, 1);
   struct Kept {
-    float u[G::kItems][W], z[G::kItems][W];
+    float u[W], z[W];
   };
   auto prepare = [&](int k, Kept& kept) {
     Tiles::pairs_to_float(sm.raw[k & 1], a.N, sm.pairs[k & 1]);
+    if (!G::kAllLanes && cell_t >= kTile) return;
+    float delta[W];
+    Tiles::get(sm.raw[k & 1], 0, cell_t, warp * G::CW + cell_c, kept.u);
+    Tiles::get(sm.raw[k & 1], 1, cell_t, warp * G::CW + cell_c, delta);
+    if (gated) Tiles::get(sm.raw[k & 1], 2, cell_t, warp * G::CW + cell_c, kept.z);
+    steps<W>(delta, bias, a.softplus, k * kTile + cell_t < n);
 #pragma unroll
-    for (int i = 0; i < G::kItems; ++i) {
-      const int t = cell_t + i * kStep;
-      if (G::kCells % 32 != 0 && t >= kTile) break;
-      float delta[W];
-      Tiles::get(sm.raw[k & 1], 0, t, warp * G::CW + cell_c, kept.u[i]);
-      Tiles::get(sm.raw[k & 1], 1, t, warp * G::CW + cell_c, delta);
-      if (gated) Tiles::get(sm.raw[k & 1], 2, t, warp * G::CW + cell_c, kept.z[i]);
-      steps<W>(delta, bias, a.softplus, k * kTile + t < n);
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        if (STATE) sum[j] += delta[j];
-        const float du = delta[j] * kept.u[i][j];
-        sm.cells[k & 1][warp][t][cell_c + j] = make_float4(delta[j], delta[j], du, du);
-      }
+    for (int j = 0; j < W; ++j) {
+      if (STATE) sum[j] += delta[j];
+      const float du = delta[j] * kept.u[j];
+      sm.cells[k & 1][warp][cell_t][cell_c + j] = make_float4(delta[j], delta[j], du, du);
     }
   };
   auto finish = [&](int k, const Kept& kept) {
+    if (!G::kAllLanes && cell_t >= kTile) return;
+    const int t = k * kTile + cell_t;
+    float y[W];
+    Vec<float, W> v;
+    v.load(&sm.ys[k & 1][warp][cell_t][cell_c]);
+    v.get(y);
 #pragma unroll
-    for (int i = 0; i < G::kItems; ++i) {
-      const int tl = cell_t + i * kStep, t = k * kTile + tl;
-      if (G::kCells % 32 != 0 && tl >= kTile) break;
-      float y[W];
-      Vec<float, W> v;
-      v.load(&sm.ys[k & 1][warp][tl][cell_c]);
-      v.get(y);
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        y[j] = fmaf(skip[j], kept.u[i][j], y[j]);
-        if (gated) y[j] *= kept.z[i][j] * sigmoid(kept.z[i][j]);
-        if (t >= n) y[j] = 0.0f;
-      }
-      if (t < a.T) store_cells<E, W, ALIGNED>(Y + (row0 + t) * a.D, cell_d, a.D, y);
+    for (int j = 0; j < W; ++j) {
+      y[j] = fmaf(skip[j], kept.u[j], y[j]);
+      if (gated) y[j] *= kept.z[j] * sigmoid(kept.z[j]);
+      if (t >= n) y[j] = 0.0f;
     }
+    if (t < a.T) store_cells<E, W, ALIGNED>(Y + (row0 + t) * a.D, cell_d, a.D, y);
   };
   Kept before, now, next;  // of tiles k - 1, k, k + 1
   if (at.k0 < live) {
@@ -277,13 +270,14 @@ __global__ void __launch_bounds__(kThreads) selective_step_kernel(SelectiveArgs 
 template <typename E, int L, bool ALIGNED>
 cudaError_t fwd_of(const SelectiveArgs& a, cudaStream_t st) {
   const int64_t blocks = static_cast<int64_t>(a.B) * a.blocks * a.segments;
-  if (a.segments > 1) {
-    cudaError_t e =
-        launch(selective_fwd_kernel<E, L, ALIGNED, true>, blocks, kFwdThreads,
-               sizeof(FwdShared<E, L, ALIGNED, true>), st, a);
-    if (e == cudaSuccess) e = launch_carry(a, a.h0, false, st);
-    if (e != cudaSuccess) return e;
-  }
+  if constexpr (L <= kSegmentLanes)
+    if (a.segments > 1) {
+      cudaError_t e =
+          launch(selective_fwd_kernel<E, L, ALIGNED, true>, blocks, kFwdThreads,
+                 sizeof(FwdShared<E, L, ALIGNED, true>), st, a);
+      if (e == cudaSuccess) e = launch_carry(a, a.h0, false, st);
+      if (e != cudaSuccess) return e;
+    }
   return launch(selective_fwd_kernel<E, L, ALIGNED, false>, blocks, kFwdThreads,
                 sizeof(FwdShared<E, L, ALIGNED, false>), st, a);
 }
@@ -323,7 +317,7 @@ int selective_segments(int B, int T, int D, int N, int* tiles_per_segment) {
   const int tiles = std::max(1, (T - 1) / kTile + 1);
   const int64_t blocks = static_cast<int64_t>(B) * selective_blocks(D, N);
   int64_t S = 1;
-  if (blocks < 2 * kSms && selective_lanes(N) < 32)
+  if (blocks < 2 * kSms && selective_lanes(N) <= kSegmentLanes)
     S = std::min<int64_t>((6 * kSms - 1) / blocks + 1, tiles / 4);
   S = std::max<int64_t>(S, 1);
   *tiles_per_segment = static_cast<int>((tiles - 1) / S + 1);
