@@ -33,8 +33,8 @@
 // exponential and eight other operations forward, an exponential and a half and about
 // twenty-five backward, packed two an instruction, beside what a token and channel costs
 // once (a softplus and the gate).  GB300, N 16, bf16, gated: B 8 T 4096 D 1536
-// forward 439 us (453 with marks; 0.8 G states, 1.8 T a second; the bytes alone would take 61),
-// backward 1422 (the bytes 106); B 1 T 32768 D 1536 617 and 1484 (segments walk twice).  First
+// forward 425 us (440 with marks; 0.8 G states, 1.9 T a second; the bytes alone would take 61),
+// backward 1390 (the bytes 106); B 1 T 32768 D 1536 597 and 1452 (segments walk twice).  First
 // version (loads by the element, decays by the series, 2 barriers a tile): 1540 and 4000.
 #pragma once
 
@@ -140,7 +140,8 @@ struct Decays {
 
 // log(1 + exp(x)) = max(x, 0) + log(1 + e) of a pair, e = exp(-|x|) <= 1, with log(1 + e) = 2
 // atanh(r), r = e / (2 + e) <= 1/3: the series r + r^3 / 3 + r^5 / 5 ... to r^13 is within
-// 2^-26 of its value, for all e alike, so that the small steps of delta have all their digits.
+// 2^-26 of its value, for all e alike.  A small step has e's own error, the rounding of
+// |x| log2(e): |x| 2^-24 of itself, 4e-7 for a delta of 0.001.
 __device__ __forceinline__ uint64_t softplus_pair(uint64_t x) {
   float x0, x1, e0, e1;
   upk2(x, x0, x1);
@@ -415,7 +416,7 @@ __device__ __forceinline__ void Stage<E, L, ALIGNED, NT>::pairs_to_float(
     v.load(reinterpret_cast<const E*>(buffer + NT * kCell + which * kPair + t * kPairPitch) +
            4 * q);
     v.get(f);
-    if (4 * q + 4 > N)  // (what fills up was never written)
+    if (4 * q + 4 > N)  // (what fills up a row of B or C need not be zero)
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[j] = 4 * q + j < N ? f[j] : 0.0f;
 #pragma unroll

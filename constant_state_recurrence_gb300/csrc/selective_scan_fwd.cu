@@ -308,8 +308,8 @@ int selective_lanes(int N) {
 int selective_blocks(int D, int N) { return (D - 1) / (kThreads / selective_lanes(N)) + 1; }
 
 // Segments of a sequence, and their tiles.  One, where whole sequences make two blocks or more
-// an SM (a split walks the tokens twice; training shape, 384 blocks: forward 439 us, backward
-// 1422 and, when both walked slower, 1466 whole and 1572 in eight segments); else about six
+// an SM (a split walks the tokens twice; training shape, 384 blocks: forward 425 us, backward
+// 1390 and, when both walked slower, 1466 whole and 1572 in eight segments); else about six
 // blocks an SM (one prompt of 32768 tokens, 48 blocks: 10, 13, 19 and 38 segments forward 852, 747,
 // 616 and 622 us, backward 2330, 1847, 1484 and 1471), of four tiles or more.  More than 64
 // states: always one.
