@@ -5,9 +5,9 @@
 // gradients.  Bound: instructions, 129 a token and warp (a quarter of them the sums over
 // channels and states), half of the issue slots used by the ten warps that an SM has at the
 // training shape.  With all decays of a tile in registers and all states in shared memory it was
-// the latter's wavefronts, 42 a token and warp: 1466 us instead of 1422 then (1390 now), one prompt of
-// 32768 tokens 1840 instead of 1567 (1452 now).  Cells as pairs twice over, without the moves that
-// make pairs of them: 1563.
+// the latter's wavefronts, 42 a token and warp: 1466 us instead of 1422 then (1390 now), one
+// prompt of 32768 tokens 1840 instead of 1567 (1452 now).  Cells as pairs twice over, without the
+// moves that make pairs of them: 1563.
 //
 // dB and dC are sums over channels: each block of 128 / L channels leaves its part of them for
 // every token, in all L / 4 times the marks.  Beyond four lanes a channel and 512 MB the parts

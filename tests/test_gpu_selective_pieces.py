@@ -60,13 +60,14 @@ def test_segments_in_pieces(dtype, D):
     assert all(torch.equal(g[k], again[k]) for k in g)
 
 
-@pytest.mark.parametrize("lens", [None, [2100, 0, 700, 1]])
-def test_whole_sequences_in_pieces(lens):
+@pytest.mark.parametrize("lens,N,dtype", [(None, 128, F32), ([2100, 0, 700, 1], 128, F32),
+                                          ([2100, 2099, 701, 16], 127, BF16)])
+def test_whole_sequences_in_pieces(lens, N, dtype):
     """Four sequences in three pieces are four of one, to the bit; sums over sequences are
     formed in their order."""
-    b, T, D, N = 4, 2100, 512, 128
+    b, T, D = 4, 2100, 512
     assert parts(b, T, D, N) > 2 * MOST > MOST > parts(1, T, D, N)
-    x, dy, dh = make(b, T, D, N, F32, 11)
+    x, dy, dh = make(b, T, D, N, dtype, 11)
     x = {k: t.to(dev()) for k, t in x.items()}
     dy, dh = dy.to(dev()), dh.to(dev())
     ln = None if lens is None else torch.tensor(lens, device=dev())
